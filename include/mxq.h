@@ -78,12 +78,17 @@ typedef enum { MXQ_BF16 = 0, MXQ_FP32 = 1 } mxq_dtype;
 /* MX element formats (mx_fake_quantize). */
 typedef enum { MXQ_FMT_MXFP8 = 0, MXQ_FMT_MXFP4 = 1 } mxq_mx_format;
 
+/* Scores of moe_route. */
+typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score;
+
 #define MXQ_ABI_VERSION 2
 #define MXQ_MXFP8_GROUP 32
 #define MXQ_NVFP4_BLOCK 16
 #define MXQ_GROUPED_MAX_EXPERTS 1024
 #define MXQ_NVFP4_GLOBAL_GIVEN 1u
 #define MXQ_NVFP4_MAX_SLICES 1024
+#define MXQ_ROUTE_MAX_TOP_K 32
+#define MXQ_ROUTE_MAX_GROUPS 32
 
 /* Version of this ABI (MXQ_ABI_VERSION of the built library). */
 int mxq_abi_version(void);
@@ -314,6 +319,138 @@ mxq_status mx_fake_quantize(int fmt, const void* x, int dt, int64_t M, int64_t N
 mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* qb,
                       const uint8_t* sb_swz, int64_t M, int64_t N, int64_t K, void* d,
                       int out_dt, int32_t* error_flag, mxq_stream_t stream);
+
+/* ------------------------------------- products with weights in 4 bits */
+
+/* y = x W^T for the weights that mxfp4_quantize and nvfp4_quantize leave,
+ * with x in bf16 or fp32: the products of decoding, where a few rows meet a
+ * weight that is read once.
+ *   y[m, n] = sum_k x[m, k] decode(packed[n, k]) 2^(scale[n, k/32] - 127)
+ *   y[m, n] = global_scale sum_k x[m, k] decode(packed[n, k])
+ *                                decode_e4m3(block_scale[n, k/16])
+ * The products of x and the codes are exact for every x (an fp32 x keeps all
+ * its bits), they are summed in fp32 (groups of 32 by the tensor cores), and
+ * y is rounded once. The order of the sum is fixed: repeated calls give
+ * identical bytes. Infinities and NaNs of x, NaN block scales and the E8M0
+ * byte 255 act as in that formula (inf * 0 is NaN).
+ *  x       [M, K] of dt, row stride ld_x elements. Any M: rows are taken 8,
+ *          16 or 32 at a time (a third of that for fp32), and each such tile
+ *          reads the weight again.
+ *  packed  [N, K/2], scale [N, K/32] (block_scale [N, K/16]): compact, as the
+ *          quantizers write them. K % 32 == 0 (MXFP4), K % 16 == 0 (NVFP4).
+ *          Scale rows that start on 4-byte boundaries (K a multiple of 128 /
+ *          64) are copied asynchronously; others are correct and slower.
+ *  global_scale  device fp32 scalar, 4-byte aligned.
+ *  y       [M, N] of out_dt, contiguous, 16-byte aligned; may not overlap an
+ *          input. K == 0 writes zeros.
+ * M, N, K <= 2^31 - 1. (The pages quantize the weights, "V4 mxfp4 #1372" and
+ * "Add FP8, NVFP4, and QARL training and export"; the product with them is
+ * this library's.) One launch. */
+mxq_status mxfp4_matvec(const void* x, int dt, int64_t M, int64_t K, int64_t ld_x,
+                        const uint8_t* packed, const uint8_t* scale, int64_t N, void* y,
+                        int out_dt, mxq_stream_t stream);
+mxq_status nvfp4_matvec(const void* x, int dt, int64_t M, int64_t K, int64_t ld_x,
+                        const uint8_t* packed, const uint8_t* block_scale,
+                        const float* global_scale, int64_t N, void* y, int out_dt,
+                        mxq_stream_t stream);
+
+/* The same for a stack of E experts' weights [E, N, K]: row r of the product
+ * belongs to the expert e with row_offsets[e] <= r < row_offsets[e + 1] and is
+ * multiplied by its weight. An expert without rows is not read.
+ *  row_offsets  DEVICE int64 [E + 1], 8-byte aligned, non-decreasing, in
+ *          [0, R] (moe_dispatch writes them). Each is clamped to [0, R]. Rows
+ *          before row_offsets[0] and from row_offsets[E] on are left as they
+ *          were.
+ *  R       rows of the product.
+ *  order   NULL: x has R rows and row r is x's row r (top_k is 1 then). Or
+ *          device int32 [R]: row r is x's row order[r] / top_k, the token of
+ *          the pair that moe_dispatch put there; entries that lead outside
+ *          x's x_rows rows count as rows of zeros.
+ *  swiglu  0: y is [R, N]. 1: the first N/2 rows of a weight are the gate and
+ *          the others the up projection (N even), and y [R, N/2] is
+ *          gate / (1 + exp(-gate)) * up, from the fp32 sums.
+ *  packed [E, N, K/2], scale [E, N, K/32] (block_scale [E, N, K/16]), compact.
+ *  global_scales      device fp32 [E], or [E, 2] (rows [0, N/2) and [N/2, N);
+ *          N even) with scales_per_expert 1 or 2.
+ * 1 <= E <= MXQ_GROUPED_MAX_EXPERTS; otherwise as above. One launch. */
+mxq_status mxfp4_matvec_grouped(const void* x, int dt, int64_t x_rows, int64_t K, int64_t ld_x,
+                                const uint8_t* packed, const uint8_t* scale, int32_t E,
+                                int64_t N, const int64_t* row_offsets, int64_t R,
+                                const int32_t* order, int32_t top_k, int32_t swiglu, void* y,
+                                int out_dt, mxq_stream_t stream);
+mxq_status nvfp4_matvec_grouped(const void* x, int dt, int64_t x_rows, int64_t K, int64_t ld_x,
+                                const uint8_t* packed, const uint8_t* block_scale,
+                                const float* global_scales, int32_t scales_per_expert,
+                                int32_t E, int64_t N, const int64_t* row_offsets, int64_t R,
+                                const int32_t* order, int32_t top_k, int32_t swiglu, void* y,
+                                int out_dt, mxq_stream_t stream);
+
+/* The last step of the experts' products: each token's rows added up with its
+ * router weights, y[t, n] = sum_j weights[t, j] rows[positions[t, j], n] in
+ * fp32, in the order of j.
+ *  rows       [R, N] fp32, contiguous, 16-byte aligned.
+ *  positions  device int32 [T, top_k] (moe_dispatch's); one outside [0, R)
+ *             adds nothing, whatever its weight.
+ *  weights    device fp32 [T, top_k].
+ *  y          [T, N] of out_dt, 16-byte aligned. One launch. */
+mxq_status moe_combine(const float* rows, int64_t R, int64_t N, const int32_t* positions,
+                       const float* weights, int64_t T, int32_t top_k, void* y, int out_dt,
+                       mxq_stream_t stream);
+
+/* ----------------------------------------------------- routing to experts */
+
+/* The router of a mixture of experts: the experts of each token and their
+ * weights ("V4 mxfp4 #1372", description: MoE expert weights; the pages have
+ * no router of their own). For each row of logits:
+ *   p_e     softmax of the row, or 1 / (1 + exp(-logit)), by `scoring`;
+ *   choice  the top_k experts by p_e + bias[e], best first, ties to the lowest
+ *           index. With groups > 1 the experts are cut into that many
+ *           consecutive groups of equal size, a group's score is the sum of
+ *           its two largest p + bias (its only one where a group has one
+ *           expert), and the choice is among the experts of the top_groups
+ *           best groups (ties to the lowest group);
+ *   weight  scale * p, or with renormalize scale * p / (sum of the chosen p).
+ * The bias counts for the choice only. The choice is that of the exact p +
+ * bias, not of their fp32 roundings (differences that fp32 cannot tell are
+ * taken again in fp64). NaN logits count as -inf, NaN sums with a bias as the
+ * lowest; +inf logits share the softmax equally. Where the chosen p are all
+ * zero (a row of -inf), the weights are zero.
+ *  logits   [T, E] bf16 or fp32 (dt), row stride ld elements (ld >= E), no
+ *           alignment beyond the element's. 1 <= E <= 1024.
+ *  bias     NULL, or device fp32 [E].
+ *  groups   1 .. MXQ_ROUTE_MAX_GROUPS, dividing E; 1 <= top_groups <= groups.
+ *  top_k    1 .. MXQ_ROUTE_MAX_TOP_K, at most E / groups * top_groups.
+ *  weights  [T, top_k] fp32; experts [T, top_k] int32.
+ * One launch. */
+mxq_status moe_route(const void* logits, int dt, int64_t T, int32_t E, int64_t ld, int scoring,
+                     const float* bias, int32_t groups, int32_t top_groups, int32_t top_k,
+                     int32_t renormalize, float scale, float* weights, int32_t* experts,
+                     mxq_stream_t stream);
+
+/* Gradient of moe_route's weights with respect to the logits, for the experts
+ * that it chose (the choice, the bias and the groups have none):
+ * grad_logits [T, E] of dt, contiguous, from grad_weights [T, top_k] fp32.
+ * Entries of `experts` outside [0, E) are left out, as if the token had fewer
+ * choices; an expert named twice gets the sum. The fp32 gradient is rounded
+ * once. One launch. */
+mxq_status moe_route_backward(const float* grad_weights, const void* logits, int dt, int64_t T,
+                              int32_t E, int64_t ld, const int32_t* experts, int scoring,
+                              int32_t top_k, int32_t renormalize, float scale, void* grad_logits,
+                              mxq_stream_t stream);
+
+/* The (token, choice) pairs in the order of their experts, stable: what the
+ * grouped entry points take. Pair p = t * top_k + j has expert experts[p].
+ *  experts      device int32 [P], P <= 2^31 - 1; a pair with an expert outside
+ *               [0, E) (of another rank, or of a padding token) is dropped.
+ *  row_offsets  device int64 [E + 1], 8-byte aligned: expert e's pairs take
+ *               the places row_offsets[e] .. row_offsets[e + 1] - 1; dropped
+ *               pairs the places from row_offsets[E] on.
+ *  order        device int32 [P]: the pair at each place.
+ *  positions    device int32 [P]: the place of each pair, -1 if dropped.
+ * P == 0 writes row_offsets (zeros) only. 1 <= E <= MXQ_GROUPED_MAX_EXPERTS.
+ * One launch of one cluster. */
+mxq_status moe_dispatch(const int32_t* experts, int64_t P, int32_t E, int64_t* row_offsets,
+                        int32_t* order, int32_t* positions, mxq_stream_t stream);
 
 /* Self-check of the bounded barrier wait that lets mxfp8_gemm give up
  * instead of hanging (the wait behind error_flag), run on the device in one

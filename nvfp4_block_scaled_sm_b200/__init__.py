@@ -26,6 +26,8 @@ __all__ = [
     "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped", "mxfp8_quantize_columnwise",
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_quantize_grouped", "mx_fake_quantize",
     "mxfp8_gemm",
+    "mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
+    "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
     "nvfp4_amax", "nvfp4_quantize", "nvfp4_dequantize",
     "nvfp4_amax_sliced", "nvfp4_quantize_sliced", "nvfp4_quantize_experts",
     "swizzled_scale_bytes", "nvfp4_workspace_bytes", "set_output_allocator", "swizzle_scales",
@@ -87,7 +89,20 @@ def _load() -> ctypes.CDLL:
     L.nvfp4_quantize_sliced.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp, u32, vp,
                                         sz, vp]
     L.nvfp4_amax_sliced.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, sz, vp]
-    for f in ("mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped",
+    f32 = ctypes.c_float
+    L.mxfp4_matvec.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, vp, i32, vp]
+    L.nvfp4_matvec.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, i32, vp]
+    L.mxfp4_matvec_grouped.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, i64, vp, i64, vp, i32,
+                                       i32, vp, i32, vp]
+    L.nvfp4_matvec_grouped.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, i32, i32, i64, vp, i64,
+                                       vp, i32, i32, vp, i32, vp]
+    L.moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i32, vp, i32, vp]
+    L.moe_route.argtypes = [vp, i32, i64, i32, i64, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp]
+    L.moe_route_backward.argtypes = [vp, vp, i32, i64, i32, i64, vp, i32, i32, i32, f32, vp, vp]
+    L.moe_dispatch.argtypes = [vp, i64, i32, vp, vp, vp, vp]
+    for f in ("mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
+              "moe_combine", "moe_route", "moe_route_backward", "moe_dispatch",
+              "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped",
               "mxfp8_quantize_grouped_swizzled", "mxfp8_quantize_grouped_ptrs",
               "mxfp8_quantize_columnwise", "mxfp4_quantize", "mxfp4_dequantize",
               "mxfp4_quantize_grouped", "mxfp4_quantize_grouped_swizzled",
@@ -453,6 +468,303 @@ def mxfp8_gemm(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Tensor,
     return d
 
 
+# ------------------------------------------- products with 4-bit weights
+
+def _launch(fn: str, dev: torch.device, *args):
+    """Calls ``fn`` with the stream of ``dev`` that is current, on that device
+    (tensors may live on another device than the current one)."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        status = getattr(lib, fn)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, fn)(*args, stream)
+    if status:
+        _check(fn, status)
+
+
+def _same_device(x: torch.Tensor, *ts: torch.Tensor):
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must live on a CUDA device (no CPU path exists)")
+    for t in ts:
+        if t.device != dev:
+            raise ValueError("tensors must live on one CUDA device")
+
+
+def _weight_args(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, block: int, dims: int):
+    """(N, K) of a 4-bit weight [N, K/2] (or a stack [E, N, K/2]) that
+    multiplies rows x [..., K]."""
+    if packed.dtype != torch.uint8 or scale.dtype != torch.uint8:
+        raise TypeError("codes and scales must be uint8")
+    if not (packed.is_contiguous() and scale.is_contiguous()):
+        raise ValueError("codes and scales must be contiguous")
+    if packed.dim() != dims or scale.dim() != dims:
+        raise ValueError(f"expected {dims}-D codes and scales")
+    N, K = packed.shape[-2], packed.shape[-1] * 2
+    if K % block or scale.shape != (*packed.shape[:-1], K // block):
+        raise ValueError("scale does not match the codes")
+    if x.dim() == 0 or x.shape[-1] != K:
+        raise ValueError(f"expected rows of {K} elements")
+    return N, K
+
+
+def _matvec(fn: str, x, packed, scale, global_scale, dtype, block: int) -> torch.Tensor:
+    _same_device(x, packed, scale)
+    N, K = _weight_args(x, packed, scale, block, 2)
+    dt, out_dt = _dtype_code(x.dtype), _dtype_code(dtype)
+    M, _, ld = _rows_view(x)
+    g = ()
+    if global_scale is not None:
+        if global_scale.dtype != torch.float32 or global_scale.numel() != 1:
+            raise TypeError("global_scale must be a single fp32 value")
+        global_scale = global_scale.to(x.device)
+        g = (global_scale.data_ptr(),)
+    y = _empty((*x.shape[:-1], N), dtype, x.device)
+    _launch(fn, x.device, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(), *g, N,
+            y.data_ptr(), out_dt)
+    return y
+
+
+def mxfp4_matvec(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
+                 dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y = x W^T for a weight W in MXFP4: rows ``x`` [..., K] in bf16 or fp32,
+    ``packed`` [N, K/2] and ``scale`` [N, K/32] as :func:`mxfp4_quantize`
+    returns them. Returns y [..., N] as ``dtype``: exact products of x and the
+    decoded weight, summed in fp32, rounded once. Made for the few rows of
+    decoding; more rows are right and read the weight again every 8 to 32."""
+    return _matvec("mxfp4_matvec", x, packed, scale, None, dtype, 32)
+
+
+def nvfp4_matvec(x: torch.Tensor, packed: torch.Tensor, block_scale: torch.Tensor,
+                 global_scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y = x W^T for a weight in NVFP4 (``packed`` [N, K/2], ``block_scale``
+    [N, K/16], a single fp32 ``global_scale``: :func:`nvfp4_quantize`'s
+    results), otherwise as :func:`mxfp4_matvec`."""
+    return _matvec("nvfp4_matvec", x, packed, block_scale, global_scale, dtype, 16)
+
+
+def _device_offsets(dev, row_offsets, E: int, R: int) -> torch.Tensor:
+    """row_offsets [E + 1] as a device int64 tensor; a list or a CPU tensor is
+    checked, offsets on the device are clamped by the kernels."""
+    if isinstance(row_offsets, torch.Tensor) and row_offsets.is_cuda:
+        if row_offsets.dtype != torch.int64 or row_offsets.numel() != E + 1:
+            raise TypeError("row_offsets must be int64 with E + 1 entries")
+        if row_offsets.device != dev:
+            raise ValueError("tensors must live on one CUDA device")
+        return row_offsets.contiguous()
+    host = [int(v) for v in (row_offsets.tolist() if isinstance(row_offsets, torch.Tensor)
+                             else row_offsets)]
+    if len(host) != E + 1 or host[0] < 0 or host[-1] > R or \
+            any(b < a for a, b in zip(host[:-1], host[1:])):
+        raise ValueError(f"row_offsets must rise within the {R} rows in {E + 1} entries")
+    return torch.tensor(host, dtype=torch.int64).to(dev)
+
+
+def _int32(t: torch.Tensor, dev, what: str) -> torch.Tensor:
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32")
+    if t.device != dev:
+        raise ValueError("tensors must live on one CUDA device")
+    return t.contiguous()
+
+
+def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k, swiglu, combine,
+                    dtype, block: int) -> torch.Tensor:
+    _same_device(x, packed, scale)
+    dev = x.device
+    N, K = _weight_args(x, packed, scale, block, 3)
+    E = packed.shape[0]
+    if x.dim() != 2:
+        raise ValueError("expected rows [R, K]")
+    dt, out_dt = _dtype_code(x.dtype), _dtype_code(dtype)
+    x_rows, _, ld = _rows_view(x)
+    if order is not None:
+        order = _int32(order, dev, "order")
+        R = order.numel()
+        top_k = int(top_k)
+        if top_k < 1:
+            raise ValueError("top_k must be at least 1")
+    else:
+        if top_k != 1:
+            raise ValueError("top_k goes with order")
+        R = x_rows
+    if (swiglu or (scales is not None and scales.numel() == 2 * E)) and N % 2:
+        raise ValueError("halves of an expert need an even number of rows")
+    offsets = _device_offsets(dev, row_offsets, E, R)
+    g = ()
+    if scales is not None:
+        if scales.dtype != torch.float32 or scales.numel() not in (E, 2 * E):
+            raise TypeError("global_scales must be fp32 with one or two values per expert")
+        scales = scales.to(dev).contiguous()
+        g = (scales.data_ptr(), scales.numel() // E)
+    outs = N // 2 if swiglu else N
+    if combine is not None:
+        positions, weights = combine
+        positions = _int32(positions, dev, "positions")
+        if positions.dim() == 0 or weights.shape != positions.shape:
+            raise ValueError("positions and weights must be [..., top_k]")
+    y = _empty((R, outs), torch.float32 if combine is not None else dtype, dev)
+    _launch(fn, dev, x.data_ptr(), dt, x_rows, K, ld, packed.data_ptr(), scale.data_ptr(), *g, E, N,
+            offsets.data_ptr(), R, None if order is None else order.data_ptr(), top_k,
+            1 if swiglu else 0, y.data_ptr(), FP32 if combine is not None else out_dt)
+    return y if combine is None else moe_combine(y, positions, weights, dtype)
+
+
+def mxfp4_matvec_grouped(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, row_offsets, *,
+                         order: torch.Tensor | None = None, top_k: int = 1, swiglu: bool = False,
+                         combine=None, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The experts' products for rows sorted by expert: row r of the result is
+    its row of ``x`` times the weight of the expert e with
+    ``row_offsets[e] <= r < row_offsets[e + 1]``. ``packed`` [E, N, K/2] and
+    ``scale`` [E, N, K/32] are a stack of MXFP4 weights; experts without rows
+    are not read.
+
+    ``row_offsets``: E + 1 offsets, int64 on the device (as
+    :func:`moe_dispatch` returns them; clamped to the rows), or a list.
+    ``order`` (int32 [R], :func:`moe_dispatch`'s) with ``top_k`` gathers: row r
+    reads ``x[order[r] // top_k]``; without it ``x`` has the R rows themselves.
+    ``swiglu=True``: the first N/2 rows of each weight are the gate, the others
+    the up projection, and the result [R, N/2] is silu(gate) * up.
+    ``combine=(positions, weights)`` (int32 and fp32 [..., top_k]) adds the
+    rows up into the tokens (:func:`moe_combine`), from fp32 rows: the result
+    is [..., N].
+
+    Returns [R, N] (see above) as ``dtype``. Rows that belong to no expert
+    (dropped pairs) are not written: what they hold is undefined."""
+    return _matvec_grouped("mxfp4_matvec_grouped", x, packed, scale, None, row_offsets, order, top_k,
+                           swiglu, combine, dtype, 32)
+
+
+def nvfp4_matvec_grouped(x: torch.Tensor, packed: torch.Tensor, block_scale: torch.Tensor,
+                         global_scales: torch.Tensor, row_offsets, *,
+                         order: torch.Tensor | None = None, top_k: int = 1, swiglu: bool = False,
+                         combine=None, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """:func:`mxfp4_matvec_grouped` for a stack of NVFP4 weights as
+    :func:`nvfp4_quantize_experts` returns it: ``packed`` [E, N, K/2],
+    ``block_scale`` [E, N, K/16] and fp32 ``global_scales`` [E], or [E, 2] with
+    one scale per half of an expert's rows."""
+    return _matvec_grouped("nvfp4_matvec_grouped", x, packed, block_scale, global_scales, row_offsets,
+                           order, top_k, swiglu, combine, dtype, 16)
+
+
+def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tensor,
+                dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """Each token's rows added up with its router weights, in fp32:
+    ``y[t] = sum_j weights[t, j] * rows[positions[t, j]]`` for fp32 ``rows``
+    [R, N]; a position outside [0, R) (:func:`moe_dispatch`'s -1) adds nothing.
+    Returns [..., N] as ``dtype``."""
+    _same_device(rows, positions, weights)
+    if rows.dtype != torch.float32 or weights.dtype != torch.float32:
+        raise TypeError("rows and weights must be fp32")
+    if rows.dim() != 2 or not rows.is_contiguous():
+        raise ValueError("expected contiguous rows [R, N]")
+    positions = _int32(positions, rows.device, "positions")
+    if positions.dim() == 0 or weights.shape != positions.shape:
+        raise ValueError("positions and weights must be [..., top_k]")
+    weights = weights.contiguous()
+    R, N = rows.shape
+    top_k = positions.shape[-1]
+    T = positions.numel() // top_k if top_k else 0
+    y = _empty((*positions.shape[:-1], N), dtype, rows.device)
+    _launch("moe_combine", rows.device, rows.data_ptr(), R, N, positions.data_ptr(),
+            weights.data_ptr(), T, top_k, y.data_ptr(), _dtype_code(dtype))
+    return y
+
+
+# ------------------------------------------------------ routing to experts
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _route_rows(logits: torch.Tensor, scoring: str):
+    if scoring not in _SCORES:
+        raise ValueError(f"scoring must be one of {sorted(_SCORES)}")
+    if logits.dim() < 1:
+        raise ValueError("expected logits [..., E]")
+    dt = _dtype_code(logits.dtype)
+    T, E, ld = _rows_view(logits)
+    return dt, T, E, ld, _SCORES[scoring]
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
+              bias: torch.Tensor | None = None, groups: int = 1, top_groups: int = 1,
+              renormalize: bool = True, scale: float = 1.0):
+    """The router of a mixture of experts: ``logits`` [..., E] (bf16 or fp32)
+    to ``(weights, experts)``, fp32 and int32 [..., top_k], best first.
+
+    Scores p are the softmax or the sigmoid of the logits. Experts are chosen
+    by p + ``bias`` (fp32 [E], for balance; it does not enter the weights),
+    ties to the lowest index; with ``groups`` > 1 only among the ``top_groups``
+    best of that many consecutive groups of experts, a group's score being the
+    sum of its two largest p + bias. Weights are ``scale`` times p, divided by
+    the sum of the chosen p with ``renormalize``. The choice is that of the
+    exact scores, not of their fp32 roundings. For training,
+    :func:`moe_route_backward` gives the logits' gradient (this call records
+    none)."""
+    _same_device(logits)
+    dt, T, E, ld, score = _route_rows(logits, scoring)
+    if bias is not None:
+        if bias.dtype != torch.float32 or bias.shape != (E,):
+            raise TypeError("bias must be fp32 [E]")
+        _same_device(logits, bias)
+        bias = bias.contiguous()
+    top_k = int(top_k)
+    shape = (*logits.shape[:-1], max(top_k, 0))
+    weights = _empty(shape, torch.float32, logits.device)
+    experts = _empty(shape, torch.int32, logits.device)
+    _launch("moe_route", logits.device, logits.data_ptr(), dt, T, E, ld, score,
+            None if bias is None else bias.data_ptr(), int(groups), int(top_groups), top_k,
+            1 if renormalize else 0, float(scale), weights.data_ptr(), experts.data_ptr())
+    return weights, experts
+
+
+def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, *,
+                       scoring: str = "softmax", renormalize: bool = True,
+                       scale: float = 1.0) -> torch.Tensor:
+    """Gradient of :func:`moe_route`'s weights with respect to the logits, for
+    the ``experts`` that it chose (int32 [..., top_k]) and the gradient of its
+    weights (fp32 [..., top_k]); shaped and typed like ``logits``. Experts
+    outside [0, E) are left out; the choice itself has no gradient."""
+    _same_device(logits, grad_weights, experts)
+    dt, T, E, ld, score = _route_rows(logits, scoring)
+    if grad_weights.dtype != torch.float32:
+        raise TypeError("grad_weights must be fp32")
+    experts = _int32(experts, logits.device, "experts")
+    if experts.dim() != logits.dim() or experts.shape[:-1] != logits.shape[:-1] or \
+            grad_weights.shape != experts.shape:
+        raise ValueError("grad_weights and experts must be [..., top_k] with the rows of logits")
+    grad_weights = grad_weights.contiguous()
+    out = _empty(logits.shape, logits.dtype, logits.device)
+    _launch("moe_route_backward", logits.device, grad_weights.data_ptr(), logits.data_ptr(), dt, T, E,
+            ld, experts.data_ptr(), score, experts.shape[-1], 1 if renormalize else 0, float(scale),
+            out.data_ptr())
+    return out
+
+
+def moe_dispatch(experts: torch.Tensor, E: int):
+    """The pairs (token, choice) sorted by expert, stable: ``experts`` int32
+    [..., top_k] (:func:`moe_route`'s) to ``(row_offsets, order, positions)``.
+
+    ``row_offsets`` int64 [E + 1], ``order`` int32 [P] (the flat index of the
+    pair at each place) and ``positions`` int32 shaped like ``experts`` (the
+    place of each pair) are on the device, so the grouped calls
+    (``mxfp8_quantize_grouped(x[order // top_k], row_offsets=...)``,
+    :func:`mxfp4_matvec_grouped`) follow without a copy to the host. Pairs with
+    an expert outside [0, E) are dropped: they come after ``row_offsets[E]``
+    and have position -1."""
+    _same_device(experts)
+    experts = _int32(experts, experts.device, "experts")
+    P, E = experts.numel(), int(E)
+    dev = experts.device
+    row_offsets = _empty(max(E, 0) + 1, torch.int64, dev)
+    order = _empty(P, torch.int32, dev)
+    positions = _empty(experts.shape, torch.int32, dev)
+    _launch("moe_dispatch", dev, experts.data_ptr(), P, E, row_offsets.data_ptr(), order.data_ptr(),
+            positions.data_ptr())
+    return row_offsets, order, positions
+
+
 def check_bounded_wait(timeout_ns: int = 2_000_000, device=None) -> dict:
     """Runs the self-check of the GEMM's bounded barrier wait on a CUDA device
     (``mxq_check_bounded_wait``): a wait on a barrier that nothing arrives on
@@ -671,6 +983,8 @@ def _traced(fn):
 for _name in ("mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped",
               "mxfp8_quantize_columnwise", "mxfp4_quantize", "mxfp4_dequantize",
               "mxfp4_quantize_grouped", "mx_fake_quantize", "mxfp8_gemm", "nvfp4_amax",
+              "mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
+              "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
               "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_amax_sliced", "nvfp4_quantize_sliced",
               "nvfp4_quantize_experts", "swizzle_scales"):
     globals()[_name] = _traced(globals()[_name])

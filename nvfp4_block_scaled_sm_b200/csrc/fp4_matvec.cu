@@ -1,0 +1,902 @@
+// fp4_matvec.cu -- products of a few rows with weights held in 4 bits
+// (MXFP4 and NVFP4): y[m, n] = sum_k x[m, k] w[n, k], for one weight and for
+// the experts of a stack.
+//
+// Mathematics. An E2M1 code is exact in fp16, and so is its product with an
+// E4M3 block scale (2 + 4 significant bits, 2^-10 .. 2688). A row x is brought
+// to fp16 in groups of 32 elements: with E the exponent of the group's largest
+// finite magnitude, the fp16 piece is x 2^(15 - E), so every element of at
+// least 2^-32 of that magnitude keeps all eight bits of a bf16. fp32 rows take
+// three pieces (11 + 11 + 2 bits, the first x 2^(14 - E)). What is left after the pieces of a pass is
+// computed exactly (x minus the pieces); if any of it is not zero, another
+// pass over the weights adds it, so the products that are summed are those of
+// x itself whatever its range. Each group's 32 products are summed by two
+// m16n8k16 MMAs (fp16 products exact, fp32 sums); the group's scales (the
+// E8M0 scale of MXFP4, the power of two of the piece) multiply that sum in
+// fp32 as it is added to the row's fp32 accumulator. NVFP4's global scale
+// multiplies the finished sum.
+//
+// Tiling. A warp holds 16 weight rows; a CTA of 8 warps 128 rows of a share of
+// K, up to 8 CTAs of a cluster the shares of the same rows, added up through
+// distributed shared memory in rank order (the same bits every run). Codes
+// arrive by 16-byte asynchronous copies in a ring of three or four stages per
+// warp (256 codes of each of its rows a stage), each warp waiting for its own;
+// the x pieces of the CTA's share are made once per CTA, in the order in which
+// a lane feeds them to the MMA, while the first codes are on their way.
+#include "common.cuh"
+
+namespace mxq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kStageK = 256;              // codes of a row in one stage
+constexpr int kStageGroups = 8;           // groups of 32 in one stage
+constexpr int kRowPitch = 144;            // bytes of a row of codes in shared memory: 128 + 16
+constexpr int kWarpTile = 16 * kRowPitch; // 16 rows; the pad keeps 8 rows x 4 words off each other's banks
+constexpr int kTileRows = 16 * kWarps;
+constexpr int kRedPitch = kTileRows + 4;  // floats of one column of the sums
+constexpr int kMaxPasses = 32;            // each pass takes at least 11 bits of a range of 277
+
+enum Fmt { kMx = 0, kNv = 1 };
+
+struct MatvecArgs {
+  const void* x;
+  const uint8_t* w;
+  const uint8_t* s;
+  const float* g;           // NVFP4: global scales
+  void* y;
+  const int64_t* off;       // NULL: one weight, else E + 1 row offsets
+  const int32_t* order;     // NULL, or the source of each row: order[r] / top_k
+  int64_t ld_x;
+  int64_t N, K;             // rows and columns of a weight
+  int64_t M;                // rows of the product (all experts)
+  int64_t x_rows;           // rows of x
+  int64_t w_pitch, s_pitch; // bytes of a weight row's codes and scales
+  int64_t w_expert, s_expert;
+  uint32_t E;
+  int32_t top_k;
+  uint32_t slots;           // (expert, rows) pairs that the grid covers
+  uint32_t stages;          // of K
+  uint32_t split;           // CTAs that share K (the cluster)
+  uint32_t chunk;           // stages of x pieces in shared memory
+  uint32_t colw;            // columns held for one n-tile
+  uint32_t g_per;           // global scales of an expert: 1, or 2 (one per half)
+  int swiglu;
+  int out_bf16;
+  int fast_scales;          // scale rows start on 4-byte boundaries
+};
+
+__device__ __forceinline__ uint32_t smem_ptr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Asynchronous copies to shared memory; `bytes` of the source are read and
+// the rest of the destination is zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Four fp16 pairs of the eight E2M1 codes of a word, lowest byte first.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{ .reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2; cvt.rn.f16x2.e2m1x2 %3, b3; }"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// c += A B for a 16 x 16 tile A (rows of weights) and a 16 x 8 tile B.
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <typename XT>
+struct Pieces;
+template <>
+struct Pieces<uint16_t> { static constexpr int n = 1, top = 15; };
+template <>
+struct Pieces<float> { static constexpr int n = 3, top = 14; };
+
+// Eight consecutive elements of a row as fp32 (zeros where !there).
+template <typename XT>
+__device__ __forceinline__ void load8(const XT* p, bool there, float (&v)[8]) {
+  In8<XT> in;
+  if (there) in.load(p); else in.zero();
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = in[i];
+}
+
+// One fp16 piece of a group of 32 elements held by four neighbouring lanes (8
+// each): h = fp16(v m) with m = 2^(TOP - E), E the exponent of the group's
+// largest finite magnitude; v becomes what the piece leaves (exact: h / m is a
+// rounding of v to fewer bits). TOP is 15 for bf16 values (at most 65280 then)
+// and 14 for fp32 ones, which 15 could round up to 2^16, fp16's infinity.
+// Infinities and NaNs go into the piece as they are and leave nothing. Returns
+// 1 / m.
+template <int TOP>
+__device__ __forceinline__ float take_piece(float (&v)[8], uint32_t (&h)[4]) {
+  float top = 0.f;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float a = fabsf(v[i]);
+    const bool finite = a < __uint_as_float(0x7f800000u);
+    odd |= !finite;
+    top = fmaxf(top, finite ? a : 0.f);
+  }
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+  const uint32_t E = __float_as_uint(top) >> 23;
+  const uint32_t mb = min(254u + TOP - E, 254u);  // biased exponent of m
+  const float m = __uint_as_float(mb << 23);
+  const float inv = __uint_as_float(mb == 254 ? 0x00400000u : (254u - mb) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    h[k] = cvt_f16x2(v[2 * k] * m, v[2 * k + 1] * m);
+    const float2 f = f16x2_to_f32x2(h[k]);
+    v[2 * k] -= f.x * inv;
+    v[2 * k + 1] -= f.y * inv;
+  }
+  if (odd) {                                      // inf - inf
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (!(fabsf(v[i]) < __uint_as_float(0x7f800000u))) v[i] = 0.f;
+  }
+  return inv;
+}
+
+// The (expert, rows) pair number `slot` of the pairs that the row offsets
+// make, TT rows at most in each: expert in *e, first row and row count; false
+// if there are fewer. Offsets are clamped to [0, M], so no row outside the
+// product is touched whatever they hold. One thread looks after one expert.
+__device__ __forceinline__ bool find_slot(const MatvecArgs& a, uint32_t slot, uint32_t TT, int64_t* sh,
+                                          uint32_t* e, int64_t* r0, uint32_t* m) {
+  // sh: [0] result expert, [1] first row, [2] rows, [3 ..] warp totals
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh[2] = 0;
+  uint64_t before = 0;
+  for (uint32_t base = 0; base < a.E; base += kThreads) {
+    const uint32_t i = base + tid;
+    int64_t b = 0, n = 0;
+    if (i < a.E) {
+      b = min(max(a.off[i], int64_t(0)), a.M);
+      n = max(min(max(a.off[i + 1], int64_t(0)), a.M) - b, int64_t(0));
+    }
+    const uint64_t tiles = (uint64_t(n) + TT - 1) / TT;
+    uint64_t incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t up = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += up;
+    }
+    __syncthreads();                              // sh[2] is set; the last totals are read
+    if (lane == 31) sh[3 + warp] = int64_t(incl);
+    __syncthreads();
+    uint64_t first = before + incl - tiles;
+    for (int w = 0; w < kWarps; w++) {
+      if (w < warp) first += uint64_t(sh[3 + w]);
+      before += uint64_t(sh[3 + w]);
+    }
+    if (slot >= first && slot < first + tiles) {
+      const int64_t skip = int64_t(slot - first) * TT;
+      sh[0] = i;
+      sh[1] = b + skip;
+      sh[2] = min(n - skip, int64_t(TT));
+    }
+    if (before > slot) break;                     // the same for every thread
+  }
+  __syncthreads();
+  *e = uint32_t(sh[0]);
+  *r0 = sh[1];
+  *m = uint32_t(sh[2]);
+  return sh[2] > 0;
+}
+
+__device__ __forceinline__ void cluster_arrive_wait() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float r;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr));
+  return r;
+}
+
+// One stage of a warp: 16 rows x 256 codes against the first NC of NT tiles of
+// 8 columns.
+// codes / scales: the stage's buffers of this warp; xf: the pieces of the
+// stage's first group at this lane's place; sx: their scales at this lane's
+// columns.
+template <int FMT, int NC, int NT>
+__device__ __forceinline__ void stage_math(float (&acc)[NT][4], uint32_t codes, uint32_t scales, uint32_t xf,
+                                           uint32_t xf_group, uint32_t sx, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t rowA = codes + g * kRowPitch + t * 4, rowB = rowA + 8 * kRowPitch;
+  if constexpr (FMT == kMx) {
+    const uint2 sA = lds64(scales + g * 8), sB = lds64(scales + g * 8 + 64);
+    // every scale byte in [64, 191]: the fp32 products c 2^(s - 127) can
+    // neither overflow nor leave the normal range, and the byte is the fp32
+    // exponent field as it stands
+    const uint32_t v = lds32(scales + lane * 4);
+    const bool plain = ((v ^ (v << 1)) & 0x80808080u) == 0x80808080u;
+    if (__all_sync(kFull, plain)) {
+#pragma unroll
+      for (int j = 0; j < kStageGroups; j++) {
+        uint32_t hA[4], hB[4];
+        codes_f16(lds32(rowA + j * 16), hA);
+        codes_f16(lds32(rowB + j * 16), hB);
+        const uint32_t wa = j < 4 ? sA.x : sA.y, wb = j < 4 ? sB.x : sB.y;
+        const int sh = 23 - 8 * (j & 3);
+        const float fA = __uint_as_float((sh >= 0 ? wa << (sh & 31) : wa >> 1) & 0x7f800000u);
+        const float fB = __uint_as_float((sh >= 0 ? wb << (sh & 31) : wb >> 1) & 0x7f800000u);
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint4 b = lds128(xf + j * xf_group + n * 512);
+          const uint2 u = lds64(sx + (j * NT + n) * 32);
+          const float s0 = __uint_as_float(u.x), s1 = __uint_as_float(u.y);
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(c, hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          mma16816(c, hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+          acc[n][0] = __fmaf_rn(c[0] * fA, s0, acc[n][0]);
+          acc[n][1] = __fmaf_rn(c[1] * fA, s1, acc[n][1]);
+          acc[n][2] = __fmaf_rn(c[2] * fB, s0, acc[n][2]);
+          acc[n][3] = __fmaf_rn(c[3] * fB, s1, acc[n][3]);
+        }
+      }
+    } else {
+      // scales near the ends of the range, and the NaN byte 255: the scaled
+      // sum is formed in fp64, where neither factor order can overflow or
+      // underflow, and rounded once to fp32
+#pragma unroll 1
+      for (int j = 0; j < kStageGroups; j++) {
+        uint32_t hA[4], hB[4];
+        codes_f16(lds32(rowA + j * 16), hA);
+        codes_f16(lds32(rowB + j * 16), hB);
+        const uint32_t ba = ((j < 4 ? sA.x : sA.y) >> (8 * (j & 3))) & 255u;
+        const uint32_t bb = ((j < 4 ? sB.x : sB.y) >> (8 * (j & 3))) & 255u;
+        const double fA = double(pow2_dequant(ba)), fB = double(pow2_dequant(bb));
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint4 b = lds128(xf + j * xf_group + n * 512);
+          const uint2 u = lds64(sx + (j * NT + n) * 32);
+          const double s0 = double(__uint_as_float(u.x)), s1 = double(__uint_as_float(u.y));
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(c, hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          mma16816(c, hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+          acc[n][0] += float(double(c[0]) * fA * s0);
+          acc[n][1] += float(double(c[1]) * fA * s1);
+          acc[n][2] += float(double(c[2]) * fB * s0);
+          acc[n][3] += float(double(c[3]) * fB * s1);
+        }
+      }
+    }
+  } else {
+    // 16 block scales of each row; this lane's codes of group j lie in block
+    // 2j + t / 2, whose byte is doubled into an fp16 pair
+    const uint4 sA = lds128(scales + g * 16), sB = lds128(scales + g * 16 + 128);
+    const uint32_t pick = (t >> 1) * 0x11u;
+#pragma unroll
+    for (int j = 0; j < kStageGroups; j++) {
+      uint32_t hA[4], hB[4];
+      codes_f16(lds32(rowA + j * 16), hA);
+      codes_f16(lds32(rowB + j * 16), hB);
+      const uint32_t wa = j < 2 ? sA.x : j < 4 ? sA.y : j < 6 ? sA.z : sA.w;
+      const uint32_t wb = j < 2 ? sB.x : j < 4 ? sB.y : j < 6 ? sB.z : sB.w;
+      const uint32_t sel = pick + ((j & 1) ? 0x22u : 0u);
+      const uint32_t fA = cvt_f16x2_from_e4m3x2(__byte_perm(wa, 0, sel));
+      const uint32_t fB = cvt_f16x2_from_e4m3x2(__byte_perm(wb, 0, sel));
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        hA[k] = mul_f16x2(hA[k], fA);
+        hB[k] = mul_f16x2(hB[k], fB);
+      }
+#pragma unroll
+      for (int n = 0; n < NC; n++) {
+        const uint4 b = lds128(xf + j * xf_group + n * 512);
+        const uint2 u = lds64(sx + (j * NT + n) * 32);
+        const float s0 = __uint_as_float(u.x), s1 = __uint_as_float(u.y);
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(c, hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+        mma16816(c, hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+        acc[n][0] = __fmaf_rn(c[0], s0, acc[n][0]);
+        acc[n][1] = __fmaf_rn(c[1], s1, acc[n][1]);
+        acc[n][2] = __fmaf_rn(c[2], s0, acc[n][2]);
+        acc[n][3] = __fmaf_rn(c[3], s1, acc[n][3]);
+      }
+    }
+  }
+}
+
+template <int FMT>
+struct ScaleBytes { static constexpr int stage = FMT == kMx ? 128 : 256; };   // of 16 rows
+
+// Bytes of the warps' rings of ST stages.
+template <int FMT, int ST>
+struct Ring { static constexpr int bytes = kWarps * ST * (kWarpTile + ScaleBytes<FMT>::stage); };
+
+template <int FMT, typename XT, int NT, bool A16, int ST>
+__global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArgs a) {
+  constexpr int P = Pieces<XT>::n;
+  constexpr uint32_t TT = 8 * NT / P;                  // rows of x in a tile
+  constexpr int kScale = ScaleBytes<FMT>::stage;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t found[3 + kWarps];
+  pdl_enter();
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = blockIdx.x % a.split;
+  const uint32_t unit = blockIdx.x / a.split;
+  const uint32_t slot = unit % a.slots;
+  const int64_t tile = unit / a.slots;
+  uint32_t e = 0, m = 0;
+  int64_t r0 = 0;
+  if (a.off) {
+    if (!find_slot(a, slot, TT, found, &e, &r0, &m)) return;   // the same for the whole cluster
+  } else {
+    r0 = int64_t(slot) * TT;
+    m = uint32_t(min(int64_t(TT), a.M - r0));
+  }
+
+  // ---- this warp's 16 weight rows: consecutive, or 8 of the gate half and
+  // the 8 of the up half that meet them (rows 0-7 and 8-15 of the MMA tile, so
+  // one lane ends up with both)
+  const int64_t half = a.N / 2;
+  const int64_t outs = a.swiglu ? half : a.N;
+  const int64_t o0 = tile * (a.swiglu ? kTileRows / 2 : kTileRows);
+  const int64_t wrow0 = o0 + warp * (a.swiglu ? 8 : 16);
+  auto weight_row = [&](int r, bool& there) -> int64_t {
+    const int64_t o = wrow0 + (a.swiglu ? (r & 7) : r);
+    there = o < outs;
+    return there ? (a.swiglu && r >= 8 ? o + half : o) : 0;
+  };
+  const uint8_t* const we = a.w + int64_t(e) * a.w_expert;
+  const uint8_t* const se = a.s + int64_t(e) * a.s_expert;
+
+  const uint32_t ring = smem_ptr(smem) + warp * ST * (kWarpTile + kScale);
+  const uint32_t s_begin = uint32_t(uint64_t(a.stages) * rank / a.split);
+  const uint32_t s_end = uint32_t(uint64_t(a.stages) * (rank + 1) / a.split);
+
+  // copies: 16 bytes a lane, 4 rows of 128 bytes an instruction (8 bytes and 2
+  // rows where rows start on 8-byte boundaries only)
+  constexpr int kLanes = A16 ? 8 : 16, kBytes = A16 ? 16 : 8, kStep = 32 / kLanes;
+  const int cr = lane / kLanes, cc = (lane % kLanes) * kBytes;
+  bool there0;
+  const uint8_t* const srcA = we + weight_row(cr, there0) * a.w_pitch + cc;
+  const uint8_t* const srcB = we + weight_row(cr + 8, there0) * a.w_pitch + cc;
+  // the row of a half's copy number i is kStep i further down; it exists while
+  // its output does
+  const int64_t last = outs - wrow0;
+  // scales: 4 bytes a lane
+  constexpr int kSLanes = kScale / 64;                 // lanes of a row: 2 or 4
+  const int64_t S = a.s_pitch;
+
+  auto issue = [&](uint32_t stage) {
+    const uint32_t buf = ring + (stage % ST) * (kWarpTile + kScale);
+    const int64_t k0 = int64_t(stage) * (kStageK / 2);
+    const int64_t left = a.w_pitch - k0 - cc;
+    const uint32_t bytes = left >= kBytes ? kBytes : left > 0 ? uint32_t(left) : 0u;
+#pragma unroll
+    for (int i = 0; i < 8 / kStep; i++) {
+      const int r = cr + kStep * i;
+      // both halves' rows r and r + 8
+      const bool ra = r < last, rb = (a.swiglu ? r : r + 8) < last;
+      const uint32_t na = ra ? bytes : 0u, nb = rb ? bytes : 0u;
+      const uint8_t* pa = na ? srcA + i * kStep * a.w_pitch + k0 : a.w;
+      const uint8_t* pb = nb ? srcB + i * kStep * a.w_pitch + k0 : a.w;
+      const uint32_t dst = buf + r * kRowPitch + cc;
+      if constexpr (A16) {
+        cp_async16(dst, pa, na);
+        cp_async16(dst + 8 * kRowPitch, pb, nb);
+      } else {
+        cp_async8(dst, pa, na);
+        cp_async8(dst + 8 * kRowPitch, pb, nb);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kScale / 128; i++) {
+      const int idx = lane + 32 * i;
+      const int r = idx / kSLanes;
+      const int64_t c = int64_t(stage) * kSLanes * 4 + (idx % kSLanes) * 4;
+      bool there;
+      const uint8_t* p = se + weight_row(r, there) * S + c;
+      const uint32_t dst = buf + kWarpTile + idx * 4;
+      constexpr uint32_t kNone = FMT == kMx ? 0x7f7f7f7fu : 0u;     // scale 1, or block scale 0
+      if (!there || c >= S) {
+        sts32(dst, kNone);
+      } else if (a.fast_scales) {
+        cp_async4(dst, p);
+      } else {
+        uint32_t v = kNone;
+#pragma unroll
+        for (int b = 0; b < 4; b++)
+          if (c + b < S) v = (v & ~(255u << (8 * b))) | (uint32_t(p[b]) << (8 * b));
+        sts32(dst, v);
+      }
+    }
+  };
+
+  // ---- x pieces of a chunk of stages, in shared memory: [group][column][32]
+  // fp16 and [group][8] scales of each n-tile
+  const uint32_t xbase = smem_ptr(smem) + Ring<FMT, ST>::bytes;
+  const uint32_t gstride = NT == 1 ? a.colw * 64 : NT * 512;        // bytes of one group's pieces
+  const uint32_t sbase = xbase + a.chunk * kStageGroups * gstride;
+  const XT* const x = static_cast<const XT*>(a.x);
+
+  auto stage_x = [&](uint32_t first, uint32_t n, int pass) -> bool {
+    bool left = false;
+    const uint32_t ng = n * kStageGroups;
+    const uint32_t tasks = m * ng * 4;
+    for (uint32_t i0 = warp * 32; i0 < tasks; i0 += kThreads) {     // tasks is a multiple of 32
+      const uint32_t i = i0 + lane;
+      const uint32_t t = i & 3, gi = (i >> 2) % ng, mi = (i >> 2) / ng;
+      const int64_t k = (int64_t(first) * kStageGroups + gi) * 32 + t * 8;
+      int64_t row = r0 + mi;
+      bool there = k < a.K;
+      if (a.order) {
+        const int32_t pair = a.order[row];
+        row = pair / a.top_k;
+        there = there && pair >= 0 && row < a.x_rows;
+      }
+      float v[8];
+      load8(x + (there ? row * a.ld_x + k : 0), there, v);
+      uint32_t h[4];
+      for (int q = 0; q < pass * P; q++) (void)take_piece<Pieces<XT>::top>(v, h);
+#pragma unroll
+      for (int p = 0; p < P; p++) {
+        const float inv = take_piece<Pieces<XT>::top>(v, h);
+        const uint32_t col = mi * P + p;
+        const uint32_t dst = xbase + gi * gstride + col * 64 + t * 16;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                     "r"(h[3]) : "memory");
+        if (t == 0) sts32(sbase + (gi * NT + (col >> 3)) * 32 + (col & 7) * 4, __float_as_uint(inv));
+      }
+#pragma unroll
+      for (int q = 0; q < 8; q++) left |= v[q] != 0.f;
+    }
+    return left;
+  };
+
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t lane_x = (NT == 1 ? (min(uint32_t(g), a.colw - 1) * 4 + t) : uint32_t(lane)) * 16;
+  const uint32_t used = (m * P + 7) / 8;                            // n-tiles with columns
+
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; n++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[n][i] = 0.f;
+
+  for (int pass = 0; pass < kMaxPasses; pass++) {
+    bool more = false;
+#pragma unroll
+    for (int i = 0; i < ST - 1; i++) {
+      if (s_begin + i < s_end) issue(s_begin + i);
+      cp_commit();
+    }
+    uint32_t c_begin = s_begin, c_end = s_begin;
+    for (uint32_t s = s_begin; s < s_end; s++) {
+      if (s == c_end) {
+        c_begin = s;
+        c_end = min(s + a.chunk, s_end);
+        __syncthreads();                                            // the last chunk has been read
+        const bool left = stage_x(c_begin, c_end - c_begin, pass);
+        more |= __syncthreads_or(left) != 0;
+      }
+      cp_wait<ST - 2>();
+      __syncwarp();                                                 // the stage is in; the one before is read
+      if (s + ST - 1 < s_end) issue(s + ST - 1);
+      cp_commit();
+      const uint32_t buf = ring + (s % ST) * (kWarpTile + kScale);
+      const uint32_t gi = (s - c_begin) * kStageGroups;
+      const uint32_t xf = xbase + gi * gstride + lane_x, sx = sbase + gi * NT * 32 + t * 8;
+      if (NT > 1 && used == 1)
+        stage_math<FMT, 1, NT>(acc, buf, buf + kWarpTile, xf, gstride, sx, lane);
+      else if (NT > 2 && used == 2)
+        stage_math<FMT, (NT > 2 ? 2 : NT), NT>(acc, buf, buf + kWarpTile, xf, gstride, sx, lane);
+      else
+        stage_math<FMT, NT, NT>(acc, buf, buf + kWarpTile, xf, gstride, sx, lane);
+    }
+    if (!more) break;
+    __syncthreads();
+  }
+
+  // ---- sums of the cluster's shares, in rank order
+  cp_wait<0>();
+  __syncthreads();                                                  // the rings are free
+  float* const red = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    if (uint32_t(n) < used) {
+      float* const c0 = red + (n * 8 + 2 * t) * kRedPitch + warp * 16 + g;
+      c0[0] = acc[n][0];
+      c0[kRedPitch] = acc[n][1];
+      c0[8] = acc[n][2];
+      c0[kRedPitch + 8] = acc[n][3];
+    }
+  }
+  if (a.split > 1) cluster_arrive_wait(); else __syncthreads();
+
+  const uint32_t per = a.swiglu ? kTileRows / 2 : kTileRows;
+  const uint32_t lo = per * rank / a.split, len = per * (rank + 1) / a.split - lo;
+  const uint32_t red_addr = smem_ptr(red);
+  auto total = [&](uint32_t col, uint32_t row) -> float {
+    float v = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; p++) {
+      const uint32_t at = ((col * P + p) * kRedPitch + row) * 4;
+      if (a.split == 1) {
+        v += red[at / 4];
+      } else {
+        for (uint32_t q = 0; q < a.split; q++) v += cluster_ld(cluster_map(red_addr + at, q));
+      }
+    }
+    return v;
+  };
+  for (uint32_t i = tid; i < m * len; i += kThreads) {
+    const uint32_t mi = i / len, o = lo + i % len;
+    if (o0 + o >= outs) continue;
+    float gA = 1.f, gB = 1.f;
+    if constexpr (FMT == kNv) {
+      const float* gp = a.g + int64_t(e) * a.g_per;
+      gA = gp[0];
+      gB = a.g_per == 2 ? gp[1] : gA;
+    }
+    float v;
+    if (a.swiglu) {
+      const uint32_t row = (o >> 3) * 16 + (o & 7);
+      const float gate = total(mi, row) * gA, up = total(mi, row + 8) * gB;
+      // silu(z) = z / (1 + e^-z); e^-z overflows to inf for z < -88, where
+      // silu is -0 to fp32's last bit
+      v = gate / (1.f + expf(-gate)) * up;
+    } else {
+      v = total(mi, o) * (o0 + o >= half && a.g_per == 2 ? gB : gA);
+    }
+    const int64_t at = (r0 + mi) * outs + o0 + o;
+    if (a.out_bf16)
+      static_cast<uint16_t*>(a.y)[at] = uint16_t(cvt_bf16x2(v, 0.f));
+    else
+      static_cast<float*>(a.y)[at] = v;
+  }
+  if (a.split > 1) cluster_arrive_wait();                           // no CTA leaves while its sums are read
+}
+
+// y[t, n] = sum_j weights[t, j] rows[positions[t, j], n]: a token's rows added
+// up in fp32 in the order of its choices (the same bits every run); a position
+// outside [0, R) adds nothing. One thread holds VEC neighbouring outputs.
+template <int VEC>
+__global__ void __launch_bounds__(kThreads) moe_combine_kernel(const float* __restrict__ rows,
+                                                               const int32_t* __restrict__ positions,
+                                                               const float* __restrict__ weights, void* y,
+                                                               int64_t R, int64_t T, int64_t N, int32_t top_k,
+                                                               uint32_t col_blocks, int out_bf16) {
+  pdl_enter();
+  const int64_t t = blockIdx.x / col_blocks;
+  const int64_t n = (int64_t(blockIdx.x % col_blocks) * kThreads + threadIdx.x) * VEC;
+  if (n >= N) return;
+  float v[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; i++) v[i] = 0.f;
+  for (int32_t j = 0; j < top_k; j++) {
+    const int64_t at = positions[t * top_k + j];
+    if (at < 0 || at >= R) continue;
+    const float w = weights[t * top_k + j];
+    const float* p = rows + at * N + n;
+    if constexpr (VEC == 4) {
+      const uint4 q = ld_nc_v4(p);
+      v[0] = __fmaf_rn(w, __uint_as_float(q.x), v[0]);
+      v[1] = __fmaf_rn(w, __uint_as_float(q.y), v[1]);
+      v[2] = __fmaf_rn(w, __uint_as_float(q.z), v[2]);
+      v[3] = __fmaf_rn(w, __uint_as_float(q.w), v[3]);
+    } else {
+      v[0] = __fmaf_rn(w, *p, v[0]);
+    }
+  }
+  const int64_t at = t * N + n;
+  if constexpr (VEC == 4) {
+    if (out_bf16)
+      st_v2(static_cast<uint16_t*>(y) + at, make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])));
+    else
+      st_v4(static_cast<float*>(y) + at, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                    __float_as_uint(v[2]), __float_as_uint(v[3])));
+  } else if (out_bf16) {
+    static_cast<uint16_t*>(y)[at] = uint16_t(cvt_bf16x2(v[0], 0.f));
+  } else {
+    static_cast<float*>(y)[at] = v[0];
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr uint32_t kPieceBytes = 30 << 10;       // shared memory for x pieces
+
+// How K is shared out: the split whose busiest multiprocessor has least to do,
+// counting a CTA's fixed work (its x pieces, the exchange of the sums) as two
+// stages.
+uint32_t choose_split(uint64_t units, uint32_t stages) {
+  const uint64_t sms = uint64_t(sm_count());
+  uint32_t best = 1;
+  uint64_t best_cost = ~0ull;
+  for (uint32_t c = 1; c <= 8 && (c == 1 || c <= stages); c++) {
+    const uint64_t cost = (units * c + sms - 1) / sms * ((stages + c - 1) / c + 2);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = c;
+    }
+  }
+  return best;
+}
+
+template <int FMT, typename XT, int NT, bool A16>
+mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
+  constexpr int ST = NT == 4 ? 3 : 4;
+  constexpr uint32_t P = Pieces<XT>::n;
+  constexpr uint32_t TT = 8 * NT / P;
+  const uint64_t tile_rows = a.swiglu ? kTileRows / 2 : kTileRows;
+  const uint64_t tiles = (uint64_t(a.swiglu ? a.N / 2 : a.N) + tile_rows - 1) / tile_rows;
+  uint64_t slots, likely;
+  if (a.off) {
+    // non-empty experts, and the tiles beyond their first
+    const uint64_t n = std::min<uint64_t>(a.E, uint64_t(a.M));
+    slots = n + (uint64_t(a.M) - n) / TT;
+    likely = n;
+  } else {
+    slots = likely = (uint64_t(a.M) + TT - 1) / TT;
+  }
+  a.split = choose_split(likely * tiles, a.stages);
+  if (slots * tiles * a.split > 0x7fffffffull) return MXQ_ERR_SHAPE;
+  a.slots = uint32_t(slots);
+  a.colw = NT == 1 ? uint32_t(std::min<uint64_t>(8, std::min<uint64_t>(TT, uint64_t(a.M)) * P)) : 8;
+  const uint32_t per_stage = kStageGroups * NT * (a.colw * 64 + 32);
+  const uint32_t share = (a.stages + a.split - 1) / a.split;
+  a.chunk = std::max(1u, std::min(share, kPieceBytes / per_stage));
+  const size_t smem = size_t(Ring<FMT, ST>::bytes) + size_t(a.chunk) * per_stage;
+
+  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, ST>;
+  constexpr int kMostSmem = Ring<FMT, ST>::bytes + int(kPieceBytes);
+  const cudaError_t attr_err = ensure_smem_limit<kernel>(kMostSmem);
+  if (attr_err != cudaSuccess) {
+    record_cuda_error(attr_err);
+    return MXQ_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(uint32_t(slots * tiles) * a.split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return launched(cudaLaunchKernelEx(&cfg, kernel, a));
+}
+
+template <int FMT, typename XT, bool A16>
+mxq_status launch_columns(const MatvecArgs& a, cudaStream_t stream) {
+  // columns of the MMA that a tile of rows takes; an expert's rows vary, so
+  // twice the average has to fit
+  const uint64_t rows = a.off ? (2 * uint64_t(a.M) + a.E - 1) / a.E : uint64_t(a.M);
+  const uint64_t cols = rows * Pieces<XT>::n;
+  if (cols <= 8) return launch_matvec<FMT, XT, 1, A16>(a, stream);
+  if (cols <= 16) return launch_matvec<FMT, XT, 2, A16>(a, stream);
+  return launch_matvec<FMT, XT, 4, A16>(a, stream);
+}
+
+template <int FMT>
+mxq_status launch_fp4(const MatvecArgs& a, int dt, cudaStream_t stream) {
+  if constexpr (FMT == kNv) {
+    if (a.w_pitch % 16 != 0)
+      return dt == MXQ_BF16 ? launch_columns<FMT, uint16_t, false>(a, stream)
+                            : launch_columns<FMT, float, false>(a, stream);
+  }
+  return dt == MXQ_BF16 ? launch_columns<FMT, uint16_t, true>(a, stream)
+                        : launch_columns<FMT, float, true>(a, stream);
+}
+
+struct Call {
+  const void* x;
+  int dt;
+  int64_t x_rows, K, ld_x;
+  const uint8_t* packed;
+  const uint8_t* scale;
+  const float* g;
+  int64_t N;
+  void* y;
+  int out_dt;
+};
+
+constexpr int64_t kMostRows = 0x7fffffff;
+
+// The checks that one weight and the experts' weights share; MXQ_OK with
+// *done set when there is nothing to do.
+template <int FMT>
+mxq_status check_call(const Call& c, int64_t M, int64_t E, bool* done) {
+  constexpr int kBlock = FMT == kMx ? 32 : 16;
+  *done = false;
+  if (!valid_dtype(c.dt) || !valid_dtype(c.out_dt)) return MXQ_ERR_DTYPE;
+  if (M < 0 || c.x_rows < 0 || c.N < 0 || c.K < 0 || c.K % kBlock != 0 || c.ld_x < c.K) return MXQ_ERR_SHAPE;
+  if (M > kMostRows || c.x_rows > kMostRows || c.N > kMostRows || c.K > kMostRows) return MXQ_ERR_SHAPE;
+  if (M == 0 || c.N == 0) {
+    *done = true;
+    return MXQ_OK;
+  }
+  if (!c.y) return MXQ_ERR_NULL;
+  if (c.K > 0 && (!c.x || !c.packed || !c.scale || (FMT == kNv && !c.g))) return MXQ_ERR_NULL;
+  if (!aligned16(c.x) || !aligned16(c.packed) || !aligned16(c.y) || (c.ld_x * elem_size(c.dt)) % 16 != 0)
+    return MXQ_ERR_ALIGN;
+  if (FMT == kNv && (reinterpret_cast<uintptr_t>(c.g) & 3u)) return MXQ_ERR_ALIGN;
+  (void)E;
+  return MXQ_OK;
+}
+
+template <int FMT>
+MatvecArgs make_args(const Call& c, int64_t M) {
+  constexpr int kBlock = FMT == kMx ? 32 : 16;
+  MatvecArgs a{};
+  a.x = c.x;
+  a.w = c.packed;
+  a.s = c.scale;
+  a.g = c.g;
+  a.y = c.y;
+  a.ld_x = c.ld_x;
+  a.N = c.N;
+  a.K = c.K;
+  a.M = M;
+  a.x_rows = c.x_rows;
+  a.w_pitch = c.K / 2;
+  a.s_pitch = c.K / kBlock;
+  a.w_expert = c.N * a.w_pitch;
+  a.s_expert = c.N * a.s_pitch;
+  a.top_k = 1;
+  a.g_per = 1;
+  a.stages = uint32_t((c.K + kStageK - 1) / kStageK);
+  a.out_bf16 = c.out_dt == MXQ_BF16;
+  a.fast_scales = a.s_pitch % 4 == 0 && (reinterpret_cast<uintptr_t>(c.scale) & 3u) == 0;
+  return a;
+}
+
+template <int FMT>
+mxq_status matvec_entry(const Call& c, mxq_stream_t stream) {
+  bool done;
+  const mxq_status st = check_call<FMT>(c, c.x_rows, 1, &done);
+  if (st != MXQ_OK || done) return st;
+  return launch_fp4<FMT>(make_args<FMT>(c, c.x_rows), c.dt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+template <int FMT>
+mxq_status grouped_entry(const Call& c, int32_t E, int32_t scales_per_expert, const int64_t* row_offsets,
+                         int64_t R, const int32_t* order, int32_t top_k, int32_t swiglu,
+                         mxq_stream_t stream) {
+  if (E < 1 || E > MXQ_GROUPED_MAX_EXPERTS) return MXQ_ERR_SHAPE;
+  if (swiglu != 0 && swiglu != 1) return MXQ_ERR_ARG;
+  if (scales_per_expert != 1 && scales_per_expert != 2) return MXQ_ERR_ARG;
+  if ((swiglu || scales_per_expert == 2) && c.N % 2 != 0) return MXQ_ERR_SHAPE;
+  if (order ? top_k < 1 : (top_k != 1 || c.x_rows != R)) return MXQ_ERR_ARG;
+  bool done;
+  const mxq_status st = check_call<FMT>(c, R, E, &done);
+  if (st != MXQ_OK || done) return st;
+  if (!row_offsets) return MXQ_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(row_offsets) & 7u) || (reinterpret_cast<uintptr_t>(order) & 3u))
+    return MXQ_ERR_ALIGN;
+  MatvecArgs a = make_args<FMT>(c, R);
+  a.off = row_offsets;
+  a.order = order;
+  a.top_k = top_k;
+  a.E = uint32_t(E);
+  a.g_per = uint32_t(scales_per_expert);
+  a.swiglu = swiglu;
+  return launch_fp4<FMT>(a, c.dt, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+}  // namespace mxq
+
+extern "C" {
+
+mxq_status mxfp4_matvec(const void* x, int dt, int64_t M, int64_t K, int64_t ld_x, const uint8_t* packed,
+                        const uint8_t* scale, int64_t N, void* y, int out_dt, mxq_stream_t stream) {
+  return mxq::matvec_entry<mxq::kMx>({x, dt, M, K, ld_x, packed, scale, nullptr, N, y, out_dt}, stream);
+}
+
+mxq_status nvfp4_matvec(const void* x, int dt, int64_t M, int64_t K, int64_t ld_x, const uint8_t* packed,
+                        const uint8_t* block_scale, const float* global_scale, int64_t N, void* y, int out_dt,
+                        mxq_stream_t stream) {
+  return mxq::matvec_entry<mxq::kNv>({x, dt, M, K, ld_x, packed, block_scale, global_scale, N, y, out_dt},
+                                     stream);
+}
+
+mxq_status mxfp4_matvec_grouped(const void* x, int dt, int64_t x_rows, int64_t K, int64_t ld_x,
+                                const uint8_t* packed, const uint8_t* scale, int32_t E, int64_t N,
+                                const int64_t* row_offsets, int64_t R, const int32_t* order, int32_t top_k,
+                                int32_t swiglu, void* y, int out_dt, mxq_stream_t stream) {
+  return mxq::grouped_entry<mxq::kMx>({x, dt, x_rows, K, ld_x, packed, scale, nullptr, N, y, out_dt}, E, 1,
+                                      row_offsets, R, order, top_k, swiglu, stream);
+}
+
+mxq_status nvfp4_matvec_grouped(const void* x, int dt, int64_t x_rows, int64_t K, int64_t ld_x,
+                                const uint8_t* packed, const uint8_t* block_scale, const float* global_scales,
+                                int32_t scales_per_expert, int32_t E, int64_t N, const int64_t* row_offsets,
+                                int64_t R, const int32_t* order, int32_t top_k, int32_t swiglu, void* y,
+                                int out_dt, mxq_stream_t stream) {
+  return mxq::grouped_entry<mxq::kNv>({x, dt, x_rows, K, ld_x, packed, block_scale, global_scales, N, y, out_dt},
+                                      E, scales_per_expert, row_offsets, R, order, top_k, swiglu, stream);
+}
+
+mxq_status moe_combine(const float* rows, int64_t R, int64_t N, const int32_t* positions, const float* weights,
+                       int64_t T, int32_t top_k, void* y, int out_dt, mxq_stream_t stream) {
+  using namespace mxq;
+  if (!valid_dtype(out_dt)) return MXQ_ERR_DTYPE;
+  if (R < 0 || N < 0 || T < 0 || top_k < 0 || R > kMostRows || N > kMostRows || T > kMostRows)
+    return MXQ_ERR_SHAPE;
+  if (T == 0 || N == 0) return MXQ_OK;
+  if (!y || (top_k > 0 && (!positions || !weights)) || (R > 0 && !rows)) return MXQ_ERR_NULL;
+  if (!aligned16(rows) || !aligned16(y) || (reinterpret_cast<uintptr_t>(positions) & 3u) ||
+      (reinterpret_cast<uintptr_t>(weights) & 3u))
+    return MXQ_ERR_ALIGN;
+  const bool wide = N % 4 == 0;
+  const int64_t per = int64_t(kThreads) * (wide ? 4 : 1);
+  const int64_t blocks = (N + per - 1) / per;
+  if (blocks * T > 0x7fffffffll) return MXQ_ERR_SHAPE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int bf16 = out_dt == MXQ_BF16;
+  return launched(wide ? launch_pdl(moe_combine_kernel<4>, uint32_t(blocks * T), s, rows, positions, weights, y, R,
+                                    T, N, top_k, uint32_t(blocks), bf16)
+                       : launch_pdl(moe_combine_kernel<1>, uint32_t(blocks * T), s, rows, positions, weights, y, R,
+                                    T, N, top_k, uint32_t(blocks), bf16));
+}
+
+}  // extern "C"
