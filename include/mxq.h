@@ -343,7 +343,7 @@ mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
  *  global_scale  device fp32 scalar, 4-byte aligned.
  *  y       [M, N] of out_dt, contiguous, 16-byte aligned; may not overlap an
  *          input. K == 0 writes zeros.
- * M, N, K <= 2^31 - 1. (The pages quantize the weights, "V4 mxfp4 #1372" and
+ * M, N <= 2^31 - 1, K <= 2^23. (The pages quantize the weights, "V4 mxfp4 #1372" and
  * "Add FP8, NVFP4, and QARL training and export"; the product with them is
  * this library's.) One launch. */
 mxq_status mxfp4_matvec(const void* x, int dt, int64_t M, int64_t K, int64_t ld_x,

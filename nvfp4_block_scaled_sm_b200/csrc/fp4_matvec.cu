@@ -23,19 +23,20 @@
 // warp (256 codes of each of its rows a stage), each warp waiting for its own;
 // the x pieces of the CTA's share are made once per CTA, in the order in which
 // a lane feeds them to the MMA, while the first codes are on their way.
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace mxq {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kStageK = 256;              // codes of a row in one stage
 constexpr int kStageGroups = 8;           // groups of 32 in one stage
 constexpr int kRowPitch = 144;            // bytes of a row of codes in shared memory: 128 + 16
 constexpr int kWarpTile = 16 * kRowPitch; // 16 rows; the pad keeps 8 rows x 4 words off each other's banks
-constexpr int kTileRows = 16 * kWarps;
-constexpr int kRedPitch = kTileRows + 4;  // floats of one column of the sums
 constexpr int kMaxPasses = 32;            // each pass takes at least 11 bits of a range of 277
+
+constexpr uint32_t kNarrow = 4;           // columns (rows of x times pieces) that stage_narrow takes
 
 enum Fmt { kMx = 0, kNv = 1 };
 
@@ -63,15 +64,23 @@ struct MatvecArgs {
   uint32_t g_per;           // global scales of an expert: 1, or 2 (one per half)
   int swiglu;
   int out_bf16;
-  int fast_scales;          // scale rows start on 4-byte boundaries
+  uint32_t scale_align;     // scale rows start on boundaries of 16, 4 or 1 bytes
 };
 
 __device__ __forceinline__ uint32_t smem_ptr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Asynchronous copies to shared memory; `bytes` of the source are read and
-// the rest of the destination is zero.
+// Asynchronous copies to shared memory; where `bytes` is given, that many of
+// the source are read and the rest of the destination is zero. The 16-byte
+// form asks L2 for 256 bytes around it: a warp reads 128 bytes of a row in one
+// stage and the next 128 in the following one.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -107,7 +116,9 @@ __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-// Four fp16 pairs of the eight E2M1 codes of a word, lowest byte first.
+// Four fp16 pairs of the eight E2M1 codes of a word, lowest byte first. The
+// bytes are named within one asm statement: the conversion picks its byte of
+// the register, where shifting them down first costs an instruction each.
 __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
   asm("{ .reg .b8 b0, b1, b2, b3; mov.b32 {b0, b1, b2, b3}, %4;\n\t"
       "cvt.rn.f16x2.e2m1x2 %0, b0; cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
@@ -130,6 +141,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// c = A B.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -143,65 +163,95 @@ struct Pieces<uint16_t> { static constexpr int n = 1, top = 15; };
 template <>
 struct Pieces<float> { static constexpr int n = 3, top = 14; };
 
-// Eight consecutive elements of a row as fp32 (zeros where !there).
-template <typename XT>
-__device__ __forceinline__ void load8(const XT* p, bool there, float (&v)[8]) {
-  In8<XT> in;
-  if (there) in.load(p); else in.zero();
-#pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = in[i];
-}
-
-// One fp16 piece of a group of 32 elements held by four neighbouring lanes (8
-// each): h = fp16(v m) with m = 2^(TOP - E), E the exponent of the group's
-// largest finite magnitude; v becomes what the piece leaves (exact: h / m is a
-// rounding of v to fewer bits). TOP is 15 for bf16 values (at most 65280 then)
-// and 14 for fp32 ones, which 15 could round up to 2^16, fp16's infinity.
-// Infinities and NaNs go into the piece as they are and leave nothing. Returns
-// 1 / m.
-template <int TOP>
+// One fp16 piece of elements held 8 a lane, of a group of 32 (four
+// neighbouring lanes) or, with COMMON, of the warp's 256: h = fp16(v m) with
+// m = 2^(TOP - E), E the exponent of their largest finite magnitude; v becomes
+// what the piece leaves (exact: h / m is a rounding of v to fewer bits). TOP
+// is 15 for bf16 values (at most 65280 then) and 14 for fp32 ones, which 15
+// could round up to 2^16, fp16's infinity. Infinities and NaNs go into the
+// piece as they are and leave nothing. Returns 1 / m.
+template <int TOP, bool COMMON>
 __device__ __forceinline__ float take_piece(float (&v)[8], uint32_t (&h)[4]) {
-  float top = 0.f;
+  constexpr uint32_t kInf = 0x7f800000u;
+  uint32_t top = 0;                               // bits of magnitudes order as they do
   bool odd = false;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const float a = fabsf(v[i]);
-    const bool finite = a < __uint_as_float(0x7f800000u);
-    odd |= !finite;
-    top = fmaxf(top, finite ? a : 0.f);
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+    odd |= b >= kInf;
+    top = max(top, b);
   }
-  top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-  const uint32_t E = __float_as_uint(top) >> 23;
-  const uint32_t mb = min(254u + TOP - E, 254u);  // biased exponent of m
+  if (odd) {
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;
+      top = max(top, b < kInf ? b : 0u);
+    }
+  }
+  if constexpr (COMMON) {
+    top = __reduce_max_sync(kFull, top);
+  } else {
+    top = max(top, __shfl_xor_sync(kFull, top, 1));
+    top = max(top, __shfl_xor_sync(kFull, top, 2));
+  }
+  const uint32_t mb = min(254u + TOP - (top >> 23), 254u);          // biased exponent of m
   const float m = __uint_as_float(mb << 23);
   const float inv = __uint_as_float(mb == 254 ? 0x00400000u : (254u - mb) << 23);
 #pragma unroll
   for (int k = 0; k < 4; k++) {
     h[k] = cvt_f16x2(v[2 * k] * m, v[2 * k + 1] * m);
     const float2 f = f16x2_to_f32x2(h[k]);
-    v[2 * k] -= f.x * inv;
-    v[2 * k + 1] -= f.y * inv;
+    v[2 * k] = __fmaf_rn(-f.x, inv, v[2 * k]);
+    v[2 * k + 1] = __fmaf_rn(-f.y, inv, v[2 * k + 1]);
   }
   if (odd) {                                      // inf - inf
 #pragma unroll
     for (int i = 0; i < 8; i++)
-      if (!(fabsf(v[i]) < __uint_as_float(0x7f800000u))) v[i] = 0.f;
+      if ((__float_as_uint(v[i]) & kInf) == kInf) v[i] = 0.f;
   }
   return inv;
+}
+
+// The piece of a warp's 256 bf16 values (pairs, 8 a lane) under one scale,
+// taken on the packed values: the largest and the smallest non-zero magnitude
+// tell whether it holds all of them (an element of biased exponent e has its
+// last bit at 2^(e - 134), the piece's last bit is m 2^-24 with m = 2^(142 - E)).
+// False if it does not, or if there is an infinity.
+__device__ __forceinline__ bool whole_piece(const uint32_t (&w)[4], uint32_t (&h)[4], float& inv) {
+  const uint32_t am = absmax_bf16x2(absmax_bf16x2(w[0], w[1]), absmax_bf16x2(w[2], w[3])) & 0x7fff7fffu;
+  const uint32_t top = __reduce_max_sync(kFull, max(am >> 16, am & 0xffffu));
+  uint32_t low = 0xffffffffu;                     // smallest magnitude less one, zeros as 65535
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    uint32_t b = w[k] & 0x7fff7fffu;
+    asm("{ .reg .b32 t; add.u16x2 t, %1, %2; min.u16x2 %0, %0, t; }" : "+r"(low) : "r"(b), "r"(0xffffffffu));
+  }
+  low = __reduce_min_sync(kFull, min(low >> 16, low & 0xffffu));
+  const uint32_t E = top >> 7;
+  const uint32_t mb = min(269u - E, 254u);        // biased exponent of m
+  const float m = __uint_as_float(mb << 23);
+  inv = __uint_as_float(mb == 254 ? 0x00400000u : (254u - mb) << 23);
+#pragma unroll
+  for (int k = 0; k < 4; k++) {
+    const float2 f = mul_bf16x2_pow2(w[k], m);
+    h[k] = cvt_f16x2(f.x, f.y);
+  }
+  return top < 0x7f80u && int(low) + 1 >= (int(E) - 32) * 128;
 }
 
 // The (expert, rows) pair number `slot` of the pairs that the row offsets
 // make, TT rows at most in each: expert in *e, first row and row count; false
 // if there are fewer. Offsets are clamped to [0, M], so no row outside the
 // product is touched whatever they hold. One thread looks after one expert.
+template <int W>
 __device__ __forceinline__ bool find_slot(const MatvecArgs& a, uint32_t slot, uint32_t TT, int64_t* sh,
                                           uint32_t* e, int64_t* r0, uint32_t* m) {
   // sh: [0] result expert, [1] first row, [2] rows, [3 ..] warp totals
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sh[2] = 0;
   uint64_t before = 0;
-  for (uint32_t base = 0; base < a.E; base += kThreads) {
+  for (uint32_t base = 0; base < a.E; base += W * 32) {
     const uint32_t i = base + tid;
     int64_t b = 0, n = 0;
     if (i < a.E) {
@@ -219,7 +269,7 @@ __device__ __forceinline__ bool find_slot(const MatvecArgs& a, uint32_t slot, ui
     if (lane == 31) sh[3 + warp] = int64_t(incl);
     __syncthreads();
     uint64_t first = before + incl - tiles;
-    for (int w = 0; w < kWarps; w++) {
+    for (int w = 0; w < W; w++) {
       if (w < warp) first += uint64_t(sh[3 + w]);
       before += uint64_t(sh[3 + w]);
     }
@@ -252,24 +302,40 @@ __device__ __forceinline__ float cluster_ld(uint32_t addr) {
   return r;
 }
 
+// Scales are copied for several stages at a time (16 bytes of a row or more):
+// two blocks of 16 rows a warp. A block is overwritten when the second one
+// after it is begun, which is ST - 1 stages ahead of the reader.
+template <int FMT, int ST>
+struct ScaleBlock {
+  static constexpr int stages = ST == 3 ? 2 : 4;
+  static_assert(ST - 1 <= stages, "two blocks do not cover the stages in flight");
+  static constexpr int stage = FMT == kMx ? 8 : 16;              // bytes of a row in one stage
+  static constexpr int row = stages * stage;
+  static constexpr int bytes = 16 * row;
+};
+
 // One stage of a warp: 16 rows x 256 codes against the first NC of NT tiles of
-// 8 columns.
-// codes / scales: the stage's buffers of this warp; xf: the pieces of the
-// stage's first group at this lane's place; sx: their scales at this lane's
-// columns.
-template <int FMT, int NC, int NT>
-__device__ __forceinline__ void stage_math(float (&acc)[NT][4], uint32_t codes, uint32_t scales, uint32_t xf,
-                                           uint32_t xf_group, uint32_t sx, int lane) {
+// 8 columns. codes / scales: the stage's buffers of this warp; xf: the pieces
+// of the stage's first group at this lane's place; sx: their scales at this
+// lane's columns, sx_group bytes from group to group; even: every column's
+// pieces share one scale in this stage.
+template <int FMT, int ST, int NC, int NA>
+__device__ __forceinline__ void stage_math(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t xf,
+                                           uint32_t xf_group, uint32_t sx, uint32_t sx_group, bool even,
+                                           int lane) {
+  constexpr int kRow = ScaleBlock<FMT, ST>::row;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t rowA = codes + g * kRowPitch + t * 4, rowB = rowA + 8 * kRowPitch;
+  float c[NC][4];
   if constexpr (FMT == kMx) {
-    const uint2 sA = lds64(scales + g * 8), sB = lds64(scales + g * 8 + 64);
+    const uint2 sA = lds64(scales + g * kRow), sB = lds64(scales + (g + 8) * kRow);
     // every scale byte in [64, 191]: the fp32 products c 2^(s - 127) can
     // neither overflow nor leave the normal range, and the byte is the fp32
     // exponent field as it stands
-    const uint32_t v = lds32(scales + lane * 4);
+    const uint32_t v = lds32(scales + (lane >> 1) * kRow + (lane & 1) * 4);
     const bool plain = ((v ^ (v << 1)) & 0x80808080u) == 0x80808080u;
-    if (__all_sync(kFull, plain)) {
+    if (__all_sync(kFull, plain && even)) {
+      float part[NC][4];
 #pragma unroll
       for (int j = 0; j < kStageGroups; j++) {
         uint32_t hA[4], hB[4];
@@ -282,21 +348,24 @@ __device__ __forceinline__ void stage_math(float (&acc)[NT][4], uint32_t codes, 
 #pragma unroll
         for (int n = 0; n < NC; n++) {
           const uint4 b = lds128(xf + j * xf_group + n * 512);
-          const uint2 u = lds64(sx + (j * NT + n) * 32);
-          const float s0 = __uint_as_float(u.x), s1 = __uint_as_float(u.y);
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(c, hA[0], hB[0], hA[1], hB[1], b.x, b.y);
-          mma16816(c, hA[2], hB[2], hA[3], hB[3], b.z, b.w);
-          acc[n][0] = __fmaf_rn(c[0] * fA, s0, acc[n][0]);
-          acc[n][1] = __fmaf_rn(c[1] * fA, s1, acc[n][1]);
-          acc[n][2] = __fmaf_rn(c[2] * fB, s0, acc[n][2]);
-          acc[n][3] = __fmaf_rn(c[3] * fB, s1, acc[n][3]);
+          mma16816_first(c[n], hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          mma16816(c[n], hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            part[n][i] = j == 0 ? c[n][i] * (i < 2 ? fA : fB) : __fmaf_rn(c[n][i], i < 2 ? fA : fB, part[n][i]);
         }
       }
+#pragma unroll
+      for (int n = 0; n < NC; n++) {
+        const uint2 u = lds64(sx + n * 32);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          acc[n][i] = __fmaf_rn(part[n][i], __uint_as_float(i & 1 ? u.y : u.x), acc[n][i]);
+      }
     } else {
-      // scales near the ends of the range, and the NaN byte 255: the scaled
-      // sum is formed in fp64, where neither factor order can overflow or
-      // underflow, and rounded once to fp32
+      // pieces with a scale for each group, scales near the ends of the range,
+      // and the NaN byte 255: the scaled sum is formed in fp64, where neither
+      // factor order can overflow or underflow, and rounded once to fp32
 #pragma unroll 1
       for (int j = 0; j < kStageGroups; j++) {
         uint32_t hA[4], hB[4];
@@ -308,26 +377,21 @@ __device__ __forceinline__ void stage_math(float (&acc)[NT][4], uint32_t codes, 
 #pragma unroll
         for (int n = 0; n < NC; n++) {
           const uint4 b = lds128(xf + j * xf_group + n * 512);
-          const uint2 u = lds64(sx + (j * NT + n) * 32);
-          const double s0 = double(__uint_as_float(u.x)), s1 = double(__uint_as_float(u.y));
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(c, hA[0], hB[0], hA[1], hB[1], b.x, b.y);
-          mma16816(c, hA[2], hB[2], hA[3], hB[3], b.z, b.w);
-          acc[n][0] += float(double(c[0]) * fA * s0);
-          acc[n][1] += float(double(c[1]) * fA * s1);
-          acc[n][2] += float(double(c[2]) * fB * s0);
-          acc[n][3] += float(double(c[3]) * fB * s1);
+          const uint2 u = lds64(sx + j * sx_group + n * 32);
+          mma16816_first(c[n], hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          mma16816(c[n], hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            acc[n][i] += float(double(c[n][i]) * (i < 2 ? fA : fB) * double(__uint_as_float(i & 1 ? u.y : u.x)));
         }
       }
     }
   } else {
     // 16 block scales of each row; this lane's codes of group j lie in block
     // 2j + t / 2, whose byte is doubled into an fp16 pair
-    const uint4 sA = lds128(scales + g * 16), sB = lds128(scales + g * 16 + 128);
+    const uint4 sA = lds128(scales + g * kRow), sB = lds128(scales + (g + 8) * kRow);
     const uint32_t pick = (t >> 1) * 0x11u;
-#pragma unroll
-    for (int j = 0; j < kStageGroups; j++) {
-      uint32_t hA[4], hB[4];
+    auto weights = [&](int j, uint32_t (&hA)[4], uint32_t (&hB)[4]) {
       codes_f16(lds32(rowA + j * 16), hA);
       codes_f16(lds32(rowB + j * 16), hB);
       const uint32_t wa = j < 2 ? sA.x : j < 4 ? sA.y : j < 6 ? sA.z : sA.w;
@@ -340,37 +404,192 @@ __device__ __forceinline__ void stage_math(float (&acc)[NT][4], uint32_t codes, 
         hA[k] = mul_f16x2(hA[k], fA);
         hB[k] = mul_f16x2(hB[k], fB);
       }
+    };
+    auto add = [&](int j) {
 #pragma unroll
       for (int n = 0; n < NC; n++) {
-        const uint4 b = lds128(xf + j * xf_group + n * 512);
-        const uint2 u = lds64(sx + (j * NT + n) * 32);
-        const float s0 = __uint_as_float(u.x), s1 = __uint_as_float(u.y);
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(c, hA[0], hB[0], hA[1], hB[1], b.x, b.y);
-        mma16816(c, hA[2], hB[2], hA[3], hB[3], b.z, b.w);
-        acc[n][0] = __fmaf_rn(c[0], s0, acc[n][0]);
-        acc[n][1] = __fmaf_rn(c[1], s1, acc[n][1]);
-        acc[n][2] = __fmaf_rn(c[2], s0, acc[n][2]);
-        acc[n][3] = __fmaf_rn(c[3], s1, acc[n][3]);
+        const uint2 u = lds64(sx + j * sx_group + n * 32);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          acc[n][i] = __fmaf_rn(c[n][i], __uint_as_float(i & 1 ? u.y : u.x), acc[n][i]);
+      }
+    };
+    if (even) {                                   // the stage's 256 products are one sum
+#pragma unroll
+      for (int j = 0; j < kStageGroups; j++) {
+        uint32_t hA[4], hB[4];
+        weights(j, hA, hB);
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint4 b = lds128(xf + j * xf_group + n * 512);
+          if (j == 0) mma16816_first(c[n], hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          else mma16816(c[n], hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          mma16816(c[n], hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+        }
+      }
+      add(0);
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < kStageGroups; j++) {
+        uint32_t hA[4], hB[4];
+        weights(j, hA, hB);
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint4 b = lds128(xf + j * xf_group + n * 512);
+          mma16816_first(c[n], hA[0], hB[0], hA[1], hB[1], b.x, b.y);
+          mma16816(c[n], hA[2], hB[2], hA[3], hB[3], b.z, b.w);
+        }
+        add(j);
       }
     }
   }
 }
 
-template <int FMT>
-struct ScaleBytes { static constexpr int stage = FMT == kMx ? 128 : 256; };   // of 16 rows
+// Products of one MMA chain with its scales: acc += c f s, f the blocks' scales
+// of rows g (0, 1) and g + 8 (2, 3), s the pieces'.
+__device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&c)[4], const float (&f)[4], float s0,
+                                           float s1) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) acc[i] = __fmaf_rn(c[i] * f[i], i & 1 ? s1 : s0, acc[i]);
+}
 
-// Bytes of the warps' rings of ST stages.
-template <int FMT, int ST>
-struct Ring { static constexpr int bytes = kWarps * ST * (kWarpTile + ScaleBytes<FMT>::stage); };
+// The same for a few columns (rows of x times pieces), where the MMA's eight
+// columns keep apart what the scales keep apart: lane t of four takes a whole
+// block of codes (32 with one MXFP4 scale, 16 with one NVFP4 scale) into its
+// places of K, and a column of B holds x at the places of one lane only; all
+// its other elements are zeros (lanes read them from shared memory as well).
+// The sum of four blocks is then one chain of MMAs, and each lane scales four
+// sums of blocks, where stage_math scales four sums of every group: about half
+// the instructions, for MMAs that are mostly zeros.
+//   COLS == 1: column n of B is block n of eight.
+//   else     : column n of B is block n % 4 of four, for x's column n / 4; NC
+//              tiles of B for x's columns 2n and 2n + 1.
+// acc[n][i]: row g (i < 2) or g + 8. x0: x's pieces of this stage's first
+// group; zero: a place of zeros.
+template <int FMT, int ST, int COLS, int NA>
+__device__ __forceinline__ void stage_narrow(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t x0,
+                                             uint32_t x_group, uint32_t zero, uint32_t sx, uint32_t sx_group,
+                                             int lane) {
+  constexpr int kRow = ScaleBlock<FMT, ST>::row;
+  constexpr int NC = COLS <= 2 ? 1 : 2;
+  const int g = lane >> 2, t = lane & 3;
+  const bool diagonal = (g & 3) == t;
+  const uint32_t xcol = COLS == 1 ? 0 : (g >> 2) * 64;
+  float c[NC][4];
+  if constexpr (FMT == kMx) {
+    const uint2 sA = lds64(scales + g * kRow), sB = lds64(scales + (g + 8) * kRow);
+    const uint32_t v = lds32(scales + (lane >> 1) * kRow + (lane & 1) * 4);
+    const bool plain = __all_sync(kFull, ((v ^ (v << 1)) & 0x80808080u) == 0x80808080u);
+    const int shift = 16 * (t & 1);
+    // one or two sums of blocks: this lane's are group gi and gi + 1 of the stage
+    auto scale = [&](uint32_t wa, uint32_t wb, int gi) {
+      const uint32_t a2 = wa >> shift, b2 = wb >> shift;
+      if (plain) {
+        const float f[4] = {__uint_as_float((a2 << 23) & 0x7f800000u), __uint_as_float((a2 << 15) & 0x7f800000u),
+                            __uint_as_float((b2 << 23) & 0x7f800000u), __uint_as_float((b2 << 15) & 0x7f800000u)};
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint32_t at = sx + gi * sx_group + (COLS == 1 ? 0 : n * 8 + (t >> 1) * 4);
+          add_scaled(acc[n], c[n], f, __uint_as_float(lds32(at)), __uint_as_float(lds32(at + sx_group)));
+        }
+      } else {                                    // as in stage_math
+        const double f[4] = {double(pow2_dequant(a2 & 255u)), double(pow2_dequant((a2 >> 8) & 255u)),
+                             double(pow2_dequant(b2 & 255u)), double(pow2_dequant((b2 >> 8) & 255u))};
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint32_t at = sx + gi * sx_group + (COLS == 1 ? 0 : n * 8 + (t >> 1) * 4);
+          const double s0 = double(__uint_as_float(lds32(at))), s1 = double(__uint_as_float(lds32(at + sx_group)));
+#pragma unroll
+          for (int i = 0; i < 4; i++) acc[n][i] += float(double(c[n][i]) * f[i] * (i & 1 ? s1 : s0));
+        }
+      }
+    };
+#pragma unroll
+    for (int b = 0; b < 2; b++) {
+      // rows of 128 bytes; odd rows have their halves exchanged, so that two
+      // rows' 64 bytes fall on all banks
+      const uint32_t row = codes + g * 128 + ((b ^ (g & 1)) * 64) + t * 16;
+      const uint4 wA = lds128(row), wB = lds128(row + 8 * 128);
+      const bool on = diagonal && (COLS > 1 || (g >> 2) == b);
+      const uint32_t xb = on ? x0 + (4 * b + t) * x_group + xcol : zero;
+#pragma unroll
+      for (int r = 0; r < 4; r++) {
+        uint32_t hA[4], hB[4];
+        codes_f16(r == 0 ? wA.x : r == 1 ? wA.y : r == 2 ? wA.z : wA.w, hA);
+        codes_f16(r == 0 ? wB.x : r == 1 ? wB.y : r == 2 ? wB.z : wB.w, hB);
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint4 x = lds128(xb + n * 128 + r * 16);
+          if (r == 0 && (COLS > 1 || b == 0)) mma16816_first(c[n], hA[0], hB[0], hA[1], hB[1], x.x, x.y);
+          else mma16816(c[n], hA[0], hB[0], hA[1], hB[1], x.x, x.y);
+          mma16816(c[n], hA[2], hB[2], hA[3], hB[3], x.z, x.w);
+        }
+      }
+      if constexpr (COLS > 1) scale(b ? sA.y : sA.x, b ? sB.y : sB.x, 4 * b + 2 * (t & 1));
+    }
+    if constexpr (COLS == 1) scale(t < 2 ? sA.x : sA.y, t < 2 ? sB.x : sB.y, 2 * t);
+  } else {
+    const uint4 sA = lds128(scales + g * kRow), sB = lds128(scales + (g + 8) * kRow);
+    const int shift = 16 * (t & 1);
+    // this lane's two blocks are those of one group, gi of the stage
+    auto scale = [&](uint32_t wa, uint32_t wb, int gi) {
+      const float2 fA = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(wa >> shift));
+      const float2 fB = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(wb >> shift));
+      const float f[4] = {fA.x, fA.y, fB.x, fB.y};
+#pragma unroll
+      for (int n = 0; n < NC; n++) {
+        const float s = __uint_as_float(lds32(sx + gi * sx_group + (COLS == 1 ? 0 : n * 8 + (t >> 1) * 4)));
+        add_scaled(acc[n], c[n], f, s, s);
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      // 32 bytes of four rows on all banks
+      const uint32_t row = codes + g * 128 + ((q ^ (g & 3)) * 32) + t * 8;
+      const uint2 wA = lds64(row), wB = lds64(row + 8 * 128);
+      const bool on = diagonal && (COLS > 1 || (g >> 2) == (q & 1));
+      const uint32_t xb = on ? x0 + (2 * q + (t >> 1)) * x_group + (t & 1) * 32 + xcol : zero;
+#pragma unroll
+      for (int r = 0; r < 2; r++) {
+        uint32_t hA[4], hB[4];
+        codes_f16(r == 0 ? wA.x : wA.y, hA);
+        codes_f16(r == 0 ? wB.x : wB.y, hB);
+#pragma unroll
+        for (int n = 0; n < NC; n++) {
+          const uint4 x = lds128(xb + n * 128 + r * 16);
+          if (r == 0 && (COLS > 1 || q % 2 == 0)) mma16816_first(c[n], hA[0], hB[0], hA[1], hB[1], x.x, x.y);
+          else mma16816(c[n], hA[0], hB[0], hA[1], hB[1], x.x, x.y);
+          mma16816(c[n], hA[2], hB[2], hA[3], hB[3], x.z, x.w);
+        }
+      }
+      if constexpr (COLS > 1) {
+        scale(q == 0 ? sA.x : q == 1 ? sA.y : q == 2 ? sA.z : sA.w,
+              q == 0 ? sB.x : q == 1 ? sB.y : q == 2 ? sB.z : sB.w, 2 * q + (t & 1));
+      } else if (q % 2 == 1) {
+        scale(q == 1 ? (t < 2 ? sA.x : sA.y) : (t < 2 ? sA.z : sA.w),
+              q == 1 ? (t < 2 ? sB.x : sB.y) : (t < 2 ? sB.z : sB.w), 2 * (q - 1) + t);
+      }
+    }
+  }
+}
 
-template <int FMT, typename XT, int NT, bool A16, int ST>
-__global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArgs a) {
+// Bytes of the warps' rings of ST stages of codes and two blocks of scales.
+template <int FMT, int W, int ST>
+struct Ring {
+  static constexpr int warp = ST * kWarpTile + 2 * ScaleBlock<FMT, ST>::bytes;
+  static constexpr int bytes = W * warp;
+};
+
+template <int FMT, typename XT, int NT, bool A16, int W, int ST>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(const MatvecArgs a) {
+  constexpr int kTileRows = 16 * W;
+  constexpr int kRedPitch = kTileRows + 4;             // floats of one column of the sums
   constexpr int P = Pieces<XT>::n;
   constexpr uint32_t TT = 8 * NT / P;                  // rows of x in a tile
-  constexpr int kScale = ScaleBytes<FMT>::stage;
+  using Scales = ScaleBlock<FMT, ST>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t found[3 + kWarps];
+  __shared__ int64_t found[3 + W];
+  __shared__ __align__(128) uint32_t zeros[64];
   pdl_enter();
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -381,11 +600,16 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArg
   uint32_t e = 0, m = 0;
   int64_t r0 = 0;
   if (a.off) {
-    if (!find_slot(a, slot, TT, found, &e, &r0, &m)) return;   // the same for the whole cluster
+    if (!find_slot<W>(a, slot, TT, found, &e, &r0, &m)) return;   // the same for the whole cluster
   } else {
     r0 = int64_t(slot) * TT;
     m = uint32_t(min(int64_t(TT), a.M - r0));
   }
+
+  // the same for the whole cluster; rows on 8-byte boundaries are rare, and
+  // left to the general form
+  const bool narrow = A16 && m * P <= kNarrow;
+  if (tid < 64) zeros[tid] = 0;                        // read after the barriers of the first chunk
 
   // ---- this warp's 16 weight rows: consecutive, or 8 of the gate half and
   // the 8 of the up half that meet them (rows 0-7 and 8-15 of the MMA tile, so
@@ -393,170 +617,298 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArg
   const int64_t half = a.N / 2;
   const int64_t outs = a.swiglu ? half : a.N;
   const int64_t o0 = tile * (a.swiglu ? kTileRows / 2 : kTileRows);
-  const int64_t wrow0 = o0 + warp * (a.swiglu ? 8 : 16);
-  auto weight_row = [&](int r, bool& there) -> int64_t {
-    const int64_t o = wrow0 + (a.swiglu ? (r & 7) : r);
-    there = o < outs;
-    return there ? (a.swiglu && r >= 8 ? o + half : o) : 0;
-  };
   const uint8_t* const we = a.w + int64_t(e) * a.w_expert;
   const uint8_t* const se = a.s + int64_t(e) * a.s_expert;
+  // sources by 32-bit distances from the first row of the CTA (K <= 2^23 keeps
+  // them below 2^32): row r < 8 of the warp from baseA, row r + 8 from baseB
+  const int64_t second = a.swiglu ? half : 8;
+  const uint8_t* const baseA = we + o0 * a.w_pitch;
+  const uint8_t* const baseB = baseA + second * a.w_pitch;
+  const uint8_t* const scaleA = se + o0 * a.s_pitch;
+  const uint8_t* const scaleB = scaleA + second * a.s_pitch;
+  const uint32_t wrow = warp * (a.swiglu ? 8 : 16);
+  const int64_t last = outs - (o0 + wrow);                          // outputs from the warp's first on
+  const int64_t lastB = a.swiglu ? last : last - 8;                 // rows of the second eight
 
-  const uint32_t ring = smem_ptr(smem) + warp * ST * (kWarpTile + kScale);
+  const uint32_t ring = smem_ptr(smem) + warp * Ring<FMT, W, ST>::warp;
+  const uint32_t scale_ring = ring + ST * kWarpTile;
   const uint32_t s_begin = uint32_t(uint64_t(a.stages) * rank / a.split);
   const uint32_t s_end = uint32_t(uint64_t(a.stages) * (rank + 1) / a.split);
 
   // copies: 16 bytes a lane, 4 rows of 128 bytes an instruction (8 bytes and 2
-  // rows where rows start on 8-byte boundaries only)
-  constexpr int kLanes = A16 ? 8 : 16, kBytes = A16 ? 16 : 8, kStep = 32 / kLanes;
+  // rows where rows start on 8-byte boundaries only), rows 0-7 and 8-15 apart.
+  // Rows in shared memory are 144 bytes apart for stage_math; for stage_narrow
+  // 128 apart with their 64 or 32 bytes exchanged.
+  constexpr int kLanes = A16 ? 8 : 16, kBytes = A16 ? 16 : 8, kStep = 32 / kLanes, kCopies = 8 / kStep;
   const int cr = lane / kLanes, cc = (lane % kLanes) * kBytes;
-  bool there0;
-  const uint8_t* const srcA = we + weight_row(cr, there0) * a.w_pitch + cc;
-  const uint8_t* const srcB = we + weight_row(cr + 8, there0) * a.w_pitch + cc;
-  // the row of a half's copy number i is kStep i further down; it exists while
-  // its output does
-  const int64_t last = outs - wrow0;
-  // scales: 4 bytes a lane
-  constexpr int kSLanes = kScale / 64;                 // lanes of a row: 2 or 4
-  const int64_t S = a.s_pitch;
-
-  auto issue = [&](uint32_t stage) {
-    const uint32_t buf = ring + (stage % ST) * (kWarpTile + kScale);
-    const int64_t k0 = int64_t(stage) * (kStageK / 2);
-    const int64_t left = a.w_pitch - k0 - cc;
-    const uint32_t bytes = left >= kBytes ? kBytes : left > 0 ? uint32_t(left) : 0u;
+  const int flip = !narrow ? 0 : FMT == kMx ? (cr & 1) * 64 : (cr & 3) * 32;
+  const uint32_t pitch = narrow ? 128 : kRowPitch;
+  const uint32_t code_dst = ring + cr * pitch + (cc ^ flip);
+  // stages that need no check: all 16 rows there, whole
+  const uint32_t whole = last >= (a.swiglu ? 8 : 16) ? uint32_t(a.w_pitch / (kStageK / 2)) : 0;
+  uint32_t from[kCopies];                                           // of the next stage to copy
+  auto rewind = [&](uint32_t stage) {
 #pragma unroll
-    for (int i = 0; i < 8 / kStep; i++) {
-      const int r = cr + kStep * i;
-      // both halves' rows r and r + 8
-      const bool ra = r < last, rb = (a.swiglu ? r : r + 8) < last;
-      const uint32_t na = ra ? bytes : 0u, nb = rb ? bytes : 0u;
-      const uint8_t* pa = na ? srcA + i * kStep * a.w_pitch + k0 : a.w;
-      const uint8_t* pb = nb ? srcB + i * kStep * a.w_pitch + k0 : a.w;
-      const uint32_t dst = buf + r * kRowPitch + cc;
-      if constexpr (A16) {
-        cp_async16(dst, pa, na);
-        cp_async16(dst + 8 * kRowPitch, pb, nb);
-      } else {
-        cp_async8(dst, pa, na);
-        cp_async8(dst + 8 * kRowPitch, pb, nb);
+    for (int i = 0; i < kCopies; i++)
+      from[i] = (wrow + cr + kStep * i) * uint32_t(a.w_pitch) + cc + stage * (kStageK / 2);
+  };
+  auto copy_codes = [&](uint32_t stage, uint32_t slot_at) {
+    if (stage < whole) {
+#pragma unroll
+      for (int i = 0; i < kCopies; i++) {
+        const uint32_t dst = code_dst + slot_at + i * kStep * pitch;
+        if constexpr (A16) {
+          cp_async16(dst, baseA + from[i]);
+          cp_async16(dst + 8 * pitch, baseB + from[i]);
+        } else {
+          cp_async8(dst, baseA + from[i]);
+          cp_async8(dst + 8 * pitch, baseB + from[i]);
+        }
+      }
+    } else {
+      const int64_t left = a.w_pitch - int64_t(stage) * (kStageK / 2) - cc;
+      const uint32_t bytes = left >= kBytes ? kBytes : left > 0 ? uint32_t(left) : 0u;
+#pragma unroll
+      for (int i = 0; i < kCopies; i++) {
+        const int r = cr + kStep * i;
+        const uint32_t na = r < last ? bytes : 0u, nb = r < lastB ? bytes : 0u;
+        const uint32_t dst = code_dst + slot_at + i * kStep * pitch;
+        if constexpr (A16) {
+          cp_async16(dst, na ? baseA + from[i] : a.w, na);
+          cp_async16(dst + 8 * pitch, nb ? baseB + from[i] : a.w, nb);
+        } else {
+          cp_async8(dst, na ? baseA + from[i] : a.w, na);
+          cp_async8(dst + 8 * pitch, nb ? baseB + from[i] : a.w, nb);
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < kScale / 128; i++) {
-      const int idx = lane + 32 * i;
-      const int r = idx / kSLanes;
-      const int64_t c = int64_t(stage) * kSLanes * 4 + (idx % kSLanes) * 4;
-      bool there;
-      const uint8_t* p = se + weight_row(r, there) * S + c;
-      const uint32_t dst = buf + kWarpTile + idx * 4;
-      constexpr uint32_t kNone = FMT == kMx ? 0x7f7f7f7fu : 0u;     // scale 1, or block scale 0
-      if (!there || c >= S) {
-        sts32(dst, kNone);
-      } else if (a.fast_scales) {
-        cp_async4(dst, p);
-      } else {
-        uint32_t v = kNone;
+    for (int i = 0; i < kCopies; i++) from[i] += kStageK / 2;
+  };
+
+  // the scales of a block of stages, 16 bytes a lane
+  constexpr int kSLanes = Scales::row / 16;                         // lanes of a row
+  auto copy_scales = [&](uint32_t block) {
+    const uint32_t dst0 = scale_ring + (block & 1) * Scales::bytes;
 #pragma unroll
-        for (int b = 0; b < 4; b++)
-          if (c + b < S) v = (v & ~(255u << (8 * b))) | (uint32_t(p[b]) << (8 * b));
-        sts32(dst, v);
+    for (int i = 0; i < (16 * kSLanes + 31) / 32; i++) {
+      const int idx = lane + 32 * i, r = idx / kSLanes, q = (idx % kSLanes) * 16;
+      if (16 * kSLanes < 32 && r >= 16) break;
+      const bool there = (r & 7) < (r < 8 ? last : lastB);
+      const int64_t col = int64_t(block) * Scales::row + q;
+      const uint8_t* const p =
+          (r < 8 ? scaleA : scaleB) + (there ? int64_t(wrow + (r & 7)) * a.s_pitch + col : int64_t(0));
+      const uint32_t dst = dst0 + r * Scales::row + q;
+      const int64_t n = there ? a.s_pitch - col : 0;                // bytes that exist
+      if (n >= 16 && a.scale_align == 16) {
+        cp_async16(dst, p);
+        continue;
+      }
+      constexpr uint32_t kNone = FMT == kMx ? 0x7f7f7f7fu : 0u;     // scale 1, or block scale 0
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        if (n < 4 * w + 4 || a.scale_align < 4) {
+          uint32_t v = kNone;
+#pragma unroll
+          for (int b = 0; b < 4; b++)
+            if (4 * w + b < n) v = (v & ~(255u << (8 * b))) | (uint32_t(p[4 * w + b]) << (8 * b));
+          sts32(dst + 4 * w, v);
+        } else {
+          cp_async4(dst + 4 * w, p + 4 * w);
+        }
       }
     }
   };
 
   // ---- x pieces of a chunk of stages, in shared memory: [group][column][32]
   // fp16 and [group][8] scales of each n-tile
-  const uint32_t xbase = smem_ptr(smem) + Ring<FMT, ST>::bytes;
+  const uint32_t xbase = smem_ptr(smem) + Ring<FMT, W, ST>::bytes;
   const uint32_t gstride = NT == 1 ? a.colw * 64 : NT * 512;        // bytes of one group's pieces
   const uint32_t sbase = xbase + a.chunk * kStageGroups * gstride;
+  const uint32_t sstride = NT == 1 ? a.colw * 4 : NT * 32;          // bytes of one group's scales
   const XT* const x = static_cast<const XT*>(a.x);
 
+  const uint32_t ebase = sbase + a.chunk * kStageGroups * sstride;  // one word a stage: pieces with uneven scales
+
+  // A warp takes one stage of one row, 8 elements a lane; its pieces get one
+  // scale, or one for each group where that leaves something of the row.
+  // Returns whether anything is left.
   auto stage_x = [&](uint32_t first, uint32_t n, int pass) -> bool {
     bool left = false;
-    const uint32_t ng = n * kStageGroups;
-    const uint32_t tasks = m * ng * 4;
-    for (uint32_t i0 = warp * 32; i0 < tasks; i0 += kThreads) {     // tasks is a multiple of 32
-      const uint32_t i = i0 + lane;
-      const uint32_t t = i & 3, gi = (i >> 2) % ng, mi = (i >> 2) / ng;
-      const int64_t k = (int64_t(first) * kStageGroups + gi) * 32 + t * 8;
-      int64_t row = r0 + mi;
-      bool there = k < a.K;
-      if (a.order) {
-        const int32_t pair = a.order[row];
-        row = pair / a.top_k;
-        there = there && pair >= 0 && row < a.x_rows;
-      }
-      float v[8];
-      load8(x + (there ? row * a.ld_x + k : 0), there, v);
-      uint32_t h[4];
-      for (int q = 0; q < pass * P; q++) (void)take_piece<Pieces<XT>::top>(v, h);
+    const uint32_t units = m * n;
+    const uint32_t t = lane & 3, group = lane >> 2;
+    constexpr int kAhead = P == 1 ? 4 : 2;                          // units whose loads are in flight together
+    for (uint32_t u0 = warp; u0 < units; u0 += W * kAhead) {
+      In8<XT> in[kAhead];
 #pragma unroll
-      for (int p = 0; p < P; p++) {
-        const float inv = take_piece<Pieces<XT>::top>(v, h);
-        const uint32_t col = mi * P + p;
-        const uint32_t dst = xbase + gi * gstride + col * 64 + t * 16;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-                     "r"(h[3]) : "memory");
-        if (t == 0) sts32(sbase + (gi * NT + (col >> 3)) * 32 + (col & 7) * 4, __float_as_uint(inv));
+      for (int q = 0; q < kAhead; q++) {
+        const uint32_t u = u0 + q * W;
+        const uint32_t mi = u / n;
+        const int64_t k = int64_t(first + u % n) * kStageK + lane * 8;
+        int64_t row = r0 + mi;
+        bool there = u < units && k < a.K;
+        if (a.order && there) {
+          const int32_t pair = a.order[row];
+          row = pair / a.top_k;
+          there = pair >= 0 && row < a.x_rows;
+        }
+        if (there) in[q].load(x + row * a.ld_x + k); else in[q].zero();
       }
 #pragma unroll
-      for (int q = 0; q < 8; q++) left |= v[q] != 0.f;
+      for (int q = 0; q < kAhead; q++) {
+        const uint32_t u = u0 + q * W;
+        if (u >= units) break;
+        const uint32_t mi = u / n, st = u % n;
+        auto put = [&](int p, const uint32_t (&h)[4], float inv) {
+          const uint32_t col = mi * P + p, gi = st * kStageGroups + group;
+          const uint32_t dst = xbase + gi * gstride + col * 64 + t * 16;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                       "r"(h[3]) : "memory");
+          if (t == 0) sts32(sbase + gi * sstride + col * 4, __float_as_uint(inv));
+        };
+        float v[8];
+        uint32_t h[4];
+        bool rest;
+        if constexpr (P == 1) {
+          float inv;
+          rest = !whole_piece(in[q].w, h, inv);
+          if (pass > 0) h[0] = h[1] = h[2] = h[3] = 0;              // the first pass had it
+          if (!rest) put(0, h, inv);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[i] = in[q][i];
+#pragma unroll
+          for (int p = 0; p < P; p++) {
+            const float inv = take_piece<Pieces<XT>::top, true>(v, h);
+            if (pass > 0) h[0] = h[1] = h[2] = h[3] = 0;
+            put(p, h, inv);
+          }
+          rest = false;
+#pragma unroll
+          for (int i = 0; i < 8; i++) rest |= v[i] != 0.f;
+          rest = __any_sync(kFull, rest);
+        }
+        if (rest) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[i] = in[q][i];
+          for (int i = 0; i < pass * P; i++) (void)take_piece<Pieces<XT>::top, false>(v, h);
+#pragma unroll 1
+          for (int p = 0; p < P; p++) {
+            const float inv = take_piece<Pieces<XT>::top, false>(v, h);
+            put(p, h, inv);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; i++) left |= v[i] != 0.f;
+          if (lane == 0) sts32(ebase + st * 4, 1u);
+        }
+      }
     }
     return left;
   };
 
   const int g = lane >> 2, t = lane & 3;
   const uint32_t lane_x = (NT == 1 ? (min(uint32_t(g), a.colw - 1) * 4 + t) : uint32_t(lane)) * 16;
-  const uint32_t used = (m * P + 7) / 8;                            // n-tiles with columns
+  const uint32_t zero = smem_ptr(zeros) + 32;                       // 32 past a multiple of 64: not x's banks
 
-  float acc[NT][4];
+  constexpr int NA = NT < 2 ? 2 : NT;
+  float acc[NA][4];
 #pragma unroll
-  for (int n = 0; n < NT; n++)
+  for (int n = 0; n < NA; n++)
 #pragma unroll
     for (int i = 0; i < 4; i++) acc[n][i] = 0.f;
 
-  for (int pass = 0; pass < kMaxPasses; pass++) {
-    bool more = false;
+  // The CTA's share of K: one way of taking a stage, chosen once. FORM < 0:
+  // stage_narrow for -FORM columns; else stage_math for FORM n-tiles.
+  auto sweep = [&](auto form_of) {
+    constexpr int FORM = decltype(form_of)::value;
+    for (int pass = 0; pass < kMaxPasses; pass++) {
+      bool more = false;
+      rewind(s_begin);
 #pragma unroll
-    for (int i = 0; i < ST - 1; i++) {
-      if (s_begin + i < s_end) issue(s_begin + i);
-      cp_commit();
-    }
-    uint32_t c_begin = s_begin, c_end = s_begin;
-    for (uint32_t s = s_begin; s < s_end; s++) {
-      if (s == c_end) {
-        c_begin = s;
-        c_end = min(s + a.chunk, s_end);
-        __syncthreads();                                            // the last chunk has been read
-        const bool left = stage_x(c_begin, c_end - c_begin, pass);
-        more |= __syncthreads_or(left) != 0;
+      for (int i = 0; i < ST - 1; i++) {
+        if (s_begin + i < s_end) {
+          if (i == 0 || (s_begin + i) % Scales::stages == 0) copy_scales((s_begin + i) / Scales::stages);
+          copy_codes(s_begin + i, i * kWarpTile);
+        }
+        cp_commit();
       }
-      cp_wait<ST - 2>();
-      __syncwarp();                                                 // the stage is in; the one before is read
-      if (s + ST - 1 < s_end) issue(s + ST - 1);
-      cp_commit();
-      const uint32_t buf = ring + (s % ST) * (kWarpTile + kScale);
-      const uint32_t gi = (s - c_begin) * kStageGroups;
-      const uint32_t xf = xbase + gi * gstride + lane_x, sx = sbase + gi * NT * 32 + t * 8;
-      if (NT > 1 && used == 1)
-        stage_math<FMT, 1, NT>(acc, buf, buf + kWarpTile, xf, gstride, sx, lane);
-      else if (NT > 2 && used == 2)
-        stage_math<FMT, (NT > 2 ? 2 : NT), NT>(acc, buf, buf + kWarpTile, xf, gstride, sx, lane);
-      else
-        stage_math<FMT, NT, NT>(acc, buf, buf + kWarpTile, xf, gstride, sx, lane);
+      uint32_t c_begin = s_begin, c_end = s_begin;
+      uint32_t read = 0, fill = (ST - 1) * kWarpTile;               // slots of the ring
+      uint32_t xg = xbase, sg = sbase;
+      for (uint32_t s = s_begin; s < s_end; s++) {
+        if (s == c_end) {
+          c_begin = s;
+          c_end = min(s + a.chunk, s_end);
+          xg = xbase;
+          sg = sbase;
+          __syncthreads();                                          // the last chunk has been read
+          if (uint32_t(tid) < c_end - c_begin) sts32(ebase + tid * 4, 0u);
+          __syncthreads();
+          const bool left = stage_x(c_begin, c_end - c_begin, pass);
+          more |= __syncthreads_or(left) != 0;
+        }
+        cp_wait<ST - 2>();
+        __syncwarp();                                               // the stage is in; the one before is read
+        const uint32_t ahead = s + ST - 1;
+        if (ahead < s_end) {
+          if (ahead % Scales::stages == 0) copy_scales(ahead / Scales::stages);
+          copy_codes(ahead, fill);
+        }
+        cp_commit();
+        const uint32_t codes = ring + read;
+        const uint32_t scales =
+            scale_ring + (s / Scales::stages & 1) * Scales::bytes + s % Scales::stages * Scales::stage;
+        if constexpr (FORM < 0)
+          stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, lane);
+        else
+          stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride,
+                                        lds32(ebase + (s - c_begin) * 4) == 0, lane);
+        xg += kStageGroups * gstride;
+        sg += kStageGroups * sstride;
+        read = read == (ST - 1) * kWarpTile ? 0 : read + kWarpTile;
+        fill = fill == (ST - 1) * kWarpTile ? 0 : fill + kWarpTile;
+      }
+      if (!more) break;
+      __syncthreads();
     }
-    if (!more) break;
-    __syncthreads();
+  };
+  const uint32_t cols = m * P, used = (cols + 7) / 8;               // n-tiles with columns
+  if (narrow) {
+    if (cols == 1) sweep(std::integral_constant<int, -1>{});
+    else if (cols == 2) sweep(std::integral_constant<int, -2>{});
+    else sweep(std::integral_constant<int, -4>{});
+  } else if (NT == 1 || used == 1) {
+    sweep(std::integral_constant<int, 1>{});
+  } else if (NT == 2 || used == 2) {
+    sweep(std::integral_constant<int, NT < 2 ? 1 : 2>{});
+  } else {
+    sweep(std::integral_constant<int, NT>{});
   }
 
   // ---- sums of the cluster's shares, in rank order
   cp_wait<0>();
   __syncthreads();                                                  // the rings are free
   float* const red = reinterpret_cast<float*>(smem);
+  if (narrow) {
+#pragma unroll
+    for (int n = 0; n < 2; n++) {
+      float lo = acc[n][0] + acc[n][1], hi = acc[n][2] + acc[n][3];   // rows g and g + 8
+      lo += __shfl_xor_sync(kFull, lo, 1);
+      hi += __shfl_xor_sync(kFull, hi, 1);
+      if (cols == 1) {
+        lo += __shfl_xor_sync(kFull, lo, 2);
+        hi += __shfl_xor_sync(kFull, hi, 2);
+      }
+      const uint32_t col = 2 * n + (t >> 1);
+      if ((t & 1) == 0 && col < cols) {
+        red[col * kRedPitch + warp * 16 + g] = lo;
+        red[col * kRedPitch + warp * 16 + g + 8] = hi;
+      }
+    }
+  }
 #pragma unroll
   for (int n = 0; n < NT; n++) {
-    if (uint32_t(n) < used) {
+    if (!narrow && uint32_t(n) < used) {
       float* const c0 = red + (n * 8 + 2 * t) * kRedPitch + warp * 16 + g;
       c0[0] = acc[n][0];
       c0[kRedPitch] = acc[n][1];
@@ -577,12 +929,16 @@ __global__ void __launch_bounds__(kThreads, 2) fp4_matvec_kernel(const MatvecArg
       if (a.split == 1) {
         v += red[at / 4];
       } else {
-        for (uint32_t q = 0; q < a.split; q++) v += cluster_ld(cluster_map(red_addr + at, q));
+        float part[8];                                              // all on their way at once
+#pragma unroll
+        for (uint32_t q = 0; q < 8; q++) part[q] = q < a.split ? cluster_ld(cluster_map(red_addr + at, q)) : 0.f;
+#pragma unroll
+        for (uint32_t q = 0; q < 8; q++) v += part[q];
       }
     }
     return v;
   };
-  for (uint32_t i = tid; i < m * len; i += kThreads) {
+  for (uint32_t i = tid; i < m * len; i += 32 * W) {
     const uint32_t mi = i / len, o = lo + i % len;
     if (o0 + o >= outs) continue;
     float gA = 1.f, gB = 1.f;
@@ -657,17 +1013,17 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const float* __re
 
 // ------------------------------------------------------------------ host
 
-constexpr uint32_t kPieceBytes = 30 << 10;       // shared memory for x pieces
 
 // How K is shared out: the split whose busiest multiprocessor has least to do,
-// counting a CTA's fixed work (its x pieces, the exchange of the sums) as two
-// stages.
-uint32_t choose_split(uint64_t units, uint32_t stages) {
+// counting the fixed work of a round of resident CTAs (x pieces, the exchange
+// of the sums) as three stages.
+uint32_t choose_split(uint64_t units, uint32_t stages, uint64_t resident) {
   const uint64_t sms = uint64_t(sm_count());
   uint32_t best = 1;
   uint64_t best_cost = ~0ull;
   for (uint32_t c = 1; c <= 8 && (c == 1 || c <= stages); c++) {
-    const uint64_t cost = (units * c + sms - 1) / sms * ((stages + c - 1) / c + 2);
+    const uint64_t per_sm = (units * c + sms - 1) / sms;
+    const uint64_t cost = per_sm * ((stages + c - 1) / c) + 3 * ((per_sm + resident - 1) / resident);
     if (cost < best_cost) {
       best_cost = cost;
       best = c;
@@ -678,10 +1034,13 @@ uint32_t choose_split(uint64_t units, uint32_t stages) {
 
 template <int FMT, typename XT, int NT, bool A16>
 mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
-  constexpr int ST = NT == 4 ? 3 : 4;
+  // one n-tile: three CTAs of 8 warps a multiprocessor (74 KB each); more: one
+  // of 16, whose 256 rows share the x pieces
+  constexpr int W = NT == 1 ? 8 : 16, ST = NT == 1 ? 3 : 4;
+  constexpr uint32_t kPieces = (NT == 1 ? 73u << 10 : 225u << 10) - Ring<FMT, W, ST>::bytes;   // for x pieces
   constexpr uint32_t P = Pieces<XT>::n;
   constexpr uint32_t TT = 8 * NT / P;
-  const uint64_t tile_rows = a.swiglu ? kTileRows / 2 : kTileRows;
+  const uint64_t tile_rows = a.swiglu ? 8 * W : 16 * W;
   const uint64_t tiles = (uint64_t(a.swiglu ? a.N / 2 : a.N) + tile_rows - 1) / tile_rows;
   uint64_t slots, likely;
   if (a.off) {
@@ -692,17 +1051,19 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   } else {
     slots = likely = (uint64_t(a.M) + TT - 1) / TT;
   }
-  a.split = choose_split(likely * tiles, a.stages);
+  a.split = choose_split(likely * tiles, a.stages, NT == 1 ? 3 : 1);
   if (slots * tiles * a.split > 0x7fffffffull) return MXQ_ERR_SHAPE;
   a.slots = uint32_t(slots);
-  a.colw = NT == 1 ? uint32_t(std::min<uint64_t>(8, std::min<uint64_t>(TT, uint64_t(a.M)) * P)) : 8;
-  const uint32_t per_stage = kStageGroups * NT * (a.colw * 64 + 32);
+  // columns in shared memory: up to four, or all eight of an n-tile
+  const uint64_t most = std::min<uint64_t>(TT, uint64_t(a.M)) * P;
+  a.colw = NT == 1 && most <= kNarrow && A16 ? uint32_t(most) : 8;
+  const uint32_t per_stage = kStageGroups * NT * a.colw * (64 + 4) + 4;
   const uint32_t share = (a.stages + a.split - 1) / a.split;
-  a.chunk = std::max(1u, std::min(share, kPieceBytes / per_stage));
-  const size_t smem = size_t(Ring<FMT, ST>::bytes) + size_t(a.chunk) * per_stage;
+  a.chunk = std::max(1u, std::min(share, kPieces / per_stage));
+  const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + size_t(a.chunk) * per_stage;
 
-  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, ST>;
-  constexpr int kMostSmem = Ring<FMT, ST>::bytes + int(kPieceBytes);
+  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W, ST>;
+  constexpr int kMostSmem = Ring<FMT, W, ST>::bytes + int(kPieces);
   const cudaError_t attr_err = ensure_smem_limit<kernel>(kMostSmem);
   if (attr_err != cudaSuccess) {
     record_cuda_error(attr_err);
@@ -710,7 +1071,7 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t(slots * tiles) * a.split);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -759,7 +1120,7 @@ struct Call {
   int out_dt;
 };
 
-constexpr int64_t kMostRows = 0x7fffffff;
+constexpr int64_t kMostRows = 0x7fffffff, kMostK = 1 << 23;
 
 // The checks that one weight and the experts' weights share; MXQ_OK with
 // *done set when there is nothing to do.
@@ -769,7 +1130,7 @@ mxq_status check_call(const Call& c, int64_t M, int64_t E, bool* done) {
   *done = false;
   if (!valid_dtype(c.dt) || !valid_dtype(c.out_dt)) return MXQ_ERR_DTYPE;
   if (M < 0 || c.x_rows < 0 || c.N < 0 || c.K < 0 || c.K % kBlock != 0 || c.ld_x < c.K) return MXQ_ERR_SHAPE;
-  if (M > kMostRows || c.x_rows > kMostRows || c.N > kMostRows || c.K > kMostRows) return MXQ_ERR_SHAPE;
+  if (M > kMostRows || c.x_rows > kMostRows || c.N > kMostRows || c.K > kMostK) return MXQ_ERR_SHAPE;
   if (M == 0 || c.N == 0) {
     *done = true;
     return MXQ_OK;
@@ -805,7 +1166,8 @@ MatvecArgs make_args(const Call& c, int64_t M) {
   a.g_per = 1;
   a.stages = uint32_t((c.K + kStageK - 1) / kStageK);
   a.out_bf16 = c.out_dt == MXQ_BF16;
-  a.fast_scales = a.s_pitch % 4 == 0 && (reinterpret_cast<uintptr_t>(c.scale) & 3u) == 0;
+  const uintptr_t low = uintptr_t(a.s_pitch) | reinterpret_cast<uintptr_t>(c.scale);
+  a.scale_align = low % 16 == 0 ? 16 : low % 4 == 0 ? 4 : 1;
   return a;
 }
 
