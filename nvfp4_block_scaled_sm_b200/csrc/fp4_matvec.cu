@@ -580,6 +580,44 @@ struct Ring {
   static constexpr int bytes = W * warp;
 };
 
+// The copies of a stage whose rows or columns are not all there, kept out of
+// the loop's code: `bytes` of each row that exists, zeros for the rest.
+template <bool A16, int COPIES>
+__device__ __noinline__ void copy_codes_edge(uint32_t dst, uint32_t step, uint32_t second, const uint8_t* pa,
+                                             const uint8_t* pb, int64_t row_step, int rows_a, int rows_b,
+                                             uint32_t bytes, const uint8_t* any) {
+#pragma unroll 1
+  for (int i = 0; i < COPIES; i++) {
+    const uint32_t na = i < rows_a ? bytes : 0u, nb = i < rows_b ? bytes : 0u;
+    if constexpr (A16) {
+      cp_async16(dst, na ? pa : any, na);
+      cp_async16(dst + second, nb ? pb : any, nb);
+    } else {
+      cp_async8(dst, na ? pa : any, na);
+      cp_async8(dst + second, nb ? pb : any, nb);
+    }
+    dst += step;
+    pa += row_step;
+    pb += row_step;
+  }
+}
+
+// 16 bytes of scales of which n exist (none if n <= 0), at a source on a
+// boundary of `align` bytes; the rest is `none`.
+__device__ __noinline__ void copy_scales_edge(uint32_t dst, const uint8_t* p, int n, uint32_t align, uint32_t none) {
+#pragma unroll 1
+  for (int w = 0; w < 4; w++) {
+    if (n >= 4 * w + 4 && align >= 4) {
+      cp_async4(dst + 4 * w, p + 4 * w);
+    } else {
+      uint32_t v = none;
+      for (int b = 0; b < 4; b++)
+        if (4 * w + b < n) v = (v & ~(255u << (8 * b))) | (uint32_t(p[4 * w + b]) << (8 * b));
+      sts32(dst + 4 * w, v);
+    }
+  }
+}
+
 template <int FMT, typename XT, int NT, bool A16, int W, int ST>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(const MatvecArgs a) {
   constexpr int kTileRows = 16 * W;
@@ -644,14 +682,11 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
   const int flip = !narrow ? 0 : FMT == kMx ? (cr & 1) * 64 : (cr & 3) * 32;
   const uint32_t pitch = narrow ? 128 : kRowPitch;
   const uint32_t code_dst = ring + cr * pitch + (cc ^ flip);
-  // stages that need no check: all 16 rows there, whole
-  const uint32_t whole = last >= (a.swiglu ? 8 : 16) ? uint32_t(a.w_pitch / (kStageK / 2)) : 0;
+  // stages and blocks of scales that need no check: all 16 rows there, whole
+  const bool all_rows = last >= (a.swiglu ? 8 : 16);
+  const uint32_t whole = all_rows ? uint32_t(a.w_pitch / (kStageK / 2)) : 0;
+  const uint32_t whole_scales = all_rows && a.scale_align == 16 ? uint32_t(a.s_pitch / Scales::row) : 0;
   uint32_t from[kCopies];                                           // of the next stage to copy
-  auto rewind = [&](uint32_t stage) {
-#pragma unroll
-    for (int i = 0; i < kCopies; i++)
-      from[i] = (wrow + cr + kStep * i) * uint32_t(a.w_pitch) + cc + stage * (kStageK / 2);
-  };
   auto copy_codes = [&](uint32_t stage, uint32_t slot_at) {
     if (stage < whole) {
 #pragma unroll
@@ -667,20 +702,11 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
       }
     } else {
       const int64_t left = a.w_pitch - int64_t(stage) * (kStageK / 2) - cc;
-      const uint32_t bytes = left >= kBytes ? kBytes : left > 0 ? uint32_t(left) : 0u;
-#pragma unroll
-      for (int i = 0; i < kCopies; i++) {
-        const int r = cr + kStep * i;
-        const uint32_t na = r < last ? bytes : 0u, nb = r < lastB ? bytes : 0u;
-        const uint32_t dst = code_dst + slot_at + i * kStep * pitch;
-        if constexpr (A16) {
-          cp_async16(dst, na ? baseA + from[i] : a.w, na);
-          cp_async16(dst + 8 * pitch, nb ? baseB + from[i] : a.w, nb);
-        } else {
-          cp_async8(dst, na ? baseA + from[i] : a.w, na);
-          cp_async8(dst + 8 * pitch, nb ? baseB + from[i] : a.w, nb);
-        }
-      }
+      const int rows_a = last <= cr ? 0 : int(min((last - cr + kStep - 1) / kStep, int64_t(kCopies)));
+      const int rows_b = lastB <= cr ? 0 : int(min((lastB - cr + kStep - 1) / kStep, int64_t(kCopies)));
+      copy_codes_edge<A16, kCopies>(code_dst + slot_at, kStep * pitch, 8 * pitch, baseA + from[0],
+                                    baseB + from[0], kStep * a.w_pitch, rows_a, rows_b,
+                                    left >= kBytes ? kBytes : left > 0 ? uint32_t(left) : 0u, a.w);
     }
 #pragma unroll
     for (int i = 0; i < kCopies; i++) from[i] += kStageK / 2;
@@ -688,35 +714,36 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
 
   // the scales of a block of stages, 16 bytes a lane
   constexpr int kSLanes = Scales::row / 16;                         // lanes of a row
+  constexpr int kSCopies = (16 * kSLanes + 31) / 32;
+  uint32_t sfrom[kSCopies];                                         // of the next block to copy
   auto copy_scales = [&](uint32_t block) {
-    const uint32_t dst0 = scale_ring + (block & 1) * Scales::bytes;
 #pragma unroll
-    for (int i = 0; i < (16 * kSLanes + 31) / 32; i++) {
-      const int idx = lane + 32 * i, r = idx / kSLanes, q = (idx % kSLanes) * 16;
-      if (16 * kSLanes < 32 && r >= 16) break;
-      const bool there = (r & 7) < (r < 8 ? last : lastB);
-      const int64_t col = int64_t(block) * Scales::row + q;
-      const uint8_t* const p =
-          (r < 8 ? scaleA : scaleB) + (there ? int64_t(wrow + (r & 7)) * a.s_pitch + col : int64_t(0));
-      const uint32_t dst = dst0 + r * Scales::row + q;
-      const int64_t n = there ? a.s_pitch - col : 0;                // bytes that exist
-      if (n >= 16 && a.scale_align == 16) {
-        cp_async16(dst, p);
-        continue;
-      }
-      constexpr uint32_t kNone = FMT == kMx ? 0x7f7f7f7fu : 0u;     // scale 1, or block scale 0
-#pragma unroll
-      for (int w = 0; w < 4; w++) {
-        if (n < 4 * w + 4 || a.scale_align < 4) {
-          uint32_t v = kNone;
-#pragma unroll
-          for (int b = 0; b < 4; b++)
-            if (4 * w + b < n) v = (v & ~(255u << (8 * b))) | (uint32_t(p[4 * w + b]) << (8 * b));
-          sts32(dst + 4 * w, v);
+    for (int i = 0; i < kSCopies; i++) {
+      const int idx = lane + 32 * i, r = idx / kSLanes;
+      if (16 * kSLanes >= 32 || lane < 16) {
+        const uint32_t dst = scale_ring + (block & 1) * Scales::bytes + idx * 16;
+        const uint8_t* const p = (r < 8 ? scaleA : scaleB) + sfrom[i];
+        if (block < whole_scales) {
+          cp_async16(dst, p);
         } else {
-          cp_async4(dst + 4 * w, p + 4 * w);
+          const bool there = (r & 7) < (r < 8 ? last : lastB);
+          const int64_t n = there ? a.s_pitch - (int64_t(block) * Scales::row + (idx % kSLanes) * 16) : 0;
+          copy_scales_edge(dst, p, int(min(max(n, int64_t(0)), int64_t(16))), a.scale_align,
+                           FMT == kMx ? 0x7f7f7f7fu : 0u);          // scale 1, or block scale 0
         }
       }
+      sfrom[i] += Scales::row;
+    }
+  };
+  auto rewind = [&](uint32_t stage) {
+#pragma unroll
+    for (int i = 0; i < kCopies; i++)
+      from[i] = (wrow + cr + kStep * i) * uint32_t(a.w_pitch) + cc + stage * (kStageK / 2);
+#pragma unroll
+    for (int i = 0; i < kSCopies; i++) {
+      const int idx = lane + 32 * i;
+      sfrom[i] = (wrow + (idx / kSLanes & 7)) * uint32_t(a.s_pitch) + idx % kSLanes * 16 +
+                 stage / Scales::stages * Scales::row;
     }
   };
 
@@ -735,18 +762,26 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
   // Returns whether anything is left.
   auto stage_x = [&](uint32_t first, uint32_t n, int pass) -> bool {
     bool left = false;
-    const uint32_t units = m * n;
     const uint32_t t = lane & 3, group = lane >> 2;
     constexpr int kAhead = P == 1 ? 4 : 2;                          // units whose loads are in flight together
-    for (uint32_t u0 = warp; u0 < units; u0 += W * kAhead) {
+    uint32_t mi0 = warp / n, st0 = warp % n;                        // row and stage; the next unit is W stages on
+    while (mi0 < m) {
       In8<XT> in[kAhead];
+      uint32_t mis[kAhead], sts[kAhead];
 #pragma unroll
       for (int q = 0; q < kAhead; q++) {
-        const uint32_t u = u0 + q * W;
-        const uint32_t mi = u / n;
-        const int64_t k = int64_t(first + u % n) * kStageK + lane * 8;
+        mis[q] = mi0;
+        sts[q] = st0;
+        st0 += W;
+        while (st0 >= n) {
+          st0 -= n;
+          mi0++;
+        }
+        const uint32_t mi = mis[q];
+        if (mi >= m) continue;
+        const int64_t k = int64_t(first + sts[q]) * kStageK + lane * 8;
         int64_t row = r0 + mi;
-        bool there = u < units && k < a.K;
+        bool there = k < a.K;
         if (a.order && there) {
           const int32_t pair = a.order[row];
           row = pair / a.top_k;
@@ -756,9 +791,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
       }
 #pragma unroll
       for (int q = 0; q < kAhead; q++) {
-        const uint32_t u = u0 + q * W;
-        if (u >= units) break;
-        const uint32_t mi = u / n, st = u % n;
+        const uint32_t mi = mis[q], st = sts[q];
+        if (mi >= m) break;
         auto put = [&](int p, const uint32_t (&h)[4], float inv) {
           const uint32_t col = mi * P + p, gi = st * kStageGroups + group;
           const uint32_t dst = xbase + gi * gstride + col * 64 + t * 16;
@@ -832,41 +866,38 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
         }
         cp_commit();
       }
-      uint32_t c_begin = s_begin, c_end = s_begin;
       uint32_t read = 0, fill = (ST - 1) * kWarpTile;               // slots of the ring
-      uint32_t xg = xbase, sg = sbase;
-      for (uint32_t s = s_begin; s < s_end; s++) {
-        if (s == c_end) {
-          c_begin = s;
-          c_end = min(s + a.chunk, s_end);
-          xg = xbase;
-          sg = sbase;
-          __syncthreads();                                          // the last chunk has been read
-          if (uint32_t(tid) < c_end - c_begin) sts32(ebase + tid * 4, 0u);
-          __syncthreads();
-          const bool left = stage_x(c_begin, c_end - c_begin, pass);
-          more |= __syncthreads_or(left) != 0;
+      for (uint32_t c_begin = s_begin; c_begin < s_end; c_begin += a.chunk) {
+        const uint32_t n = min(a.chunk, s_end - c_begin);
+        __syncthreads();                                            // the last chunk has been read
+        if (uint32_t(tid) < n) sts32(ebase + tid * 4, 0u);
+        __syncthreads();
+        const bool left = stage_x(c_begin, n, pass);
+        more |= __syncthreads_or(left) != 0;
+        uint32_t xg = xbase, sg = sbase;
+#pragma unroll 1
+        for (uint32_t s = c_begin; s < c_begin + n; s++) {
+          cp_wait<ST - 2>();
+          __syncwarp();                                             // the stage is in; the one before is read
+          const uint32_t ahead = s + ST - 1;
+          if (ahead < s_end) {
+            if (ahead % Scales::stages == 0) copy_scales(ahead / Scales::stages);
+            copy_codes(ahead, fill);
+          }
+          cp_commit();
+          const uint32_t codes = ring + read;
+          const uint32_t scales =
+              scale_ring + (s / Scales::stages & 1) * Scales::bytes + s % Scales::stages * Scales::stage;
+          if constexpr (FORM < 0)
+            stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, lane);
+          else
+            stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride,
+                                          lds32(ebase + (s - c_begin) * 4) == 0, lane);
+          xg += kStageGroups * gstride;
+          sg += kStageGroups * sstride;
+          read = read == (ST - 1) * kWarpTile ? 0 : read + kWarpTile;
+          fill = fill == (ST - 1) * kWarpTile ? 0 : fill + kWarpTile;
         }
-        cp_wait<ST - 2>();
-        __syncwarp();                                               // the stage is in; the one before is read
-        const uint32_t ahead = s + ST - 1;
-        if (ahead < s_end) {
-          if (ahead % Scales::stages == 0) copy_scales(ahead / Scales::stages);
-          copy_codes(ahead, fill);
-        }
-        cp_commit();
-        const uint32_t codes = ring + read;
-        const uint32_t scales =
-            scale_ring + (s / Scales::stages & 1) * Scales::bytes + s % Scales::stages * Scales::stage;
-        if constexpr (FORM < 0)
-          stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, lane);
-        else
-          stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride,
-                                        lds32(ebase + (s - c_begin) * 4) == 0, lane);
-        xg += kStageGroups * gstride;
-        sg += kStageGroups * sstride;
-        read = read == (ST - 1) * kWarpTile ? 0 : read + kWarpTile;
-        fill = fill == (ST - 1) * kWarpTile ? 0 : fill + kWarpTile;
       }
       if (!more) break;
       __syncthreads();
