@@ -447,10 +447,17 @@ mxq_status moe_route_backward(const float* grad_weights, const void* logits, int
  *               pairs the places from row_offsets[E] on.
  *  order        device int32 [P]: the pair at each place.
  *  positions    device int32 [P]: the place of each pair, -1 if dropped.
+ *  workspace    device, 4-byte aligned, >= mxq_moe_dispatch_workspace_bytes(P,
+ *               E); may be NULL where that is 0 (P <= 4096).
  * P == 0 writes row_offsets (zeros) only. 1 <= E <= MXQ_GROUPED_MAX_EXPERTS.
- * One launch of one cluster. */
+ * One launch, or two where a workspace is needed. */
 mxq_status moe_dispatch(const int32_t* experts, int64_t P, int32_t E, int64_t* row_offsets,
-                        int32_t* order, int32_t* positions, mxq_stream_t stream);
+                        int32_t* order, int32_t* positions, void* workspace, size_t ws_bytes,
+                        mxq_stream_t stream);
+
+/* Workspace bytes of moe_dispatch (counts of each chunk of pairs): 0 for up to
+ * 4096 pairs, and for sizes that it rejects. */
+size_t mxq_moe_dispatch_workspace_bytes(int64_t P, int32_t E);
 
 /* Self-check of the bounded barrier wait that lets mxfp8_gemm give up
  * instead of hanging (the wait behind error_flag), run on the device in one

@@ -99,7 +99,9 @@ def _load() -> ctypes.CDLL:
     L.moe_combine.argtypes = [vp, i64, i64, vp, vp, i64, i32, vp, i32, vp]
     L.moe_route.argtypes = [vp, i32, i64, i32, i64, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp]
     L.moe_route_backward.argtypes = [vp, vp, i32, i64, i32, i64, vp, i32, i32, i32, f32, vp, vp]
-    L.moe_dispatch.argtypes = [vp, i64, i32, vp, vp, vp, vp]
+    L.moe_dispatch.argtypes = [vp, i64, i32, vp, vp, vp, vp, sz, vp]
+    L.mxq_moe_dispatch_workspace_bytes.argtypes = [i64, i32]
+    L.mxq_moe_dispatch_workspace_bytes.restype = sz
     for f in ("mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
               "moe_combine", "moe_route", "moe_route_backward", "moe_dispatch",
               "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped",
@@ -115,6 +117,17 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+class _Functions(dict):
+    """The library's functions by name, looked up once."""
+
+    def __missing__(self, name: str):
+        f = self[name] = getattr(lib, name)
+        return f
+
+
+_fn = _Functions()
 
 
 def _check(fn: str, status: int):
@@ -139,17 +152,27 @@ def _require_cuda(*ts: torch.Tensor):
             raise ValueError("tensors must live on a CUDA device (no CPU path exists)")
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream      # current_stream() without the object around it
+
+
 def _stream(t: torch.Tensor) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(t.device.index))
 
 
 def _rows_view(x: torch.Tensor):
     """(M, N, ld_x) of x seen as M rows of N contiguous elements with row
     stride ld_x; raises if the leading dims do not collapse to one stride."""
-    if x.dim() == 0:
+    dims = x.dim()
+    if dims == 0:
         raise ValueError("expected at least one dimension")
+    if dims == 2:
+        M, N = x.shape
+        ld, step = x.stride()
+        if N > 1 and step != 1:
+            raise ValueError("the last dimension must be contiguous")
+        return M, N, ld if M > 1 else N
     N = x.shape[-1]
-    if x.dim() == 1:
+    if dims == 1:
         return 1, N, N
     if N > 1 and x.stride(-1) != 1:
         raise ValueError("the last dimension must be contiguous")
@@ -186,9 +209,9 @@ def set_output_allocator(fn):
 
 
 def _empty(shape, dtype: torch.dtype, device) -> torch.Tensor:
-    shape = (int(shape),) if isinstance(shape, int) else tuple(int(d) for d in shape)
     if _output_allocator is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    shape = (int(shape),) if isinstance(shape, int) else tuple(int(d) for d in shape)
     t = _output_allocator(shape, dtype, device)
     if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
         raise RuntimeError("the output allocator returned a tensor of the wrong layout")
@@ -473,36 +496,38 @@ def mxfp8_gemm(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Tensor,
 def _launch(fn: str, dev: torch.device, *args):
     """Calls ``fn`` with the stream of ``dev`` that is current, on that device
     (tensors may live on another device than the current one)."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        status = getattr(lib, fn)(*args, stream)
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        status = _fn[fn](*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib, fn)(*args, stream)
+            status = _fn[fn](*args, _raw_stream(index))
     if status:
         _check(fn, status)
 
 
-def _same_device(x: torch.Tensor, *ts: torch.Tensor):
+def _same_device(x: torch.Tensor, *ts: torch.Tensor) -> torch.device:
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("tensors must live on a CUDA device (no CPU path exists)")
     for t in ts:
         if t.device != dev:
             raise ValueError("tensors must live on one CUDA device")
+    return dev
 
 
 def _weight_args(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, block: int, dims: int):
     """(N, K) of a 4-bit weight [N, K/2] (or a stack [E, N, K/2]) that
     multiplies rows x [..., K]."""
-    if packed.dtype != torch.uint8 or scale.dtype != torch.uint8:
+    if packed.dtype is not torch.uint8 or scale.dtype is not torch.uint8:
         raise TypeError("codes and scales must be uint8")
     if not (packed.is_contiguous() and scale.is_contiguous()):
         raise ValueError("codes and scales must be contiguous")
-    if packed.dim() != dims or scale.dim() != dims:
+    shape, sshape = packed.shape, scale.shape
+    if len(shape) != dims or len(sshape) != dims:
         raise ValueError(f"expected {dims}-D codes and scales")
-    N, K = packed.shape[-2], packed.shape[-1] * 2
-    if K % block or scale.shape != (*packed.shape[:-1], K // block):
+    N, K = shape[-2], shape[-1] * 2
+    if K % block or sshape[-1] * block != K or sshape[:-1] != shape[:-1]:
         raise ValueError("scale does not match the codes")
     if x.dim() == 0 or x.shape[-1] != K:
         raise ValueError(f"expected rows of {K} elements")
@@ -510,19 +535,21 @@ def _weight_args(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, blo
 
 
 def _matvec(fn: str, x, packed, scale, global_scale, dtype, block: int) -> torch.Tensor:
-    _same_device(x, packed, scale)
+    dev = _same_device(x, packed, scale)
     N, K = _weight_args(x, packed, scale, block, 2)
     dt, out_dt = _dtype_code(x.dtype), _dtype_code(dtype)
     M, _, ld = _rows_view(x)
-    g = ()
-    if global_scale is not None:
-        if global_scale.dtype != torch.float32 or global_scale.numel() != 1:
-            raise TypeError("global_scale must be a single fp32 value")
-        global_scale = global_scale.to(x.device)
-        g = (global_scale.data_ptr(),)
-    y = _empty((*x.shape[:-1], N), dtype, x.device)
-    _launch(fn, x.device, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(), *g, N,
-            y.data_ptr(), out_dt)
+    y = _empty((*x.shape[:-1], N), dtype, dev)
+    if global_scale is None:
+        _launch(fn, dev, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(), N, y.data_ptr(),
+                out_dt)
+        return y
+    if global_scale.dtype is not torch.float32 or global_scale.numel() != 1:
+        raise TypeError("global_scale must be a single fp32 value")
+    if global_scale.device != dev:
+        global_scale = global_scale.to(dev)
+    _launch(fn, dev, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(),
+            global_scale.data_ptr(), N, y.data_ptr(), out_dt)
     return y
 
 
@@ -571,8 +598,7 @@ def _int32(t: torch.Tensor, dev, what: str) -> torch.Tensor:
 
 def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k, swiglu, combine,
                     dtype, block: int) -> torch.Tensor:
-    _same_device(x, packed, scale)
-    dev = x.device
+    dev = _same_device(x, packed, scale)
     N, K = _weight_args(x, packed, scale, block, 3)
     E = packed.shape[0]
     if x.dim() != 2:
@@ -760,8 +786,10 @@ def moe_dispatch(experts: torch.Tensor, E: int):
     row_offsets = _empty(max(E, 0) + 1, torch.int64, dev)
     order = _empty(P, torch.int32, dev)
     positions = _empty(experts.shape, torch.int32, dev)
+    need = _fn["mxq_moe_dispatch_workspace_bytes"](P, E)
+    ws = _empty(need, torch.uint8, dev) if need else None
     _launch("moe_dispatch", dev, experts.data_ptr(), P, E, row_offsets.data_ptr(), order.data_ptr(),
-            positions.data_ptr())
+            positions.data_ptr(), None if ws is None else ws.data_ptr(), need)
     return row_offsets, order, positions
 
 

@@ -473,12 +473,17 @@ inline cudaError_t ensure_smem_limit(int bytes) {
   return e;
 }
 
-// Multiprocessors of the current device (148 on B200 if the query fails).
+// Multiprocessors of the current device (148 on B200 if the query fails),
+// asked for once per device.
 inline int sm_count() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 148;
+  static std::atomic<int> known[256];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  const bool slot = dev >= 0 && dev < 256;
+  if (slot && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (slot) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 // ----------------------------------------------------------- block reduce

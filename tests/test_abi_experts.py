@@ -124,7 +124,7 @@ def test_route_backward():
 
 def test_dispatch():
     f = mxq.lib.moe_dispatch
-    base = dict(e=A, P=10, E=4, off=A, order=A, pos=A, stream=None)
+    base = dict(e=A, P=10, E=4, off=A, order=A, pos=A, ws=None, n=0, stream=None)
     assert f(*edit(base)) == CUDA
     for n, v in (("P", -1), ("P", 1 << 31), ("E", 0), ("E", 1025)):
         assert f(*edit(base, **{n: v})) == SHAPE
@@ -133,6 +133,15 @@ def test_dispatch():
     for p, d in (("e", 2), ("off", 4), ("order", 1), ("pos", 2)):
         assert f(*edit(base, **{p: A + d})) == ALIGN
     assert f(*edit(base, P=0, e=None, order=None, pos=None)) == CUDA      # row_offsets are written
+    need = mxq.lib.mxq_moe_dispatch_workspace_bytes
+    assert need(4096, 64) == 0 and need(-1, 4) == 0 and need(9999, 0) == 0
+    assert need(4097, 64) == 2 * 65 * 4 and need(131072, 256) == 32 * 257 * 4
+    assert need(2 ** 31 - 1, 1024) <= 128 * 1025 * 4
+    big = dict(base, P=5000, ws=A, n=need(5000, 4))
+    assert f(*edit(big)) == CUDA
+    assert f(*edit(big, ws=None)) == WORKSPACE
+    assert f(*edit(big, n=big["n"] - 1)) == WORKSPACE
+    assert f(*edit(big, ws=A + 2)) == ALIGN
 
 
 def test_python_refuses_host_tensors():

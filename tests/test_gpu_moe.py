@@ -268,7 +268,7 @@ def check_dispatch(ids, E):
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (5, 2, 3), (31, 1, 7), (33, 3, 1024), (64, 8, 64), (512, 8, 256), (513, 8, 255),
-                                   (3000, 8, 128), (16384, 8, 256), (30011, 7, 1000), (200003, 1, 31)])
+                                   (3000, 8, 128), (512, 8, 1024), (4097, 1, 1024), (16384, 8, 256), (131072, 8, 64), (30011, 7, 1000), (200003, 1, 31)])
 @pytest.mark.parametrize("kind", ["random", "dropped", "skewed"])
 def test_dispatch(T, k, E, kind):
     rng = np.random.default_rng(T + k)
