@@ -56,11 +56,13 @@ struct MatvecArgs {
   int64_t w_expert, s_expert;
   uint32_t E;
   int32_t top_k;
-  uint32_t slots;           // (expert, rows) pairs that the grid covers
   uint32_t stages;          // of K
   uint32_t split;           // CTAs that share K (the cluster)
+  uint32_t share, longer;   // stages of a CTA's share; the first `longer` CTAs have one more
   uint32_t chunk;           // stages of x pieces in shared memory
+  int64_t tiles;            // of weight rows
   uint32_t colw;            // columns held for one n-tile
+  uint32_t red_at;          // the sums, behind the pieces
   uint32_t g_per;           // global scales of an expert: 1, or 2 (one per half)
   int swiglu;
   int out_bf16;
@@ -245,39 +247,42 @@ __device__ __forceinline__ bool whole_piece(const uint32_t (&w)[4], uint32_t (&h
 // if there are fewer. Offsets are clamped to [0, M], so no row outside the
 // product is touched whatever they hold. One thread looks after one expert.
 template <int W>
-__device__ __forceinline__ bool find_slot(const MatvecArgs& a, uint32_t slot, uint32_t TT, int64_t* sh,
+__device__ __forceinline__ bool find_slot(const MatvecArgs& a, uint32_t slot, uint32_t TT, int32_t* sh,
                                           uint32_t* e, int64_t* r0, uint32_t* m) {
-  // sh: [0] result expert, [1] first row, [2] rows, [3 ..] warp totals
+  // sh: [0] result expert, [1] first row, [2] rows, [3 ..] warp totals (M and
+  // every count of tiles are below 2^31)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sh[2] = 0;
-  uint64_t before = 0;
+  uint32_t before = 0;
   for (uint32_t base = 0; base < a.E; base += W * 32) {
     const uint32_t i = base + tid;
-    int64_t b = 0, n = 0;
+    int32_t b = 0, n = 0;
     if (i < a.E) {
-      b = min(max(a.off[i], int64_t(0)), a.M);
-      n = max(min(max(a.off[i + 1], int64_t(0)), a.M) - b, int64_t(0));
+      b = int32_t(min(max(a.off[i], int64_t(0)), a.M));
+      n = max(int32_t(min(max(a.off[i + 1], int64_t(0)), a.M)) - b, 0);
     }
-    const uint64_t tiles = (uint64_t(n) + TT - 1) / TT;
-    uint64_t incl = tiles;
+    const uint32_t tiles = (uint32_t(n) + TT - 1) / TT;
+    uint32_t incl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint64_t up = __shfl_up_sync(kFull, incl, o);
+      const uint32_t up = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += up;
     }
-    __syncthreads();                              // sh[2] is set; the last totals are read
-    if (lane == 31) sh[3 + warp] = int64_t(incl);
+    if (base > 0) __syncthreads();                // the last totals are read
+    if (lane == 31) sh[3 + warp] = int32_t(incl);
     __syncthreads();
-    uint64_t first = before + incl - tiles;
+    uint32_t first = before + incl - tiles;
+#pragma unroll
     for (int w = 0; w < W; w++) {
-      if (w < warp) first += uint64_t(sh[3 + w]);
-      before += uint64_t(sh[3 + w]);
+      const uint32_t n_w = uint32_t(sh[3 + w]);
+      first += w < warp ? n_w : 0;
+      before += n_w;
     }
     if (slot >= first && slot < first + tiles) {
-      const int64_t skip = int64_t(slot - first) * TT;
-      sh[0] = i;
+      const int32_t skip = int32_t((slot - first) * TT);
+      sh[0] = int32_t(i);
       sh[1] = b + skip;
-      sh[2] = min(n - skip, int64_t(TT));
+      sh[2] = min(n - skip, int32_t(TT));
     }
     if (before > slot) break;                     // the same for every thread
   }
@@ -294,11 +299,6 @@ __device__ __forceinline__ void cluster_arrive_wait() {
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float cluster_ld(uint32_t addr) {
-  float r;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr));
   return r;
 }
 
@@ -621,20 +621,23 @@ __device__ __noinline__ void copy_scales_edge(uint32_t dst, const uint8_t* p, in
 template <int FMT, typename XT, int NT, bool A16, int W, int ST>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(const MatvecArgs a) {
   constexpr int kTileRows = 16 * W;
-  constexpr int kRedPitch = kTileRows + 4;             // floats of one column of the sums
   constexpr int P = Pieces<XT>::n;
   constexpr uint32_t TT = 8 * NT / P;                  // rows of x in a tile
   using Scales = ScaleBlock<FMT, ST>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t found[3 + W];
+  __shared__ int32_t found[3 + W];
+  __shared__ int32_t source[TT];
   __shared__ __align__(128) uint32_t zeros[64];
   pdl_enter();
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = blockIdx.x % a.split;
-  const uint32_t unit = blockIdx.x / a.split;
-  const uint32_t slot = unit % a.slots;
-  const int64_t tile = unit / a.slots;
+  // grid: x the shares of K (a cluster) of each (expert, rows) pair, y and z
+  // the tiles of weight rows
+  uint32_t rank, slot;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%clusterid.x;" : "=r"(slot));
+  const int64_t tile = int64_t(blockIdx.z) * gridDim.y + blockIdx.y;
+  if (tile >= a.tiles) return;                         // the same for the whole cluster
   uint32_t e = 0, m = 0;
   int64_t r0 = 0;
   if (a.off) {
@@ -644,6 +647,9 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
     m = uint32_t(min(int64_t(TT), a.M - r0));
   }
 
+  // every CTA of the cluster has to be there before its memory is written:
+  // arrive now, wait before the sums are sent
+  if (a.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // the same for the whole cluster; rows on 8-byte boundaries are rare, and
   // left to the general form
   const bool narrow = A16 && m * P <= kNarrow;
@@ -670,8 +676,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
 
   const uint32_t ring = smem_ptr(smem) + warp * Ring<FMT, W, ST>::warp;
   const uint32_t scale_ring = ring + ST * kWarpTile;
-  const uint32_t s_begin = uint32_t(uint64_t(a.stages) * rank / a.split);
-  const uint32_t s_end = uint32_t(uint64_t(a.stages) * (rank + 1) / a.split);
+  const uint32_t s_begin = rank * a.share + min(rank, a.longer);
+  const uint32_t s_end = s_begin + a.share + (rank < a.longer ? 1 : 0);
 
   // copies: 16 bytes a lane, 4 rows of 128 bytes an instruction (8 bytes and 2
   // rows where rows start on 8-byte boundaries only), rows 0-7 and 8-15 apart.
@@ -754,6 +760,14 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
   const uint32_t sbase = xbase + a.chunk * kStageGroups * gstride;
   const uint32_t sstride = NT == 1 ? a.colw * 4 : NT * 32;          // bytes of one group's scales
   const XT* const x = static_cast<const XT*>(a.x);
+  if (uint32_t(tid) < m) {                                          // read after the barriers of the first chunk
+    int64_t row = r0 + tid;
+    if (a.order) {
+      const int32_t pair = a.order[row];
+      row = pair >= 0 && pair / a.top_k < a.x_rows ? pair / a.top_k : -1;
+    }
+    source[tid] = int32_t(row);
+  }
 
   const uint32_t ebase = sbase + a.chunk * kStageGroups * sstride;  // one word a stage: pieces with uneven scales
 
@@ -777,17 +791,10 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
           st0 -= n;
           mi0++;
         }
-        const uint32_t mi = mis[q];
-        if (mi >= m) continue;
+        if (mis[q] >= m) continue;
         const int64_t k = int64_t(first + sts[q]) * kStageK + lane * 8;
-        int64_t row = r0 + mi;
-        bool there = k < a.K;
-        if (a.order && there) {
-          const int32_t pair = a.order[row];
-          row = pair / a.top_k;
-          there = pair >= 0 && row < a.x_rows;
-        }
-        if (there) in[q].load(x + row * a.ld_x + k); else in[q].zero();
+        const int32_t row = source[mis[q]];
+        if (k < a.K && row >= 0) in[q].load(x + row * a.ld_x + k); else in[q].zero();
       }
 #pragma unroll
       for (int q = 0; q < kAhead; q++) {
@@ -916,10 +923,24 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
     sweep(std::integral_constant<int, NT>{});
   }
 
-  // ---- sums of the cluster's shares, in rank order
-  cp_wait<0>();
-  __syncthreads();                                                  // the rings are free
-  float* const red = reinterpret_cast<float*>(smem);
+  // ---- sums of the cluster's shares: each CTA writes its sums of an output
+  // row to the CTA that puts that row out, which adds up what came in rank order
+  // once all have arrived (no CTA reads another's memory, so each is done then).
+  // [rank][column][row of the slice], in memory that the rings do not use: other
+  // CTAs may still be at work.
+  const uint32_t per = a.swiglu ? kTileRows / 2 : kTileRows;        // outputs
+  if (a.split > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  const uint32_t slice = (per + a.split - 1) / a.split;             // of a CTA
+  const uint32_t rows_slice = a.swiglu ? 2 * slice : slice;         // weight rows of them
+  const uint32_t red = xbase + a.red_at;
+  auto send = [&](uint32_t col, uint32_t row, float v) {
+    // rows 0-7 of each 16 are gate and 8-15 up rows with swiglu
+    const uint32_t o = a.swiglu ? (row >> 4) * 8 + (row & 7) : row;
+    const uint32_t to = o / slice, at = (o - to * slice) + (a.swiglu && (row & 8) ? slice : 0);
+    uint32_t addr = red + ((rank * (8 * NT) + col) * rows_slice + at) * 4;
+    if (a.split > 1) addr = cluster_map(addr, to);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+  };
   if (narrow) {
 #pragma unroll
     for (int n = 0; n < 2; n++) {
@@ -932,69 +953,56 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
       }
       const uint32_t col = 2 * n + (t >> 1);
       if ((t & 1) == 0 && col < cols) {
-        red[col * kRedPitch + warp * 16 + g] = lo;
-        red[col * kRedPitch + warp * 16 + g + 8] = hi;
+        send(col, warp * 16 + g, lo);
+        send(col, warp * 16 + g + 8, hi);
       }
     }
-  }
+  } else {
 #pragma unroll
-  for (int n = 0; n < NT; n++) {
-    if (!narrow && uint32_t(n) < used) {
-      float* const c0 = red + (n * 8 + 2 * t) * kRedPitch + warp * 16 + g;
-      c0[0] = acc[n][0];
-      c0[kRedPitch] = acc[n][1];
-      c0[8] = acc[n][2];
-      c0[kRedPitch + 8] = acc[n][3];
+    for (int n = 0; n < NT; n++) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint32_t col = n * 8 + 2 * t + (i & 1);
+        if (col < cols) send(col, warp * 16 + g + (i < 2 ? 0 : 8), acc[n][i]);
+      }
     }
   }
   if (a.split > 1) cluster_arrive_wait(); else __syncthreads();
 
-  const uint32_t per = a.swiglu ? kTileRows / 2 : kTileRows;
-  const uint32_t lo = per * rank / a.split, len = per * (rank + 1) / a.split - lo;
-  const uint32_t red_addr = smem_ptr(red);
-  auto total = [&](uint32_t col, uint32_t row) -> float {
+  const uint32_t lo = rank * slice, len = min(slice, per - min(per, lo));
+  auto total = [&](uint32_t col, uint32_t at) -> float {
     float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < P; p++) {
-      const uint32_t at = ((col * P + p) * kRedPitch + row) * 4;
-      if (a.split == 1) {
-        v += red[at / 4];
-      } else {
-        float part[8];                                              // all on their way at once
-#pragma unroll
-        for (uint32_t q = 0; q < 8; q++) part[q] = q < a.split ? cluster_ld(cluster_map(red_addr + at, q)) : 0.f;
-#pragma unroll
-        for (uint32_t q = 0; q < 8; q++) v += part[q];
-      }
-    }
+    for (int p = 0; p < P; p++)
+      for (uint32_t q = 0; q < a.split; q++)
+        v += __uint_as_float(lds32(red + ((q * (8 * NT) + col * P + p) * rows_slice + at) * 4));
     return v;
   };
+  float gA = 1.f, gB = 1.f;
+  if constexpr (FMT == kNv) {
+    const float* gp = a.g + int64_t(e) * a.g_per;
+    gA = gp[0];
+    gB = a.g_per == 2 ? gp[1] : gA;
+  }
   for (uint32_t i = tid; i < m * len; i += 32 * W) {
-    const uint32_t mi = i / len, o = lo + i % len;
-    if (o0 + o >= outs) continue;
-    float gA = 1.f, gB = 1.f;
-    if constexpr (FMT == kNv) {
-      const float* gp = a.g + int64_t(e) * a.g_per;
-      gA = gp[0];
-      gB = a.g_per == 2 ? gp[1] : gA;
-    }
+    const uint32_t mi = i / len, o = i % len;
+    const int64_t out = o0 + lo + o;
+    if (out >= outs) continue;
     float v;
     if (a.swiglu) {
-      const uint32_t row = (o >> 3) * 16 + (o & 7);
-      const float gate = total(mi, row) * gA, up = total(mi, row + 8) * gB;
+      const float gate = total(mi, o) * gA, up = total(mi, slice + o) * gB;
       // silu(z) = z / (1 + e^-z); e^-z overflows to inf for z < -88, where
       // silu is -0 to fp32's last bit
       v = gate / (1.f + expf(-gate)) * up;
     } else {
-      v = total(mi, o) * (o0 + o >= half && a.g_per == 2 ? gB : gA);
+      v = total(mi, o) * (out >= half ? gB : gA);
     }
-    const int64_t at = (r0 + mi) * outs + o0 + o;
+    const int64_t at = (r0 + mi) * outs + out;
     if (a.out_bf16)
       static_cast<uint16_t*>(a.y)[at] = uint16_t(cvt_bf16x2(v, 0.f));
     else
       static_cast<float*>(a.y)[at] = v;
   }
-  if (a.split > 1) cluster_arrive_wait();                           // no CTA leaves while its sums are read
 }
 
 // y[t, n] = sum_j weights[t, j] rows[positions[t, j], n]: a token's rows added
@@ -1045,16 +1053,20 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const float* __re
 // ------------------------------------------------------------------ host
 
 
-// How K is shared out: the split whose busiest multiprocessor has least to do,
-// counting the fixed work of a round of resident CTAs (x pieces, the exchange
-// of the sums) as three stages.
+// How K is shared out: the split that takes least time by this estimate, in
+// stages of one CTA alone on its multiprocessor. Two CTAs beside one another
+// take 1.2 times as long for a stage, three 1.6 times (measured on 56832 x 8192
+// and on 8 experts' 2048 x 7168); a round of resident CTAs has fixed work (x's
+// pieces, the exchange of the sums) of about five stages.
 uint32_t choose_split(uint64_t units, uint32_t stages, uint64_t resident) {
   const uint64_t sms = uint64_t(sm_count());
+  constexpr uint64_t kTogether[4] = {0, 10, 12, 16};               // tenths
   uint32_t best = 1;
   uint64_t best_cost = ~0ull;
   for (uint32_t c = 1; c <= 8 && (c == 1 || c <= stages); c++) {
-    const uint64_t per_sm = (units * c + sms - 1) / sms;
-    const uint64_t cost = per_sm * ((stages + c - 1) / c) + 3 * ((per_sm + resident - 1) / resident);
+    const uint64_t per_sm = (units * c + sms - 1) / sms, share = (stages + c - 1) / c;
+    const uint64_t rounds = per_sm / resident, rest = per_sm % resident;
+    const uint64_t cost = share * (rounds * kTogether[resident] + kTogether[rest]) + 50 * (rounds + (rest ? 1 : 0));
     if (cost < best_cost) {
       best_cost = cost;
       best = c;
@@ -1065,10 +1077,13 @@ uint32_t choose_split(uint64_t units, uint32_t stages, uint64_t resident) {
 
 template <int FMT, typename XT, int NT, bool A16>
 mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
-  // one n-tile: three CTAs of 8 warps a multiprocessor (74 KB each); more: one
-  // of 16, whose 256 rows share the x pieces
-  constexpr int W = NT == 1 ? 8 : 16, ST = NT == 1 ? 3 : 4;
-  constexpr uint32_t kPieces = (NT == 1 ? 73u << 10 : 225u << 10) - Ring<FMT, W, ST>::bytes;   // for x pieces
+  // one n-tile: CTAs of 8 warps, three a multiprocessor (74 KB each) for few
+  // columns and two (112 KB) for up to eight; more: one of 16 warps, whose 256
+  // rows share the x pieces
+  constexpr int W = NT == 1 ? 8 : 16, ST = 3;
+  // the sums: a slice is rounded up, by one output (two weight rows) a CTA at
+  // most
+  constexpr uint32_t kSums = 8 * NT * (16 * W + 8 * 2) * 4;
   constexpr uint32_t P = Pieces<XT>::n;
   constexpr uint32_t TT = 8 * NT / P;
   const uint64_t tile_rows = a.swiglu ? 8 * W : 16 * W;
@@ -1082,26 +1097,36 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   } else {
     slots = likely = (uint64_t(a.M) + TT - 1) / TT;
   }
-  a.split = choose_split(likely * tiles, a.stages, NT == 1 ? 3 : 1);
-  if (slots * tiles * a.split > 0x7fffffffull) return MXQ_ERR_SHAPE;
-  a.slots = uint32_t(slots);
-  // columns in shared memory: up to four, or all eight of an n-tile
+  // columns in shared memory: those that the widest form reads, which are one,
+  // two or four in stage_narrow and all eight of an n-tile in stage_math
   const uint64_t most = std::min<uint64_t>(TT, uint64_t(a.M)) * P;
-  a.colw = NT == 1 && most <= kNarrow && A16 ? uint32_t(most) : 8;
+  a.colw = NT == 1 && most <= kNarrow && A16 ? (most <= 2 ? uint32_t(most) : 4) : 8;
+  constexpr uint32_t kMostSmem = NT == 1 ? 111u << 10 : 225u << 10;
+  const uint32_t resident = NT > 1 ? 1 : a.colw < 8 ? 3 : 2;
+  const uint32_t pieces = (resident == 3 ? 73u << 10 : kMostSmem) - Ring<FMT, W, ST>::bytes - kSums;
+  a.split = choose_split(likely * tiles, a.stages, resident);
+  if (slots * a.split > 0x7fffffffull) return MXQ_ERR_SHAPE;
+  a.tiles = int64_t(tiles);
+  a.share = a.stages / a.split;
+  a.longer = a.stages % a.split;
   const uint32_t per_stage = kStageGroups * NT * a.colw * (64 + 4) + 4;
-  const uint32_t share = (a.stages + a.split - 1) / a.split;
-  a.chunk = std::max(1u, std::min(share, kPieces / per_stage));
-  const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + size_t(a.chunk) * per_stage;
+  const uint32_t share = a.share + (a.longer ? 1 : 0);
+  a.chunk = std::max(1u, std::min(share, pieces / per_stage));
+  a.red_at = (a.chunk * per_stage + 15) / 16 * 16;
+  const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + a.red_at + kSums;
 
   constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W, ST>;
-  constexpr int kMostSmem = Ring<FMT, W, ST>::bytes + int(kPieces);
-  const cudaError_t attr_err = ensure_smem_limit<kernel>(kMostSmem);
+  static_assert(kStageGroups * NT * 8 * (64 + 4) + 4 + 16 + kSums + Ring<FMT, W, ST>::bytes <= kMostSmem,
+                "a stage of pieces has to fit");
+  const cudaError_t attr_err = ensure_smem_limit<kernel>(int(kMostSmem));
   if (attr_err != cudaSuccess) {
     record_cuda_error(attr_err);
     return MXQ_ERR_CUDA;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(uint32_t(slots * tiles) * a.split);
+  const uint64_t ny = std::min<uint64_t>(tiles, 65535), nz = (tiles + ny - 1) / ny;
+  if (nz > 65535) return MXQ_ERR_SHAPE;
+  cfg.gridDim = dim3(uint32_t(slots) * a.split, uint32_t(ny), uint32_t(nz));
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1113,7 +1138,7 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
   return launched(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
