@@ -218,9 +218,10 @@ __device__ __forceinline__ float take_piece(float (&v)[8], uint32_t (&h)[4]) {
 // The piece of a warp's 256 bf16 values (pairs, 8 a lane) under one scale,
 // taken on the packed values: the largest and the smallest non-zero magnitude
 // tell whether it holds all of them (an element of biased exponent e has its
-// last bit at 2^(e - 134), the piece's last bit is m 2^-24 with m = 2^(142 - E)).
-// False if it does not, or if there is an infinity.
-__device__ __forceinline__ bool whole_piece(const uint32_t (&w)[4], uint32_t (&h)[4], float& inv) {
+// last bit at 2^(e - 134), the piece's last bit is 2^-24 / m with
+// m = 2^(142 - E)). False if it does not; `odd` (and no piece) if there is an
+// infinity.
+__device__ __forceinline__ bool whole_piece(const uint32_t (&w)[4], uint32_t (&h)[4], float& inv, bool& odd) {
   const uint32_t am = absmax_bf16x2(absmax_bf16x2(w[0], w[1]), absmax_bf16x2(w[2], w[3])) & 0x7fff7fffu;
   const uint32_t top = __reduce_max_sync(kFull, max(am >> 16, am & 0xffffu));
   uint32_t low = 0xffffffffu;                     // smallest magnitude less one, zeros as 65535
@@ -239,7 +240,29 @@ __device__ __forceinline__ bool whole_piece(const uint32_t (&w)[4], uint32_t (&h
     const float2 f = mul_bf16x2_pow2(w[k], m);
     h[k] = cvt_f16x2(f.x, f.y);
   }
-  return top < 0x7f80u && int(low) + 1 >= (int(E) - 32) * 128;
+  odd = top >= 0x7f80u;
+  return !odd && int(low) + 1 >= (int(E) - 32) * 128;
+}
+
+// The pieces of a warp's 256 elements under one scale each, as the first pass
+// takes them; true (for all lanes) if they leave something.
+template <typename XT>
+__device__ __forceinline__ bool common_pieces(const In8<XT>& in, uint32_t (&h)[Pieces<XT>::n][4],
+                                              float (&inv)[Pieces<XT>::n]) {
+  bool odd = false;
+  if constexpr (Pieces<XT>::n == 1) {
+    if (whole_piece(in.w, h[0], inv[0], odd)) return false;
+    if (!odd) return true;
+  }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = in[i];
+#pragma unroll
+  for (int p = 0; p < Pieces<XT>::n; p++) inv[p] = take_piece<Pieces<XT>::top, true>(v, h[p]);
+  bool rest = false;
+#pragma unroll
+  for (int i = 0; i < 8; i++) rest |= v[i] != 0.f;
+  return __any_sync(kFull, rest);
 }
 
 // The (expert, rows) pair number `slot` of the pairs that the row offsets
@@ -317,8 +340,8 @@ struct ScaleBlock {
 // One stage of a warp: 16 rows x 256 codes against the first NC of NT tiles of
 // 8 columns. codes / scales: the stage's buffers of this warp; xf: the pieces
 // of the stage's first group at this lane's place; sx: their scales at this
-// lane's columns, sx_group bytes from group to group; even: every column's
-// pieces share one scale in this stage.
+// lane's columns, sx_group bytes from group to group; even: all eight groups of
+// a column have the same one (the first pass).
 template <int FMT, int ST, int NC, int NA>
 __device__ __forceinline__ void stage_math(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t xf,
                                            uint32_t xf_group, uint32_t sx, uint32_t sx_group, bool even,
@@ -626,7 +649,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
   using Scales = ScaleBlock<FMT, ST>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t found[3 + W];
-  __shared__ int32_t source[TT];
+  __shared__ const XT* source[TT];
   __shared__ __align__(128) uint32_t zeros[64];
   pdl_enter();
 
@@ -759,88 +782,80 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
   const uint32_t gstride = NT == 1 ? a.colw * 64 : NT * 512;        // bytes of one group's pieces
   const uint32_t sbase = xbase + a.chunk * kStageGroups * gstride;
   const uint32_t sstride = NT == 1 ? a.colw * 4 : NT * 32;          // bytes of one group's scales
-  const XT* const x = static_cast<const XT*>(a.x);
   if (uint32_t(tid) < m) {                                          // read after the barriers of the first chunk
     int64_t row = r0 + tid;
     if (a.order) {
       const int32_t pair = a.order[row];
       row = pair >= 0 && pair / a.top_k < a.x_rows ? pair / a.top_k : -1;
     }
-    source[tid] = int32_t(row);
+    source[tid] = row < 0 ? nullptr : static_cast<const XT*>(a.x) + row * a.ld_x;
   }
 
-  const uint32_t ebase = sbase + a.chunk * kStageGroups * sstride;  // one word a stage: pieces with uneven scales
-
-  // A warp takes one stage of one row, 8 elements a lane; its pieces get one
-  // scale, or one for each group where that leaves something of the row.
-  // Returns whether anything is left.
+  // Makes the pieces of n stages. A warp takes one stage of one row, 8 elements
+  // a lane. The first pass takes pieces under one scale each; a further one
+  // takes, with a scale for each group of 32, what those and the passes since
+  // have left. Returns whether anything is left.
+  const uint32_t piece_dst = xbase + (lane >> 2) * gstride + (lane & 3) * 16;
+  const uint32_t scale_dst = sbase + (lane >> 2) * sstride;
+  auto put = [&](uint32_t st, uint32_t col, const uint32_t (&h)[4], float inv) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece_dst + st * (kStageGroups * gstride) + col * 64),
+                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    if ((lane & 3) == 0) sts32(scale_dst + st * (kStageGroups * sstride) + col * 4, __float_as_uint(inv));
+  };
   auto stage_x = [&](uint32_t first, uint32_t n, int pass) -> bool {
     bool left = false;
-    const uint32_t t = lane & 3, group = lane >> 2;
     constexpr int kAhead = P == 1 ? 4 : 2;                          // units whose loads are in flight together
-    uint32_t mi0 = warp / n, st0 = warp % n;                        // row and stage; the next unit is W stages on
-    while (mi0 < m) {
+    const uint32_t k_end = uint32_t(a.K);
+    uint32_t mi = 0, st = warp;                                     // row and stage; the next unit is W stages on
+    while (st >= n) {
+      st -= n;
+      mi++;
+    }
+    while (mi < m) {
       In8<XT> in[kAhead];
       uint32_t mis[kAhead], sts[kAhead];
 #pragma unroll
       for (int q = 0; q < kAhead; q++) {
-        mis[q] = mi0;
-        sts[q] = st0;
-        st0 += W;
-        while (st0 >= n) {
-          st0 -= n;
-          mi0++;
+        mis[q] = mi;
+        sts[q] = st;
+        if (mi < m) {
+          const uint32_t k = (first + st) * kStageK + lane * 8;
+          const XT* const row = source[mi];
+          if (k < k_end && row) in[q].load(row + k); else in[q].zero();
         }
-        if (mis[q] >= m) continue;
-        const int64_t k = int64_t(first + sts[q]) * kStageK + lane * 8;
-        const int32_t row = source[mis[q]];
-        if (k < a.K && row >= 0) in[q].load(x + row * a.ld_x + k); else in[q].zero();
+        st += W;
+        while (st >= n) {
+          st -= n;
+          mi++;
+        }
       }
+      if (pass == 0) {
 #pragma unroll
-      for (int q = 0; q < kAhead; q++) {
-        const uint32_t mi = mis[q], st = sts[q];
-        if (mi >= m) break;
-        auto put = [&](int p, const uint32_t (&h)[4], float inv) {
-          const uint32_t col = mi * P + p, gi = st * kStageGroups + group;
-          const uint32_t dst = xbase + gi * gstride + col * 64 + t * 16;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-                       "r"(h[3]) : "memory");
-          if (t == 0) sts32(sbase + gi * sstride + col * 4, __float_as_uint(inv));
-        };
-        float v[8];
-        uint32_t h[4];
-        bool rest;
-        if constexpr (P == 1) {
-          float inv;
-          rest = !whole_piece(in[q].w, h, inv);
-          if (pass > 0) h[0] = h[1] = h[2] = h[3] = 0;              // the first pass had it
-          if (!rest) put(0, h, inv);
-        } else {
+        for (int q = 0; q < kAhead; q++) {
+          if (mis[q] >= m) break;
+          uint32_t h[P][4];
+          float inv[P];
+          left |= common_pieces(in[q], h, inv);
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[i] = in[q][i];
-#pragma unroll
-          for (int p = 0; p < P; p++) {
-            const float inv = take_piece<Pieces<XT>::top, true>(v, h);
-            if (pass > 0) h[0] = h[1] = h[2] = h[3] = 0;
-            put(p, h, inv);
-          }
-          rest = false;
-#pragma unroll
-          for (int i = 0; i < 8; i++) rest |= v[i] != 0.f;
-          rest = __any_sync(kFull, rest);
+          for (int p = 0; p < P; p++) put(sts[q], mis[q] * P + p, h[p], inv[p]);
         }
-        if (rest) {
+      } else {
+#pragma unroll
+        for (int q = 0; q < kAhead; q++) {
+          if (mis[q] >= m) break;
+          float v[8];
+          uint32_t h[4];
 #pragma unroll
           for (int i = 0; i < 8; i++) v[i] = in[q][i];
-          for (int i = 0; i < pass * P; i++) (void)take_piece<Pieces<XT>::top, false>(v, h);
 #pragma unroll 1
-          for (int p = 0; p < P; p++) {
+          for (int i = 0; i < P; i++) (void)take_piece<Pieces<XT>::top, true>(v, h);
+#pragma unroll 1
+          for (int i = 0; i < pass * P; i++) {
             const float inv = take_piece<Pieces<XT>::top, false>(v, h);
-            put(p, h, inv);
+            if (i >= (pass - 1) * P) put(sts[q], mis[q] * P + i - (pass - 1) * P, h, inv);
           }
 #pragma unroll
           for (int i = 0; i < 8; i++) left |= v[i] != 0.f;
-          if (lane == 0) sts32(ebase + st * 4, 1u);
         }
       }
     }
@@ -877,8 +892,6 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
       for (uint32_t c_begin = s_begin; c_begin < s_end; c_begin += a.chunk) {
         const uint32_t n = min(a.chunk, s_end - c_begin);
         __syncthreads();                                            // the last chunk has been read
-        if (uint32_t(tid) < n) sts32(ebase + tid * 4, 0u);
-        __syncthreads();
         const bool left = stage_x(c_begin, n, pass);
         more |= __syncthreads_or(left) != 0;
         uint32_t xg = xbase, sg = sbase;
@@ -898,8 +911,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
           if constexpr (FORM < 0)
             stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, lane);
           else
-            stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride,
-                                          lds32(ebase + (s - c_begin) * 4) == 0, lane);
+            stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride, pass == 0, lane);
           xg += kStageGroups * gstride;
           sg += kStageGroups * sstride;
           read = read == (ST - 1) * kWarpTile ? 0 : read + kWarpTile;
@@ -1109,14 +1121,14 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   a.tiles = int64_t(tiles);
   a.share = a.stages / a.split;
   a.longer = a.stages % a.split;
-  const uint32_t per_stage = kStageGroups * NT * a.colw * (64 + 4) + 4;
+  const uint32_t per_stage = kStageGroups * NT * a.colw * (64 + 4);
   const uint32_t share = a.share + (a.longer ? 1 : 0);
   a.chunk = std::max(1u, std::min(share, pieces / per_stage));
   a.red_at = (a.chunk * per_stage + 15) / 16 * 16;
   const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + a.red_at + kSums;
 
   constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W, ST>;
-  static_assert(kStageGroups * NT * 8 * (64 + 4) + 4 + 16 + kSums + Ring<FMT, W, ST>::bytes <= kMostSmem,
+  static_assert(kStageGroups * NT * 8 * (64 + 4) + 16 + kSums + Ring<FMT, W, ST>::bytes <= kMostSmem,
                 "a stage of pieces has to fit");
   const cudaError_t attr_err = ensure_smem_limit<kernel>(int(kMostSmem));
   if (attr_err != cudaSuccess) {
