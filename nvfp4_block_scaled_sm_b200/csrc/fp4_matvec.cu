@@ -642,7 +642,7 @@ __device__ __noinline__ void copy_scales_edge(uint32_t dst, const uint8_t* p, in
 }
 
 template <int FMT, typename XT, int NT, bool A16, int W, int ST>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(const MatvecArgs a) {
+__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(const MatvecArgs a) {
   constexpr int kTileRows = 16 * W;
   constexpr int P = Pieces<XT>::n;
   constexpr uint32_t TT = 8 * NT / P;                  // rows of x in a tile
@@ -804,7 +804,9 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) fp4_matvec_kernel(cons
   };
   auto stage_x = [&](uint32_t first, uint32_t n, int pass) -> bool {
     bool left = false;
-    constexpr int kAhead = P == 1 ? 4 : 2;                          // units whose loads are in flight together
+    // units whose loads are in flight together: two of bf16 where other CTAs are
+    // resident to hide them (the shorter code is worth 5 to 9 % there), else four
+    constexpr int kAhead = (NT == 1 ? 2 : 4) / (P == 1 ? 1 : 2);
     const uint32_t k_end = uint32_t(a.K);
     uint32_t mi = 0, st = warp;                                     // row and stage; the next unit is W stages on
     while (st >= n) {
@@ -1066,13 +1068,13 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const float* __re
 
 
 // How K is shared out: the split that takes least time by this estimate, in
-// stages of one CTA alone on its multiprocessor. Two CTAs beside one another
-// take 1.2 times as long for a stage, three 1.6 times (measured on 56832 x 8192
-// and on 8 experts' 2048 x 7168); a round of resident CTAs has fixed work (x's
-// pieces, the exchange of the sums) of about five stages.
+// stages of one CTA alone on its multiprocessor (1 us). Two CTAs beside one
+// another take 1.2 times as long for a stage (measured on 8 experts' 2048 x
+// 7168); a round of resident CTAs has fixed work (x's pieces, the exchange of
+// the sums) of about five stages.
 uint32_t choose_split(uint64_t units, uint32_t stages, uint64_t resident) {
   const uint64_t sms = uint64_t(sm_count());
-  constexpr uint64_t kTogether[4] = {0, 10, 12, 16};               // tenths
+  constexpr uint64_t kTogether[3] = {0, 10, 12};                   // tenths
   uint32_t best = 1;
   uint64_t best_cost = ~0ull;
   for (uint32_t c = 1; c <= 8 && (c == 1 || c <= stages); c++) {
@@ -1089,9 +1091,9 @@ uint32_t choose_split(uint64_t units, uint32_t stages, uint64_t resident) {
 
 template <int FMT, typename XT, int NT, bool A16>
 mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
-  // one n-tile: CTAs of 8 warps, three a multiprocessor (74 KB each) for few
-  // columns and two (112 KB) for up to eight; more: one of 16 warps, whose 256
-  // rows share the x pieces
+  // one n-tile: two CTAs of 8 warps a multiprocessor, 128 registers a thread
+  // (three of 80 registers took 5 to 9 % more instructions and time); more: one
+  // of 16 warps, whose 256 rows share the x pieces
   constexpr int W = NT == 1 ? 8 : 16, ST = 3;
   // the sums: a slice is rounded up, by one output (two weight rows) a CTA at
   // most
@@ -1114,16 +1116,15 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   const uint64_t most = std::min<uint64_t>(TT, uint64_t(a.M)) * P;
   a.colw = NT == 1 && most <= kNarrow && A16 ? (most <= 2 ? uint32_t(most) : 4) : 8;
   constexpr uint32_t kMostSmem = NT == 1 ? 111u << 10 : 225u << 10;
-  const uint32_t resident = NT > 1 ? 1 : a.colw < 8 ? 3 : 2;
-  const uint32_t pieces = (resident == 3 ? 73u << 10 : kMostSmem) - Ring<FMT, W, ST>::bytes - kSums;
-  a.split = choose_split(likely * tiles, a.stages, resident);
+  constexpr uint32_t kPieces = kMostSmem - Ring<FMT, W, ST>::bytes - kSums;
+  a.split = choose_split(likely * tiles, a.stages, NT == 1 ? 2 : 1);
   if (slots * a.split > 0x7fffffffull) return MXQ_ERR_SHAPE;
   a.tiles = int64_t(tiles);
   a.share = a.stages / a.split;
   a.longer = a.stages % a.split;
   const uint32_t per_stage = kStageGroups * NT * a.colw * (64 + 4);
   const uint32_t share = a.share + (a.longer ? 1 : 0);
-  a.chunk = std::max(1u, std::min(share, pieces / per_stage));
+  a.chunk = std::max(1u, std::min(share, kPieces / per_stage));
   a.red_at = (a.chunk * per_stage + 15) / 16 * 16;
   const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + a.red_at + kSums;
 
