@@ -218,6 +218,13 @@ def _empty(shape, dtype: torch.dtype, device) -> torch.Tensor:
     return t
 
 
+def _empty_like(x: torch.Tensor, shape, dtype: torch.dtype) -> torch.Tensor:
+    """:func:`_empty` on the device of ``x``, without looking it up."""
+    if _output_allocator is None:
+        return x.new_empty(shape, dtype=dtype)
+    return _empty(shape, dtype, x.device)
+
+
 def _zeros(shape, dtype: torch.dtype, device) -> torch.Tensor:
     return _empty(shape, dtype, device).zero_()
 
@@ -493,27 +500,35 @@ def mxfp8_gemm(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Tensor,
 
 # ------------------------------------------- products with 4-bit weights
 
-def _launch(fn: str, dev: torch.device, *args):
-    """Calls ``fn`` with the stream of ``dev`` that is current, on that device
-    (tensors may live on another device than the current one)."""
-    index = dev.index
+def _launch(fn: str, index: int, *args):
+    """Calls ``fn`` with the stream of CUDA device ``index`` that is current, on
+    that device (tensors may live on another device than the current one)."""
     if index == torch._C._cuda_getDevice():
         status = _fn[fn](*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = _fn[fn](*args, _raw_stream(index))
     if status:
         _check(fn, status)
 
 
-def _same_device(x: torch.Tensor, *ts: torch.Tensor) -> torch.device:
-    dev = x.device
-    if dev.type != "cuda":
+def _same_device(x: torch.Tensor, *ts: torch.Tensor) -> int:
+    """The index of the CUDA device that all of the tensors live on."""
+    index = x.get_device()
+    if index < 0:
         raise ValueError("tensors must live on a CUDA device (no CPU path exists)")
     for t in ts:
-        if t.device != dev:
+        if t.get_device() != index:
             raise ValueError("tensors must live on one CUDA device")
-    return dev
+    return index
+
+
+_CODES = {torch.bfloat16: BF16, torch.float32: FP32}
+
+
+def _code(dt: torch.dtype) -> int:
+    code = _CODES.get(dt)
+    return _dtype_code(dt) if code is None else code
 
 
 def _weight_args(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, block: int, dims: int):
@@ -535,20 +550,20 @@ def _weight_args(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor, blo
 
 
 def _matvec(fn: str, x, packed, scale, global_scale, dtype, block: int) -> torch.Tensor:
-    dev = _same_device(x, packed, scale)
+    index = _same_device(x, packed, scale)
     N, K = _weight_args(x, packed, scale, block, 2)
-    dt, out_dt = _dtype_code(x.dtype), _dtype_code(dtype)
+    dt, out_dt = _code(x.dtype), _code(dtype)
     M, _, ld = _rows_view(x)
-    y = _empty((*x.shape[:-1], N), dtype, dev)
+    y = _empty_like(x, (M, N) if x.dim() == 2 else (*x.shape[:-1], N), dtype)
     if global_scale is None:
-        _launch(fn, dev, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(), N, y.data_ptr(),
-                out_dt)
+        _launch(fn, index, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(), N,
+                y.data_ptr(), out_dt)
         return y
     if global_scale.dtype is not torch.float32 or global_scale.numel() != 1:
         raise TypeError("global_scale must be a single fp32 value")
-    if global_scale.device != dev:
-        global_scale = global_scale.to(dev)
-    _launch(fn, dev, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(),
+    if global_scale.get_device() != index:
+        global_scale = global_scale.to(x.device)
+    _launch(fn, index, x.data_ptr(), dt, M, K, ld, packed.data_ptr(), scale.data_ptr(),
             global_scale.data_ptr(), N, y.data_ptr(), out_dt)
     return y
 
@@ -571,42 +586,41 @@ def nvfp4_matvec(x: torch.Tensor, packed: torch.Tensor, block_scale: torch.Tenso
     return _matvec("nvfp4_matvec", x, packed, block_scale, global_scale, dtype, 16)
 
 
-def _device_offsets(dev, row_offsets, E: int, R: int) -> torch.Tensor:
+def _device_offsets(x: torch.Tensor, row_offsets, E: int, R: int) -> torch.Tensor:
     """row_offsets [E + 1] as a device int64 tensor; a list or a CPU tensor is
     checked, offsets on the device are clamped by the kernels."""
     if isinstance(row_offsets, torch.Tensor) and row_offsets.is_cuda:
         if row_offsets.dtype != torch.int64 or row_offsets.numel() != E + 1:
             raise TypeError("row_offsets must be int64 with E + 1 entries")
-        if row_offsets.device != dev:
-            raise ValueError("tensors must live on one CUDA device")
+        _same_device(x, row_offsets)
         return row_offsets.contiguous()
     host = [int(v) for v in (row_offsets.tolist() if isinstance(row_offsets, torch.Tensor)
                              else row_offsets)]
     if len(host) != E + 1 or host[0] < 0 or host[-1] > R or \
             any(b < a for a, b in zip(host[:-1], host[1:])):
         raise ValueError(f"row_offsets must rise within the {R} rows in {E + 1} entries")
-    return torch.tensor(host, dtype=torch.int64).to(dev)
+    return torch.tensor(host, dtype=torch.int64).to(x.device)
 
 
-def _int32(t: torch.Tensor, dev, what: str) -> torch.Tensor:
-    if t.dtype != torch.int32:
+def _int32(t: torch.Tensor, index: int, what: str) -> torch.Tensor:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{what} must be int32")
-    if t.device != dev:
+    if t.get_device() != index:
         raise ValueError("tensors must live on one CUDA device")
     return t.contiguous()
 
 
 def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k, swiglu, combine,
                     dtype, block: int) -> torch.Tensor:
-    dev = _same_device(x, packed, scale)
+    index = _same_device(x, packed, scale)
     N, K = _weight_args(x, packed, scale, block, 3)
     E = packed.shape[0]
     if x.dim() != 2:
         raise ValueError("expected rows [R, K]")
-    dt, out_dt = _dtype_code(x.dtype), _dtype_code(dtype)
+    dt, out_dt = _code(x.dtype), _code(dtype)
     x_rows, _, ld = _rows_view(x)
     if order is not None:
-        order = _int32(order, dev, "order")
+        order = _int32(order, index, "order")
         R = order.numel()
         top_k = int(top_k)
         if top_k < 1:
@@ -617,21 +631,21 @@ def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k
         R = x_rows
     if (swiglu or (scales is not None and scales.numel() == 2 * E)) and N % 2:
         raise ValueError("halves of an expert need an even number of rows")
-    offsets = _device_offsets(dev, row_offsets, E, R)
+    offsets = _device_offsets(x, row_offsets, E, R)
     g = ()
     if scales is not None:
         if scales.dtype != torch.float32 or scales.numel() not in (E, 2 * E):
             raise TypeError("global_scales must be fp32 with one or two values per expert")
-        scales = scales.to(dev).contiguous()
+        scales = scales.to(x.device).contiguous()
         g = (scales.data_ptr(), scales.numel() // E)
     outs = N // 2 if swiglu else N
     if combine is not None:
         positions, weights = combine
-        positions = _int32(positions, dev, "positions")
+        positions = _int32(positions, index, "positions")
         if positions.dim() == 0 or weights.shape != positions.shape:
             raise ValueError("positions and weights must be [..., top_k]")
-    y = _empty((R, outs), torch.float32 if combine is not None else dtype, dev)
-    _launch(fn, dev, x.data_ptr(), dt, x_rows, K, ld, packed.data_ptr(), scale.data_ptr(), *g, E, N,
+    y = _empty_like(x, (R, outs), torch.float32 if combine is not None else dtype)
+    _launch(fn, index, x.data_ptr(), dt, x_rows, K, ld, packed.data_ptr(), scale.data_ptr(), *g, E, N,
             offsets.data_ptr(), R, None if order is None else order.data_ptr(), top_k,
             1 if swiglu else 0, y.data_ptr(), FP32 if combine is not None else out_dt)
     return y if combine is None else moe_combine(y, positions, weights, dtype)
@@ -680,20 +694,20 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
     ``y[t] = sum_j weights[t, j] * rows[positions[t, j]]`` for fp32 ``rows``
     [R, N]; a position outside [0, R) (:func:`moe_dispatch`'s -1) adds nothing.
     Returns [..., N] as ``dtype``."""
-    _same_device(rows, positions, weights)
+    index = _same_device(rows, positions, weights)
     if rows.dtype != torch.float32 or weights.dtype != torch.float32:
         raise TypeError("rows and weights must be fp32")
     if rows.dim() != 2 or not rows.is_contiguous():
         raise ValueError("expected contiguous rows [R, N]")
-    positions = _int32(positions, rows.device, "positions")
+    positions = _int32(positions, index, "positions")
     if positions.dim() == 0 or weights.shape != positions.shape:
         raise ValueError("positions and weights must be [..., top_k]")
     weights = weights.contiguous()
     R, N = rows.shape
     top_k = positions.shape[-1]
     T = positions.numel() // top_k if top_k else 0
-    y = _empty((*positions.shape[:-1], N), dtype, rows.device)
-    _launch("moe_combine", rows.device, rows.data_ptr(), R, N, positions.data_ptr(),
+    y = _empty_like(rows, (*positions.shape[:-1], N), dtype)
+    _launch("moe_combine", index, rows.data_ptr(), R, N, positions.data_ptr(),
             weights.data_ptr(), T, top_k, y.data_ptr(), _dtype_code(dtype))
     return y
 
@@ -708,7 +722,7 @@ def _route_rows(logits: torch.Tensor, scoring: str):
         raise ValueError(f"scoring must be one of {sorted(_SCORES)}")
     if logits.dim() < 1:
         raise ValueError("expected logits [..., E]")
-    dt = _dtype_code(logits.dtype)
+    dt = _code(logits.dtype)
     T, E, ld = _rows_view(logits)
     return dt, T, E, ld, _SCORES[scoring]
 
@@ -728,7 +742,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     exact scores, not of their fp32 roundings. For training,
     :func:`moe_route_backward` gives the logits' gradient (this call records
     none)."""
-    _same_device(logits)
+    index = _same_device(logits)
     dt, T, E, ld, score = _route_rows(logits, scoring)
     if bias is not None:
         if bias.dtype != torch.float32 or bias.shape != (E,):
@@ -737,9 +751,9 @@ def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
         bias = bias.contiguous()
     top_k = int(top_k)
     shape = (*logits.shape[:-1], max(top_k, 0))
-    weights = _empty(shape, torch.float32, logits.device)
-    experts = _empty(shape, torch.int32, logits.device)
-    _launch("moe_route", logits.device, logits.data_ptr(), dt, T, E, ld, score,
+    weights = _empty_like(logits, shape, torch.float32)
+    experts = _empty_like(logits, shape, torch.int32)
+    _launch("moe_route", index, logits.data_ptr(), dt, T, E, ld, score,
             None if bias is None else bias.data_ptr(), int(groups), int(top_groups), top_k,
             1 if renormalize else 0, float(scale), weights.data_ptr(), experts.data_ptr())
     return weights, experts
@@ -752,17 +766,17 @@ def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, experts
     the ``experts`` that it chose (int32 [..., top_k]) and the gradient of its
     weights (fp32 [..., top_k]); shaped and typed like ``logits``. Experts
     outside [0, E) are left out; the choice itself has no gradient."""
-    _same_device(logits, grad_weights, experts)
+    index = _same_device(logits, grad_weights, experts)
     dt, T, E, ld, score = _route_rows(logits, scoring)
     if grad_weights.dtype != torch.float32:
         raise TypeError("grad_weights must be fp32")
-    experts = _int32(experts, logits.device, "experts")
+    experts = _int32(experts, index, "experts")
     if experts.dim() != logits.dim() or experts.shape[:-1] != logits.shape[:-1] or \
             grad_weights.shape != experts.shape:
         raise ValueError("grad_weights and experts must be [..., top_k] with the rows of logits")
     grad_weights = grad_weights.contiguous()
-    out = _empty(logits.shape, logits.dtype, logits.device)
-    _launch("moe_route_backward", logits.device, grad_weights.data_ptr(), logits.data_ptr(), dt, T, E,
+    out = _empty_like(logits, logits.shape, logits.dtype)
+    _launch("moe_route_backward", index, grad_weights.data_ptr(), logits.data_ptr(), dt, T, E,
             ld, experts.data_ptr(), score, experts.shape[-1], 1 if renormalize else 0, float(scale),
             out.data_ptr())
     return out
@@ -779,16 +793,15 @@ def moe_dispatch(experts: torch.Tensor, E: int):
     :func:`mxfp4_matvec_grouped`) follow without a copy to the host. Pairs with
     an expert outside [0, E) are dropped: they come after ``row_offsets[E]``
     and have position -1."""
-    _same_device(experts)
-    experts = _int32(experts, experts.device, "experts")
+    index = _same_device(experts)
+    experts = _int32(experts, index, "experts")
     P, E = experts.numel(), int(E)
-    dev = experts.device
-    row_offsets = _empty(max(E, 0) + 1, torch.int64, dev)
-    order = _empty(P, torch.int32, dev)
-    positions = _empty(experts.shape, torch.int32, dev)
-    need = _fn["mxq_moe_dispatch_workspace_bytes"](P, E)
-    ws = _empty(need, torch.uint8, dev) if need else None
-    _launch("moe_dispatch", dev, experts.data_ptr(), P, E, row_offsets.data_ptr(), order.data_ptr(),
+    row_offsets = _empty_like(experts, (max(E, 0) + 1,), torch.int64)
+    order = _empty_like(experts, (P,), torch.int32)
+    positions = _empty_like(experts, experts.shape, torch.int32)
+    need = _fn["mxq_moe_dispatch_workspace_bytes"](P, E) if P > 4096 else 0
+    ws = _empty_like(experts, (need,), torch.uint8) if need else None
+    _launch("moe_dispatch", index, experts.data_ptr(), P, E, row_offsets.data_ptr(), order.data_ptr(),
             positions.data_ptr(), None if ws is None else ws.data_ptr(), need)
     return row_offsets, order, positions
 

@@ -4,25 +4,36 @@
 //
 // Mathematics. An E2M1 code is exact in fp16, and so is its product with an
 // E4M3 block scale (2 + 4 significant bits, 2^-10 .. 2688). A row x is brought
-// to fp16 in groups of 32 elements: with E the exponent of the group's largest
-// finite magnitude, the fp16 piece is x 2^(15 - E), so every element of at
-// least 2^-32 of that magnitude keeps all eight bits of a bf16. fp32 rows take
-// three pieces (11 + 11 + 2 bits, the first x 2^(14 - E)). What is left after the pieces of a pass is
-// computed exactly (x minus the pieces); if any of it is not zero, another
-// pass over the weights adds it, so the products that are summed are those of
-// x itself whatever its range. Each group's 32 products are summed by two
-// m16n8k16 MMAs (fp16 products exact, fp32 sums); the group's scales (the
-// E8M0 scale of MXFP4, the power of two of the piece) multiply that sum in
-// fp32 as it is added to the row's fp32 accumulator. NVFP4's global scale
-// multiplies the finished sum.
+// to fp16 as well, 256 elements under one power of two: with E the exponent of
+// their largest finite magnitude, the piece of a bf16 row is x 2^(15 - E), so
+// every element of at least 2^-32 of that magnitude keeps all its eight bits;
+// fp32 rows take three pieces (11 + 11 + 2 bits, the first x 2^(14 - E)). What
+// the pieces leave is computed exactly (x minus the pieces); if any of it is not
+// zero, another pass over the weights adds it, with a power of two for each 32
+// elements, and so on: the products that are summed are those of x itself
+// whatever its range. Sums of 16 to 256 products are formed by m16n8k16 MMAs
+// (fp16 products exact, fp32 sums); the scales (MXFP4's E8M0, NVFP4's global
+// one, the power of two of the piece) multiply them in fp32 as they are added
+// to the row's fp32 accumulator.
 //
-// Tiling. A warp holds 16 weight rows; a CTA of 8 warps 128 rows of a share of
-// K, up to 8 CTAs of a cluster the shares of the same rows, added up through
-// distributed shared memory in rank order (the same bits every run). Codes
-// arrive by 16-byte asynchronous copies in a ring of three or four stages per
-// warp (256 codes of each of its rows a stage), each warp waiting for its own;
-// the x pieces of the CTA's share are made once per CTA, in the order in which
-// a lane feeds them to the MMA, while the first codes are on their way.
+// Tiling. A warp holds 16 weight rows; a CTA 128 rows (8 warps, two CTAs a
+// multiprocessor, for up to 8 columns) or 256 (16 warps, for 16 or 32: the x
+// pieces are made by each CTA, and more rows share them) of a share of K; up to
+// 8 CTAs of a cluster take the shares of the same rows and send their sums to
+// the CTA that puts a row out, which adds them up in rank order (the same bits
+// every run). Codes arrive by 16-byte asynchronous copies in a ring of three
+// stages a warp (256 codes of each of its rows a stage), each warp waiting for
+// its own; the x pieces of the CTA's share are made in the order in which a lane
+// feeds them to the MMA, while the first codes are on their way.
+//
+// What bounds it: instructions issued, then memory. With the MMAs and scales
+// left out, 64 tokens' 512 rows against 64 experts' 2048 x 7168 (MXFP4, 500 MB)
+// take 108 us, without x's pieces too 87 us (5.8 TB/s); all of it takes 198 us.
+// One row against 100003 x 4096 takes 54 us (4.0 TB/s), against 4096 x 4096
+// 7 us, of which 4 us are the start, the pieces of x and the exchange of sums.
+// Tried and slower: x's pieces made once by a kernel before (8 rows against
+// 7168 x 7168 21 us for 18), 32 rows a warp with half the warps (the experts
+// 228 us for 198), three CTAs of 80 registers (5 to 9 %).
 #include <type_traits>
 
 #include "common.cuh"
@@ -345,7 +356,7 @@ struct ScaleBlock {
 template <int FMT, int ST, int NC, int NA>
 __device__ __forceinline__ void stage_math(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t xf,
                                            uint32_t xf_group, uint32_t sx, uint32_t sx_group, bool even,
-                                           int lane) {
+                                           const float (&global)[2], int lane) {
   constexpr int kRow = ScaleBlock<FMT, ST>::row;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t rowA = codes + g * kRowPitch + t * 4, rowB = rowA + 8 * kRowPitch;
@@ -434,7 +445,7 @@ __device__ __forceinline__ void stage_math(float (&acc)[NA][4], uint32_t codes, 
         const uint2 u = lds64(sx + j * sx_group + n * 32);
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          acc[n][i] = __fmaf_rn(c[n][i], __uint_as_float(i & 1 ? u.y : u.x), acc[n][i]);
+          acc[n][i] = __fmaf_rn(c[n][i] * global[i >> 1], __uint_as_float(i & 1 ? u.y : u.x), acc[n][i]);
       }
     };
     if (even) {                                   // the stage's 256 products are one sum
@@ -492,7 +503,7 @@ __device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&c)[4],
 template <int FMT, int ST, int COLS, int NA>
 __device__ __forceinline__ void stage_narrow(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t x0,
                                              uint32_t x_group, uint32_t zero, uint32_t sx, uint32_t sx_group,
-                                             int lane) {
+                                             const float (&global)[2], int lane) {
   constexpr int kRow = ScaleBlock<FMT, ST>::row;
   constexpr int NC = COLS <= 2 ? 1 : 2;
   const int g = lane >> 2, t = lane & 3;
@@ -558,7 +569,7 @@ __device__ __forceinline__ void stage_narrow(float (&acc)[NA][4], uint32_t codes
     auto scale = [&](uint32_t wa, uint32_t wb, int gi) {
       const float2 fA = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(wa >> shift));
       const float2 fB = f16x2_to_f32x2(cvt_f16x2_from_e4m3x2(wb >> shift));
-      const float f[4] = {fA.x, fA.y, fB.x, fB.y};
+      const float f[4] = {fA.x * global[0], fA.y * global[0], fB.x * global[1], fB.y * global[1]};
 #pragma unroll
       for (int n = 0; n < NC; n++) {
         const float s = __uint_as_float(lds32(sx + gi * sx_group + (COLS == 1 ? 0 : n * 8 + (t >> 1) * 4)));
@@ -868,6 +879,20 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
   const uint32_t lane_x = (NT == 1 ? (min(uint32_t(g), a.colw - 1) * 4 + t) : uint32_t(lane)) * 16;
   const uint32_t zero = smem_ptr(zeros) + 32;                       // 32 past a multiple of 64: not x's banks
 
+  // NVFP4's global scales of rows g and g + 8. They multiply the sums of a stage
+  // (a group, in further passes) as these are added up: the products of x and
+  // the block-scaled codes alone may lie up to 2688 * 448 times higher than the
+  // result, out of fp32's range.
+  float global[2] = {1.f, 1.f};
+  if constexpr (FMT == kNv) {
+    const float* const gp = a.g + int64_t(e) * a.g_per;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const bool upper = a.swiglu ? i == 1 : o0 + wrow + g + 8 * i >= half;
+      global[i] = gp[a.g_per == 2 && upper ? 1 : 0];
+    }
+  }
+
   constexpr int NA = NT < 2 ? 2 : NT;
   float acc[NA][4];
 #pragma unroll
@@ -911,9 +936,11 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
           const uint32_t scales =
               scale_ring + (s / Scales::stages & 1) * Scales::bytes + s % Scales::stages * Scales::stage;
           if constexpr (FORM < 0)
-            stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, lane);
+            stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, global,
+                                              lane);
           else
-            stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride, pass == 0, lane);
+            stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride, pass == 0,
+                                          global, lane);
           xg += kStageGroups * gstride;
           sg += kStageGroups * sstride;
           read = read == (ST - 1) * kWarpTile ? 0 : read + kWarpTile;
@@ -992,24 +1019,18 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
         v += __uint_as_float(lds32(red + ((q * (8 * NT) + col * P + p) * rows_slice + at) * 4));
     return v;
   };
-  float gA = 1.f, gB = 1.f;
-  if constexpr (FMT == kNv) {
-    const float* gp = a.g + int64_t(e) * a.g_per;
-    gA = gp[0];
-    gB = a.g_per == 2 ? gp[1] : gA;
-  }
   for (uint32_t i = tid; i < m * len; i += 32 * W) {
     const uint32_t mi = i / len, o = i % len;
     const int64_t out = o0 + lo + o;
     if (out >= outs) continue;
     float v;
     if (a.swiglu) {
-      const float gate = total(mi, o) * gA, up = total(mi, slice + o) * gB;
+      const float gate = total(mi, o), up = total(mi, slice + o);
       // silu(z) = z / (1 + e^-z); e^-z overflows to inf for z < -88, where
       // silu is -0 to fp32's last bit
       v = gate / (1.f + expf(-gate)) * up;
     } else {
-      v = total(mi, o) * (out >= half ? gB : gA);
+      v = total(mi, o);
     }
     const int64_t at = (r0 + mi) * outs + out;
     if (a.out_bf16)

@@ -138,6 +138,43 @@ def test_wide_range_inside_a_group(fmt, xd):
     R.check(y, exact, size, K, "wide range")
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("xd", [BF16, FP32])
+def test_ends_of_the_range_of_x(fmt, xd):
+    """Subnormal rows, rows near the type's largest value, rows that hold both,
+    and zeros: scales of the pieces at both ends."""
+    rng = np.random.default_rng(12)
+    N, K = 24, 288
+    p, s = R.weight(rng, fmt, N, K, spread=1)
+    big = float(torch.finfo(xd).max)
+    x = np.zeros((6, K))
+    x[0] = rng.integers(-127, 128, K) * 2.0 ** -133             # bf16 subnormals
+    x[1] = rng.uniform(-1, 1, K) * big
+    x[2] = np.where(rng.random(K) < 0.5, rng.uniform(-1, 1, K) * big, rng.integers(-127, 128, K) * 2.0 ** -133)
+    x[3] = -0.0
+    x[4, 7] = 2.0 ** -126
+    x[5, ::32] = big
+    xt = torch.from_numpy(x.astype(np.float32)).to(xd).cuda()
+    assert torch.isfinite(xt).all()
+    for m in (6, 1):                                            # both forms of the product
+        y = run(fmt, xt[:m] if m == 6 else xt[:1], cuda(p), cuda(s), scalar(2.0 ** -20))
+        w = R.decode(p, s, fmt) * (2.0 ** -20 if fmt == "nvfp4" else 1)
+        exact, size = R.product(R.f64(xt)[:m], w)
+        top = float(np.finfo(np.float32).max)
+        safe = size * 64 < top                                  # no partial sum overflows
+        keep = torch.from_numpy(safe).cuda()
+        R.check(torch.where(keep, y, 0), np.where(safe, exact, 0), np.where(safe, size, 0), K, "range")
+        assert not y[3:4].any()
+
+
+def test_many_rows():
+    rng = np.random.default_rng(13)
+    N, K, M = 40, 512, 1000
+    p, s = R.weight(rng, "mxfp4", N, K)
+    x = rows(rng, M, K, BF16)
+    R.check(mxq.mxfp4_matvec(x, cuda(p), cuda(s), dtype=FP32), *R.product(R.f64(x), R.decode(p, s, "mxfp4")), K, "many rows")
+
+
 def test_fp32_rows_keep_their_bits():
     """x of 24 bits against one non-zero weight, a power of two: the product
     itself needs no rounding. It is the sum of the pieces of x, three a pass;
@@ -475,6 +512,31 @@ def test_offsets_past_32_bits():
     assert not y[:, :N - 64].any()
 
 
+def test_calls_from_two_threads():
+    import threading
+    rng = np.random.default_rng(34)
+    p, s = R.weight(rng, "nvfp4", 256, 512)
+    x = rows(rng, 6, 512, FP32)
+    pd, sd, g = cuda(p), cuda(s), scalar(0.5)
+    want = mxq.nvfp4_matvec(x, pd, sd, g, dtype=FP32)
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                got[i].append(mxq.nvfp4_matvec(x, pd, sd, g, dtype=FP32))
+        st.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(want, y) for l in got for y in l)
+
+
 def test_refusals():
     x = torch.zeros(2, 64, dtype=BF16, device="cuda")
     p = torch.zeros(8, 32, dtype=torch.uint8, device="cuda")
@@ -491,6 +553,7 @@ def test_refusals():
         lambda: mxq.mxfp4_matvec(x, p.view(torch.int8), s),
         lambda: mxq.mxfp4_matvec(x, p.t(), s),
         lambda: mxq.mxfp4_matvec(x.cpu(), p, s),
+        lambda: mxq.mxfp4_matvec(x[:1].expand(2, 64), p, s),
         lambda: mxq.mxfp4_matvec(x, p.cpu(), s),
         lambda: mxq.mxfp4_matvec(torch.zeros(2, 128, dtype=BF16, device="cuda")[:, ::2], p, s),
         lambda: mxq.mxfp4_matvec(torch.zeros(130, dtype=BF16, device="cuda")[1:129].view(2, 64), p, s),
