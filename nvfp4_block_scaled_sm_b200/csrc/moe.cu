@@ -14,6 +14,11 @@
 // that of the logits, which are compared as they are. With one, keys are
 // formed in fp32 with a bound on their error; a token whose choice some
 // difference below that bound could turn takes the same steps again in fp64.
+//
+// Bound by instructions: 16384 tokens of 256 experts with a bias and 4 of 8
+// groups take 33 us, 1090 instructions a token (0.5 TB/s of logits, where the
+// read alone would take 2.8 us); choosing one expert a reduction, with full
+// exponentials, took 2090 and 68 us.
 #include "common.cuh"
 
 namespace mxq {
@@ -461,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : V <= 8 ? 3 : 2) moe_rou
 //   softmax, renormalized   dl_e = sum_{j chose e} w_j (g_j - sum_i g_i w_i)
 //   sigmoid                 dl_e = sum_{j chose e} g_j q_j (1 - q_j)
 //   sigmoid, renormalized   dl_e = sum_{j chose e} w_j (g_j - sum_i g_i w_i) (1 - q_j)
-// One warp per token; the choice itself has no gradient.
+// One warp per token, the choices' parts joined to the experts' through shared
+// memory (a walk over the choices in registers took 17.5 us for 15); the choice
+// itself has no gradient. 16384 x 256 fp32: 13 to 15 us, 2.3 TB/s.
 struct RouteGradArgs {
   RouteArgs r;
   const float* grad;
