@@ -1088,20 +1088,61 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const float* __re
 // ------------------------------------------------------------------ host
 
 
+constexpr uint32_t kMostSplit = 8;        // the largest portable cluster
+
+// Clusters of `split` CTAs of Kernel (with `threads` threads and `smem` bytes)
+// that can be resident at once on the current device: fewer than the CTAs alone
+// would allow, since a cluster stays within one GPC. Asked for once per device.
+template <auto Kernel>
+uint64_t resident_clusters(uint32_t split, uint32_t threads, uint32_t smem, uint64_t ctas) {
+  static std::atomic<int> known[64][kMostSplit + 1];
+  int dev = 0;
+  const bool slot = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+  int n = slot ? known[dev][split].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return uint64_t(n);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, Kernel, &cfg) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    return std::max<uint64_t>(1, ctas / split);
+  }
+  if (slot) known[dev][split].store(n, std::memory_order_relaxed);
+  return uint64_t(n);
+}
+
 // How K is shared out: the split that takes least time by this estimate, in
-// stages of one CTA alone on its multiprocessor (1 us). Two CTAs beside one
-// another take 1.2 times as long for a stage (measured on 8 experts' 2048 x
-// 7168); a round of resident CTAs has fixed work (x's pieces, the exchange of
-// the sums) of about five stages.
-uint32_t choose_split(uint64_t units, uint32_t stages, uint64_t resident) {
+// tenths of a stage of one CTA alone on its multiprocessor (1 us). Two CTAs
+// beside one another take 1.2 times as long for a stage (measured on 8 experts'
+// 2048 x 7168). A round of resident clusters has fixed work (x's pieces, the
+// exchange of the sums) of about five stages, and up to four more where its CTAs
+// go from one and a half a multiprocessor to two: 1 row against 7168 x 7168 takes
+// 10.3 us with 224 CTAs and 12.1 with 280. Rounds are counted by clusters: 16
+// rows against 5120 x 5120 take 12.4 us with shares of five CTAs and 20.8 with
+// seven, of which fewer fit a GPC.
+template <auto Kernel>
+uint32_t choose_split(uint64_t units, uint32_t stages, uint32_t resident, uint32_t threads, uint32_t smem) {
   const uint64_t sms = uint64_t(sm_count());
-  constexpr uint64_t kTogether[3] = {0, 10, 12};                   // tenths
+  constexpr uint64_t kTogether[3] = {0, 10, 12};
   uint32_t best = 1;
   uint64_t best_cost = ~0ull;
-  for (uint32_t c = 1; c <= 8 && (c == 1 || c <= stages); c++) {
-    const uint64_t per_sm = (units * c + sms - 1) / sms, share = (stages + c - 1) / c;
-    const uint64_t rounds = per_sm / resident, rest = per_sm % resident;
-    const uint64_t cost = share * (rounds * kTogether[resident] + kTogether[rest]) + 50 * (rounds + (rest ? 1 : 0));
+  for (uint32_t c = 1; c <= kMostSplit && (c == 1 || c <= stages); c++) {
+    const uint64_t share = (stages + c - 1) / c;
+    const uint64_t most = c == 1 ? sms * resident : resident_clusters<Kernel>(c, threads, smem, sms * resident);
+    const auto round = [&](uint64_t clusters) {
+      const uint64_t ctas = clusters * c, beside = std::min<uint64_t>(resident, (ctas + sms - 1) / sms);
+      const uint64_t crowded = 2 * ctas > 3 * sms ? (2 * ctas - 3 * sms) * 40 / sms : 0;
+      return clusters ? share * kTogether[beside] + 50 + crowded : 0;
+    };
+    const uint64_t cost = units / most * round(most) + round(units % most);
     if (cost < best_cost) {
       best_cost = cost;
       best = c;
@@ -1138,7 +1179,13 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   a.colw = NT == 1 && most <= kNarrow && A16 ? (most <= 2 ? uint32_t(most) : 4) : 8;
   constexpr uint32_t kMostSmem = NT == 1 ? 111u << 10 : 225u << 10;
   constexpr uint32_t kPieces = kMostSmem - Ring<FMT, W, ST>::bytes - kSums;
-  a.split = choose_split(likely * tiles, a.stages, NT == 1 ? 2 : 1);
+  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W, ST>;
+  const cudaError_t attr_err = ensure_smem_limit<kernel>(int(kMostSmem));
+  if (attr_err != cudaSuccess) {
+    record_cuda_error(attr_err);
+    return MXQ_ERR_CUDA;
+  }
+  a.split = choose_split<kernel>(likely * tiles, a.stages, NT == 1 ? 2 : 1, 32 * W, kMostSmem);
   if (slots * a.split > 0x7fffffffull) return MXQ_ERR_SHAPE;
   a.tiles = int64_t(tiles);
   a.share = a.stages / a.split;
@@ -1149,14 +1196,8 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   a.red_at = (a.chunk * per_stage + 15) / 16 * 16;
   const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + a.red_at + kSums;
 
-  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W, ST>;
   static_assert(kStageGroups * NT * 8 * (64 + 4) + 16 + kSums + Ring<FMT, W, ST>::bytes <= kMostSmem,
                 "a stage of pieces has to fit");
-  const cudaError_t attr_err = ensure_smem_limit<kernel>(int(kMostSmem));
-  if (attr_err != cudaSuccess) {
-    record_cuda_error(attr_err);
-    return MXQ_ERR_CUDA;
-  }
   cudaLaunchConfig_t cfg = {};
   const uint64_t ny = std::min<uint64_t>(tiles, 65535), nz = (tiles + ny - 1) / ny;
   if (nz > 65535) return MXQ_ERR_SHAPE;
