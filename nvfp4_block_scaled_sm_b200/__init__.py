@@ -717,6 +717,14 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+def _count(v, what: str) -> int:
+    """``v`` as the library's 32-bit count (ctypes would cut a larger one off)."""
+    v = int(v)
+    if not -2**31 <= v < 2**31:
+        raise ValueError(f"{what} must fit in 32 bits")
+    return v
+
+
 def _route_rows(logits: torch.Tensor, scoring: str):
     if scoring not in _SCORES:
         raise ValueError(f"scoring must be one of {sorted(_SCORES)}")
@@ -742,6 +750,8 @@ def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     exact scores, not of their fp32 roundings. For training,
     :func:`moe_route_backward` gives the logits' gradient (this call records
     none)."""
+    top_k, groups = _count(top_k, "top_k"), _count(groups, "groups")
+    top_groups = _count(top_groups, "top_groups")
     index = _same_device(logits)
     dt, T, E, ld, score = _route_rows(logits, scoring)
     if bias is not None:
@@ -749,12 +759,11 @@ def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
             raise TypeError("bias must be fp32 [E]")
         _same_device(logits, bias)
         bias = bias.contiguous()
-    top_k = int(top_k)
     shape = (*logits.shape[:-1], max(top_k, 0))
     weights = _empty_like(logits, shape, torch.float32)
     experts = _empty_like(logits, shape, torch.int32)
     _launch("moe_route", index, logits.data_ptr(), dt, T, E, ld, score,
-            None if bias is None else bias.data_ptr(), int(groups), int(top_groups), top_k,
+            None if bias is None else bias.data_ptr(), groups, top_groups, top_k,
             1 if renormalize else 0, float(scale), weights.data_ptr(), experts.data_ptr())
     return weights, experts
 
@@ -793,9 +802,10 @@ def moe_dispatch(experts: torch.Tensor, E: int):
     :func:`mxfp4_matvec_grouped`) follow without a copy to the host. Pairs with
     an expert outside [0, E) are dropped: they come after ``row_offsets[E]``
     and have position -1."""
+    E = _count(E, "E")
     index = _same_device(experts)
     experts = _int32(experts, index, "experts")
-    P, E = experts.numel(), int(E)
+    P = experts.numel()
     row_offsets = _empty_like(experts, (max(E, 0) + 1,), torch.int64)
     order = _empty_like(experts, (P,), torch.int32)
     positions = _empty_like(experts, experts.shape, torch.int32)

@@ -152,3 +152,14 @@ def test_python_refuses_host_tensors():
                  lambda: mxq.moe_combine(x.float(), torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, 1))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_python_refuses_counts_beyond_32_bits():
+    logits, pairs = torch.zeros(2, 64), torch.zeros(4, 2, dtype=torch.int32)
+    big = 2 ** 32 + 1                 # cut off to 1 without the check
+    for what, call in (("top_k", lambda: mxq.moe_route(logits, big)),
+                       ("groups", lambda: mxq.moe_route(logits, 2, groups=big)),
+                       ("top_groups", lambda: mxq.moe_route(logits, 2, groups=4, top_groups=big)),
+                       ("E", lambda: mxq.moe_dispatch(pairs, big))):
+        with pytest.raises(ValueError, match=f"^{what} must fit"):
+            call()
