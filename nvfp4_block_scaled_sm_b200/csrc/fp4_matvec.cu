@@ -30,7 +30,7 @@
 // left out, 64 tokens' 512 rows against 64 experts' 2048 x 7168 (MXFP4, 500 MB)
 // take 108 us, without x's pieces too 87 us (5.8 TB/s); all of it takes 198 us.
 // One row against 100003 x 4096 takes 54 us (4.0 TB/s), against 4096 x 4096
-// 7 us, of which 4 us are the start, the pieces of x and the exchange of sums.
+// 6.2 us, of which 3.5 us are the start, the pieces of x and the exchange of sums.
 // Tried and slower: x's pieces made once by a kernel before (8 rows against
 // 7168 x 7168 21 us for 18), 32 rows a warp with half the warps (the experts
 // 228 us for 198), three CTAs of 80 registers (5 to 9 %).
