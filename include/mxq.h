@@ -340,7 +340,7 @@ mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
  *          quantizers write them. K % 32 == 0 (MXFP4), K % 16 == 0 (NVFP4).
  *          Scale rows that start on 4-byte boundaries (K a multiple of 128 /
  *          64) are copied asynchronously; others are correct and slower.
- *  global_scale  device fp32 scalar, 4-byte aligned.
+ *  global_scale  device fp32 scalar, 4-byte aligned; not NULL for any K.
  *  y       [M, N] of out_dt, contiguous, 16-byte aligned; may not overlap an
  *          input. K == 0 writes zeros.
  * M, N <= 2^31 - 1, K <= 2^23. (The pages quantize the weights, "V4 mxfp4 #1372" and

@@ -1266,8 +1266,9 @@ mxq_status check_call(const Call& c, int64_t M, int64_t E, bool* done) {
     *done = true;
     return MXQ_OK;
   }
-  if (!c.y) return MXQ_ERR_NULL;
-  if (c.K > 0 && (!c.x || !c.packed || !c.scale || (FMT == kNv && !c.g))) return MXQ_ERR_NULL;
+  // (the kernel reads the global scale for every K)
+  if (!c.y || (FMT == kNv && !c.g)) return MXQ_ERR_NULL;
+  if (c.K > 0 && (!c.x || !c.packed || !c.scale)) return MXQ_ERR_NULL;
   if (!aligned16(c.x) || !aligned16(c.packed) || !aligned16(c.y) || (c.ld_x * elem_size(c.dt)) % 16 != 0)
     return MXQ_ERR_ALIGN;
   if (FMT == kNv && (reinterpret_cast<uintptr_t>(c.g) & 3u)) return MXQ_ERR_ALIGN;
