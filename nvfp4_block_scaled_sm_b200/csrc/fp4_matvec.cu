@@ -163,6 +163,23 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// NVFP4's global scale g = in(g) out(g), out a power of two: 1, or what keeps
+// the products with in(g) inside fp32's range where g lies near its ends. The
+// sums c of products that meet it are multiples of 2^-34 (2^-24 of a piece of x,
+// 2^-10 of a code and block scale) below 2^36, so |g| in [2^-92, 2^92) leaves c g
+// a finite normal number. Beyond, in(g) is in [2^56, 2^92), where a term of the
+// result is 2^-103 at least, or in [2^-92, 2^-35), where the sum of 2^23 terms
+// stays below 2^128; out(g) multiplies the finished sums.
+__device__ __forceinline__ float global_out(float g) {
+  const float m = fabsf(g);
+  if (m >= 0x1p92f) return 0x1p36f;
+  return m < 0x1p-92f && m > 0.f ? 0x1p-57f : 1.f;
+}
+__device__ __forceinline__ float global_in(float g) {
+  const float out = global_out(g);
+  return out == 1.f ? g : g * (out > 1.f ? 0x1p-36f : 0x1p57f);
+}
+
 __device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -883,13 +900,18 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
   // (a group, in further passes) as these are added up: the products of x and
   // the block-scaled codes alone may lie up to 2688 * 448 times higher than the
   // result, out of fp32's range.
+  auto global_scale = [&](int i) {
+    const bool upper = a.swiglu ? i == 1 : o0 + wrow + g + 8 * i >= half;
+    return a.g[int64_t(e) * a.g_per + (a.g_per == 2 && upper ? 1 : 0)];
+  };
   float global[2] = {1.f, 1.f};
+  bool far = false;                                                 // a scale near the ends of fp32's range
   if constexpr (FMT == kNv) {
-    const float* const gp = a.g + int64_t(e) * a.g_per;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const bool upper = a.swiglu ? i == 1 : o0 + wrow + g + 8 * i >= half;
-      global[i] = gp[a.g_per == 2 && upper ? 1 : 0];
+      const float gs = global_scale(i);
+      global[i] = global_in(gs);
+      far |= global_out(gs) != 1.f;
     }
   }
 
@@ -962,6 +984,18 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
     sweep(std::integral_constant<int, NT < 2 ? 1 : 2>{});
   } else {
     sweep(std::integral_constant<int, NT>{});
+  }
+
+  if (FMT == kNv && far) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const float out = global_out(global_scale(i));
+#pragma unroll
+      for (int n = 0; n < NA; n++) {
+        acc[n][2 * i] *= out;
+        acc[n][2 * i + 1] *= out;
+      }
+    }
   }
 
   // ---- sums of the cluster's shares: each CTA writes its sums of an output

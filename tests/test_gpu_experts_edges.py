@@ -1,0 +1,94 @@
+"""Products with 4-bit weights, the weighted sum and the router at the ends of
+their ranges. Tolerances of products count the roundings (fp4_refs.bound)."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_block_scaled_sm_b200 as mxq
+import fp4_refs as R
+from test_gpu_fp4_matvec import check_err, cuda, grouped_exact, rows, silu_mul
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+# --------------------------------------------------- NVFP4's global scales
+
+# a global scale and the size of the rows that it meets, so that the sums stay
+# within fp32's range (or below its normal range, where the bound counts
+# roundings to multiples of 2^-149)
+GLOBALS = [(1.37 * 2.0 ** 110, 2.0 ** -8), (1.91 * 2.0 ** 115, 2.0 ** -14), (1.37 * 2.0 ** 127, 2.0 ** -30),
+           (1.99 * 2.0 ** 91, 1.0), (1.01 * 2.0 ** 92, 1.0), (-1.5 * 2.0 ** 100, 1.0),
+           (1.37 * 2.0 ** -120, 1.0), (1.37 * 2.0 ** -120, 2.0 ** 100), (1.0 * 2.0 ** -92, 1.0), (1.99 * 2.0 ** -93, 1.0),
+           (1.9 * 2.0 ** -126, 2.0 ** 60), (5 * 2.0 ** -140, 2.0 ** 90), (2.0 ** -149, 2.0 ** 105), (0.0, 1.0)]
+
+
+@pytest.mark.parametrize("xd", [BF16, FP32])
+@pytest.mark.parametrize("M,N,K", [(1, 24, 544), (2, 24, 2080), (3, 20, 272), (6, 130, 1056), (20, 40, 288)])
+def test_global_scales_of_any_size(xd, M, N, K):
+    """Weights near fp32's largest value have global scales up to 2^117, and a
+    caller may give any fp32: where the result is in range, so is each step."""
+    rng = np.random.default_rng(M * 100 + K)
+    p, s = R.weight(rng, "nvfp4", N, K)
+    w = R.decode(p, s, "nvfp4")
+    base = R.f64(rows(rng, M, K, xd))
+    for g, size in GLOBALS:
+        g = float(np.float32(g))
+        x = torch.from_numpy(base * size).to(xd).cuda()
+        y = mxq.nvfp4_matvec(x, cuda(p), cuda(s), torch.tensor(g, dtype=FP32, device="cuda"), dtype=FP32)
+        exact, mag = R.product(R.f64(x), w)
+        assert mag.max() * abs(g) * 64 < np.finfo(np.float32).max
+        R.check(y, exact * g, mag * abs(g), K, f"global scale {g}")
+
+
+@pytest.mark.parametrize("xd", [BF16, FP32])
+@pytest.mark.parametrize("M", [2, 9])
+def test_global_scales_of_any_size_in_further_passes(xd, M):
+    """Rows that span more than one pass takes, with global scales at both ends."""
+    rng = np.random.default_rng(M)
+    N, K = 40, 320
+    p, s = R.weight(rng, "nvfp4", N, K)
+    w = R.decode(p, s, "nvfp4")
+    x = rng.standard_normal((M, K))
+    x[:, 1::3] *= 2.0 ** -45
+    x[:, 2::3] *= 2.0 ** -90
+    codes = np.stack([p & 15, p >> 4], -1).reshape(N, K)
+    codes[:N // 2, 0::3] = 0                                  # what is left is the small elements' alone
+    codes[:N // 4, 1::3] = 0
+    p = (codes[:, 0::2] | (codes[:, 1::2] << 4)).astype(np.uint8)
+    w = R.decode(p, s, "nvfp4")
+    for g, size in ((1.3 * 2.0 ** 108, 2.0 ** -6), (1.3 * 2.0 ** -125, 2.0 ** 110)):
+        g = float(np.float32(g))
+        xt = torch.from_numpy(x * size).to(xd).cuda()
+        y = mxq.nvfp4_matvec(xt, cuda(p), cuda(s), torch.tensor(g, dtype=FP32, device="cuda"), dtype=FP32)
+        exact, mag = R.product(R.f64(xt), w)
+        R.check(y, exact * g, mag * abs(g), K, f"global scale {g}")
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 1], [9, 0, 4]])
+def test_global_scales_of_halves_at_both_ends(counts):
+    rng = np.random.default_rng(sum(counts))
+    E, N, K = 3, 136, 288
+    p, s = R.weight(rng, "nvfp4", E, N, K)
+    w = R.decode(p, s, "nvfp4")
+    off = np.concatenate([[0], np.cumsum(counts)])
+    M = int(off[-1])
+    x = rows(rng, M, K, BF16, 0.1)
+    gs = np.array([[1.7 * 2.0 ** -100, 1.3 * 2.0 ** 105]] * E, np.float32)
+    exact, size = grouped_exact(R.f64(x), w, off, np.arange(M), gs.astype(np.float64))
+    y = mxq.nvfp4_matvec_grouped(x, cuda(p), cuda(s), cuda(gs), cuda(off), dtype=FP32)
+    R.check(y, exact, size, K, "halves")
+    h = mxq.nvfp4_matvec_grouped(x, cuda(p), cuda(s), cuda(gs), cuda(off), swiglu=True, dtype=FP32)
+    check_err(h, *silu_mul(exact, size, K), "halves, swiglu")
+
+
+def test_a_quantized_weight_near_the_largest_value():
+    """nvfp4_quantize of weights up to 2^127 leaves a global scale of 2^115: the
+    product with ordinary rows is that of the dequantized weight."""
+    rng = np.random.default_rng(40)
+    w = torch.from_numpy(rng.uniform(-1, 1, (48, 256)) * 2.0 ** 127).to(BF16).cuda()
+    p, s, g = mxq.nvfp4_quantize(w)
+    x = rows(rng, 3, 256, BF16, 2.0 ** -12)
+    exact, size = R.product(R.f64(x), R.decode(p.cpu().numpy(), s.cpu().numpy(), "nvfp4"))
+    R.check(mxq.nvfp4_matvec(x, p, s, g, dtype=FP32), exact * float(g), size * float(g), 256, "large weights")
