@@ -669,6 +669,13 @@ __device__ __noinline__ void copy_scales_edge(uint32_t dst, const uint8_t* p, in
   }
 }
 
+// silu(gate) up for gates far below zero: silu is a normal fp32 number down to
+// about -90, where e^90 is none, and up may be large enough to bring back what
+// lies far below. Kept out of the kernel's code: such gates are rare.
+__device__ __noinline__ float swiglu_far(float gate, float up) {
+  return float(double(gate) / (1.0 + exp(-double(gate))) * double(up));
+}
+
 template <int FMT, typename XT, int NT, bool A16, int W, int ST>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(const MatvecArgs a) {
   constexpr int kTileRows = 16 * W;
@@ -1060,9 +1067,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
     float v;
     if (a.swiglu) {
       const float gate = total(mi, o), up = total(mi, slice + o);
-      // silu(z) = z / (1 + e^-z); e^-z overflows to inf for z < -88, where
-      // silu is -0 to fp32's last bit
-      v = gate / (1.f + expf(-gate)) * up;
+      // silu(z) = z / (1 + e^-z); where e^-z nears fp32's largest value, in fp64
+      v = gate < -80.f ? swiglu_far(gate, up) : gate / (1.f + expf(-gate)) * up;
     } else {
       v = total(mi, o);
     }

@@ -92,3 +92,29 @@ def test_a_quantized_weight_near_the_largest_value():
     x = rows(rng, 3, 256, BF16, 2.0 ** -12)
     exact, size = R.product(R.f64(x), R.decode(p.cpu().numpy(), s.cpu().numpy(), "nvfp4"))
     R.check(mxq.nvfp4_matvec(x, p, s, g, dtype=FP32), exact * float(g), size * float(g), 256, "large weights")
+
+
+# ------------------------------------------------------------------ SwiGLU
+
+@pytest.mark.parametrize("xd", [BF16, FP32])
+def test_swiglu_of_gates_far_below_zero(xd):
+    """silu(z) is a normal fp32 number down to z = -90, and times a large up
+    projection far below that. Gate and up are one product each here, so both
+    are exact: what rounds is the exponential (two units in the last place,
+    2^-22), the sum, the quotient and the two products (2^-24 each)."""
+    z = np.concatenate([[0.0, 1.0, -1.0, -20.0, -60.0], -np.arange(72.0, 176.0, 1.0 if xd == BF16 else 0.59375)])
+    up = 1.5 * 2.0 ** 100
+    T, H, K = len(z), 8, 32
+    codes = np.zeros((1, 2 * H, K), np.uint8)
+    codes[0, :H, 0] = 2                                       # 1 x the gate's element
+    codes[0, H:, 1] = 2
+    p = (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+    s = np.full((1, 2 * H, 1), 127, np.uint8)
+    x = np.zeros((T, K))
+    x[:, 0], x[:, 1] = z, up
+    xt = torch.from_numpy(x).to(xd).cuda()
+    z = R.f64(xt)[:, :1]
+    y = R.f64(mxq.mxfp4_matvec_grouped(xt, cuda(p), cuda(s), [0, T], swiglu=True, dtype=FP32))
+    want = np.broadcast_to(z / (1 + np.exp(-z)) * up, (T, H))
+    assert np.abs(want[np.abs(z[:, 0] + 90) < 1]).min() > 1e-8
+    assert np.all(np.abs(y - want) <= 9 * 2.0 ** -24 * np.abs(want) + 2.0 ** -149)
