@@ -915,11 +915,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
   bool far = false;                                                 // a scale near the ends of fp32's range
   if constexpr (FMT == kNv) {
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const float gs = global_scale(i);
-      global[i] = global_in(gs);
-      far |= global_out(gs) != 1.f;
-    }
+    for (int i = 0; i < 2; i++) global[i] = global_scale(i);
   }
 
   constexpr int NA = NT < 2 ? 2 : NT;
@@ -950,6 +946,13 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
         __syncthreads();                                            // the last chunk has been read
         const bool left = stage_x(c_begin, n, pass);
         more |= __syncthreads_or(left) != 0;
+        if (FMT == kNv && pass == 0 && c_begin == s_begin) {        // (the scales' loads have come by now)
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            far |= global_out(global[i]) != 1.f;
+            global[i] = global_in(global[i]);
+          }
+        }
         uint32_t xg = xbase, sg = sbase;
 #pragma unroll 1
         for (uint32_t s = c_begin; s < c_begin + n; s++) {
