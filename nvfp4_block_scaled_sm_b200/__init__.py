@@ -523,6 +523,14 @@ def _same_device(x: torch.Tensor, *ts: torch.Tensor) -> int:
     return index
 
 
+def _count(v, what: str) -> int:
+    """``v`` as the library's 32-bit count (ctypes would cut a larger one off)."""
+    v = int(v)
+    if not -2**31 <= v < 2**31:
+        raise ValueError(f"{what} must fit in 32 bits")
+    return v
+
+
 _CODES = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
@@ -612,9 +620,10 @@ def _int32(t: torch.Tensor, index: int, what: str) -> torch.Tensor:
 
 def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k, swiglu, combine,
                     dtype, block: int) -> torch.Tensor:
+    top_k = _count(top_k, "top_k")
     index = _same_device(x, packed, scale)
     N, K = _weight_args(x, packed, scale, block, 3)
-    E = packed.shape[0]
+    E = _count(packed.shape[0], "E")
     if x.dim() != 2:
         raise ValueError("expected rows [R, K]")
     dt, out_dt = _code(x.dtype), _code(dtype)
@@ -622,7 +631,6 @@ def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k
     if order is not None:
         order = _int32(order, index, "order")
         R = order.numel()
-        top_k = int(top_k)
         if top_k < 1:
             raise ValueError("top_k must be at least 1")
     else:
@@ -704,7 +712,7 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
         raise ValueError("positions and weights must be [..., top_k]")
     weights = weights.contiguous()
     R, N = rows.shape
-    top_k = positions.shape[-1]
+    top_k = _count(positions.shape[-1], "top_k")
     T = positions.numel() // top_k if top_k else 0
     y = _empty_like(rows, (*positions.shape[:-1], N), dtype)
     _launch("moe_combine", index, rows.data_ptr(), R, N, positions.data_ptr(),
@@ -717,14 +725,6 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _count(v, what: str) -> int:
-    """``v`` as the library's 32-bit count (ctypes would cut a larger one off)."""
-    v = int(v)
-    if not -2**31 <= v < 2**31:
-        raise ValueError(f"{what} must fit in 32 bits")
-    return v
-
-
 def _route_rows(logits: torch.Tensor, scoring: str):
     if scoring not in _SCORES:
         raise ValueError(f"scoring must be one of {sorted(_SCORES)}")
@@ -732,7 +732,7 @@ def _route_rows(logits: torch.Tensor, scoring: str):
         raise ValueError("expected logits [..., E]")
     dt = _code(logits.dtype)
     T, E, ld = _rows_view(logits)
-    return dt, T, E, ld, _SCORES[scoring]
+    return dt, T, _count(E, "E"), ld, _SCORES[scoring]
 
 
 def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",

@@ -21,3 +21,28 @@ def test_a_global_scale_is_asked_for_without_columns_too():
         assert f(None) == NULL
         assert f(A) == CUDA                         # the checks pass, the launch fails here
     assert mxq.lib.nvfp4_matvec(None, 0, 0, 0, 0, None, None, None, 8, None, 0, None) == OK
+
+
+def test_python_refuses_counts_of_the_products_beyond_32_bits():
+    """Cut off to 1, 2^32 + 1 would be taken as another count."""
+    big = 2 ** 32 + 1
+    x, off, order = torch.zeros(2, 64), [0, 2], torch.zeros(2, dtype=torch.int32)
+    w, s = torch.zeros(1, 8, 32, dtype=torch.uint8), torch.zeros(1, 8, 4, dtype=torch.uint8)
+    for call in (lambda: mxq.mxfp4_matvec_grouped(x, w, s[..., :2].contiguous(), off, order=order, top_k=big),
+                 lambda: mxq.nvfp4_matvec_grouped(x, w, s, torch.ones(1), off, order=order, top_k=big)):
+        with pytest.raises(ValueError, match="^top_k must fit"):
+            call()
+
+
+def test_python_refuses_sizes_beyond_32_bits(monkeypatch):
+    """Sizes that come with a tensor (none of these holds any memory)."""
+    monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
+    big = 2 ** 32 + 1
+    meta = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="meta")
+    with pytest.raises(ValueError, match="^E must fit"):
+        mxq.moe_route(meta(1, big), 1)
+    with pytest.raises(ValueError, match="^E must fit"):
+        mxq.moe_route_backward(meta(1, 1), meta(1, big), meta(1, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="^E must fit"):
+        u8 = torch.uint8
+        mxq.mxfp4_matvec_grouped(meta(1, 32), meta(big, 8, 16, dtype=u8), meta(big, 8, 1, dtype=u8), [0, 1])
