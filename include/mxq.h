@@ -365,7 +365,8 @@ mxq_status nvfp4_matvec(const void* x, int dt, int64_t M, int64_t K, int64_t ld_
  *  order   NULL: x has R rows and row r is x's row r (top_k is 1 then). Or
  *          device int32 [R]: row r is x's row order[r] / top_k, the token of
  *          the pair that moe_dispatch put there; entries that lead outside
- *          x's x_rows rows count as rows of zeros.
+ *          x's x_rows rows count as rows of zeros. R == 0 does nothing, whatever
+ *          order, top_k and x_rows are.
  *  swiglu  0: y is [R, N]. 1: the first N/2 rows of a weight are the gate and
  *          the others the up projection (N even), and y [R, N/2] is
  *          gate / (1 + exp(-gate)) * up, from the fp32 sums.

@@ -1362,7 +1362,8 @@ mxq_status grouped_entry(const Call& c, int32_t E, int32_t scales_per_expert, co
   if (swiglu != 0 && swiglu != 1) return MXQ_ERR_ARG;
   if (scales_per_expert != 1 && scales_per_expert != 2) return MXQ_ERR_ARG;
   if ((swiglu || scales_per_expert == 2) && c.N % 2 != 0) return MXQ_ERR_SHAPE;
-  if (order ? top_k < 1 : (top_k != 1 || c.x_rows != R)) return MXQ_ERR_ARG;
+  // an order of no rows may be NULL: an empty array need not have an address
+  if (order ? top_k < 1 : R != 0 && (top_k != 1 || c.x_rows != R)) return MXQ_ERR_ARG;
   bool done;
   const mxq_status st = check_call<FMT>(c, R, E, &done);
   if (st != MXQ_OK || done) return st;

@@ -46,3 +46,12 @@ def test_python_refuses_sizes_beyond_32_bits(monkeypatch):
     with pytest.raises(ValueError, match="^E must fit"):
         u8 = torch.uint8
         mxq.mxfp4_matvec_grouped(meta(1, 32), meta(big, 8, 16, dtype=u8), meta(big, 8, 1, dtype=u8), [0, 1])
+
+
+def test_an_order_of_no_rows_may_be_null():
+    """A batch without tokens: an empty array need not have an address."""
+    f, g = mxq.lib.mxfp4_matvec_grouped, mxq.lib.nvfp4_matvec_grouped
+    assert f(None, 0, 0, 64, 64, A, A, 3, 8, A, 0, None, 8, 0, None, 0, None) == OK
+    assert g(None, 0, 0, 64, 64, A, A, A, 1, 3, 8, A, 0, None, 8, 1, None, 0, None) == OK
+    assert f(None, 0, 5, 64, 64, A, A, 3, 8, A, 0, None, 2, 0, None, 0, None) == OK
+    assert f(A, 0, 0, 64, 64, A, A, 3, 8, A, 4, None, 8, 0, A, 0, None) == ARG

@@ -118,3 +118,31 @@ def test_swiglu_of_gates_far_below_zero(xd):
     want = np.broadcast_to(z / (1 + np.exp(-z)) * up, (T, H))
     assert np.abs(want[np.abs(z[:, 0] + 90) < 1]).min() > 1e-8
     assert np.all(np.abs(y - want) <= 9 * 2.0 ** -24 * np.abs(want) + 2.0 ** -149)
+
+
+# ------------------------------------------------------------ lengths of zero
+
+@pytest.fixture
+def plain_allocator():
+    """torch's own allocation, under which an empty tensor has no address."""
+    prev = mxq.set_output_allocator(None)
+    yield
+    mxq.set_output_allocator(prev)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_a_layer_of_no_tokens(fmt, plain_allocator):
+    E, k, D, H = 4, 2, 64, 32
+    rng = np.random.default_rng(41)
+    p1, s1 = (cuda(a) for a in R.weight(rng, fmt, E, 2 * H, D))
+    p2, s2 = (cuda(a) for a in R.weight(rng, fmt, E, D, H))
+    g = () if fmt == "mxfp4" else (torch.ones(E, device="cuda"),)
+    f = mxq.mxfp4_matvec_grouped if fmt == "mxfp4" else mxq.nvfp4_matvec_grouped
+    x = torch.empty(0, D, dtype=BF16, device="cuda")
+    weights, experts = mxq.moe_route(torch.empty(0, E, device="cuda"), k)
+    off, order, pos = mxq.moe_dispatch(experts, E)
+    assert off.tolist() == [0] * (E + 1) and order.numel() == 0
+    h = f(x, p1, s1, *g, off, order=order, top_k=k, swiglu=True)
+    assert h.shape == (0, H)
+    y = f(h, p2, s2, *g, off, combine=(pos, weights))
+    assert y.shape == (0, D)
