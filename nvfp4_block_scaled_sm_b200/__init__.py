@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from typing import Sequence
 
@@ -713,7 +714,7 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
     weights = weights.contiguous()
     R, N = rows.shape
     top_k = _count(positions.shape[-1], "top_k")
-    T = positions.numel() // top_k if top_k else 0
+    T = math.prod(positions.shape[:-1])            # (tokens without a choice get zeros)
     y = _empty_like(rows, (*positions.shape[:-1], N), dtype)
     _launch("moe_combine", index, rows.data_ptr(), R, N, positions.data_ptr(),
             weights.data_ptr(), T, top_k, y.data_ptr(), _dtype_code(dtype))

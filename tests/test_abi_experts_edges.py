@@ -55,3 +55,14 @@ def test_an_order_of_no_rows_may_be_null():
     assert g(None, 0, 0, 64, 64, A, A, A, 1, 3, 8, A, 0, None, 8, 1, None, 0, None) == OK
     assert f(None, 0, 5, 64, 64, A, A, 3, 8, A, 0, None, 2, 0, None, 0, None) == OK
     assert f(A, 0, 0, 64, 64, A, A, 3, 8, A, 4, None, 8, 0, A, 0, None) == ARG
+
+
+def test_combine_of_no_choices_asks_for_every_token(monkeypatch):
+    """The output's rows are the library's to write (zeros), not left as allocated."""
+    calls = []
+    monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
+    monkeypatch.setattr(mxq, "_int32", lambda t, index, what: t)
+    monkeypatch.setattr(mxq, "_launch", lambda fn, index, *args: calls.append(args))
+    for shape, T in (((5, 0), 5), ((2, 3, 0), 6), ((0,), 1), ((0, 2), 0), ((4, 2), 4)):
+        y = mxq.moe_combine(torch.ones(4, 12), torch.empty(shape, dtype=torch.int32), torch.empty(shape))
+        assert y.shape == (*shape[:-1], 12) and calls[-1][5:7] == (T, shape[-1])

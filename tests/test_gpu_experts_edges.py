@@ -146,3 +146,12 @@ def test_a_layer_of_no_tokens(fmt, plain_allocator):
     assert h.shape == (0, H)
     y = f(h, p2, s2, *g, off, combine=(pos, weights))
     assert y.shape == (0, D)
+
+
+@pytest.mark.parametrize("shape", [(5, 0), (0,), (2, 3, 0)])
+@pytest.mark.parametrize("yd", [BF16, FP32])
+def test_combine_of_no_choices_is_zero(shape, yd):
+    """An empty sum (the guarded allocator fills outputs with a canary byte)."""
+    y = mxq.moe_combine(torch.ones(4, 12, device="cuda"), torch.empty(shape, dtype=torch.int32, device="cuda"),
+                        torch.empty(shape, device="cuda"), dtype=yd)
+    assert y.shape == (*shape[:-1], 12) and not y.any()
