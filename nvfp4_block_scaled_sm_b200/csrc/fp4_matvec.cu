@@ -1312,8 +1312,9 @@ mxq_status check_call(const Call& c, int64_t M, int64_t E, bool* done) {
   // (the kernel reads the global scale for every K)
   if (!c.y || (FMT == kNv && !c.g)) return MXQ_ERR_NULL;
   if (c.K > 0 && (!c.x || !c.packed || !c.scale)) return MXQ_ERR_NULL;
-  if (!aligned16(c.x) || !aligned16(c.packed) || !aligned16(c.y) || (c.ld_x * elem_size(c.dt)) % 16 != 0)
-    return MXQ_ERR_ALIGN;
+  if (!aligned16(c.y)) return MXQ_ERR_ALIGN;
+  if (c.K > 0 && (!aligned16(c.x) || !aligned16(c.packed) || (c.ld_x * elem_size(c.dt)) % 16 != 0))
+    return MXQ_ERR_ALIGN;                         // (without columns neither is read)
   if (FMT == kNv && (reinterpret_cast<uintptr_t>(c.g) & 3u)) return MXQ_ERR_ALIGN;
   (void)E;
   return MXQ_OK;

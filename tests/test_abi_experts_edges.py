@@ -66,3 +66,12 @@ def test_combine_of_no_choices_asks_for_every_token(monkeypatch):
     for shape, T in (((5, 0), 5), ((2, 3, 0), 6), ((0,), 1), ((0, 2), 0), ((4, 2), 4)):
         y = mxq.moe_combine(torch.ones(4, 12), torch.empty(shape, dtype=torch.int32), torch.empty(shape))
         assert y.shape == (*shape[:-1], 12) and calls[-1][5:7] == (T, shape[-1])
+
+
+def test_rows_without_columns_need_no_alignment():
+    """The row stride of a contiguous [M, 0] tensor is 1."""
+    for x, ld in ((None, 1), (A + 2, 3)):
+        assert mxq.lib.mxfp4_matvec(x, 0, 3, 0, ld, None, None, 8, A, 0, None) == CUDA
+        assert mxq.lib.nvfp4_matvec(x, 1, 3, 0, ld, None, None, A, 8, A, 0, None) == CUDA
+    assert mxq.lib.mxfp4_matvec(None, 0, 3, 0, 1, None, None, 8, A + 8, 0, None) == ALIGN
+    assert mxq.lib.mxfp4_matvec(A + 2, 0, 3, 32, 40, A, A, 8, A, 0, None) == ALIGN

@@ -155,3 +155,14 @@ def test_combine_of_no_choices_is_zero(shape, yd):
     y = mxq.moe_combine(torch.ones(4, 12, device="cuda"), torch.empty(shape, dtype=torch.int32, device="cuda"),
                         torch.empty(shape, device="cuda"), dtype=yd)
     assert y.shape == (*shape[:-1], 12) and not y.any()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("xd", [BF16, FP32])
+def test_no_columns_in_contiguous_rows(fmt, xd):
+    p = torch.empty(8, 0, dtype=torch.uint8, device="cuda")
+    x = torch.empty(3, 0, dtype=xd, device="cuda")
+    args = () if fmt == "mxfp4" else (torch.ones((), device="cuda"),)
+    f = mxq.mxfp4_matvec if fmt == "mxfp4" else mxq.nvfp4_matvec
+    y = f(x, p, p, *args, dtype=FP32)
+    assert y.shape == (3, 8) and not y.any()
