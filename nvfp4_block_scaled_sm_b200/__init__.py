@@ -173,10 +173,10 @@ def _rows_view(x: torch.Tensor):
             raise ValueError("the last dimension must be contiguous")
         return M, N, ld if M > 1 else N
     N = x.shape[-1]
-    if dims == 1:
-        return 1, N, N
     if N > 1 and x.stride(-1) != 1:
         raise ValueError("the last dimension must be contiguous")
+    if dims == 1:
+        return 1, N, N
     M = 1
     for s in x.shape[:-1]:
         M *= s

@@ -75,3 +75,15 @@ def test_rows_without_columns_need_no_alignment():
         assert mxq.lib.nvfp4_matvec(x, 1, 3, 0, ld, None, None, A, 8, A, 0, None) == CUDA
     assert mxq.lib.mxfp4_matvec(None, 0, 3, 0, 1, None, None, 8, A + 8, 0, None) == ALIGN
     assert mxq.lib.mxfp4_matvec(A + 2, 0, 3, 32, 40, A, A, 8, A, 0, None) == ALIGN
+
+
+def test_one_row_with_a_stride_is_refused():
+    """A column of a matrix is one row whose elements lie apart."""
+    base = torch.zeros(8, 4)
+    for x in (base[:, 1], base[0, ::2], base[:, 1:2], base.t(), base.t()[None]):
+        if x.dim() == 2 and x.shape[-1] == 1:
+            assert mxq._rows_view(x) == (8, 1, 4)
+            continue
+        with pytest.raises(ValueError, match="contiguous"):
+            mxq._rows_view(x)
+    assert mxq._rows_view(base[3]) == (1, 4, 4) and mxq._rows_view(base[:1, 0]) == (1, 1, 1)

@@ -166,3 +166,12 @@ def test_no_columns_in_contiguous_rows(fmt, xd):
     f = mxq.mxfp4_matvec if fmt == "mxfp4" else mxq.nvfp4_matvec
     y = f(x, p, p, *args, dtype=FP32)
     assert y.shape == (3, 8) and not y.any()
+
+
+def test_a_column_as_one_row_is_refused():
+    base = torch.zeros(64, 32, device="cuda")
+    p, s = torch.zeros(4, 32, dtype=torch.uint8, device="cuda"), torch.zeros(4, 2, dtype=torch.uint8, device="cuda")
+    for call in (lambda: mxq.mxfp4_matvec(base[:, 1], p, s), lambda: mxq.moe_route(base[:, 1], 2),
+                 lambda: mxq.mxfp8_quantize(base[:, 1]), lambda: mxq.mxfp4_quantize(base.to(BF16)[:, 0])):
+        with pytest.raises(ValueError, match="contiguous"):
+            call()
