@@ -724,6 +724,7 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
 # ------------------------------------------------------ routing to experts
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_MOST_TOP_K, _MOST_EXPERTS = 32, 1024           # MXQ_ROUTE_MAX_TOP_K, MXQ_GROUPED_MAX_EXPERTS
 
 
 def _route_rows(logits: torch.Tensor, scoring: str):
@@ -760,7 +761,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
             raise TypeError("bias must be fp32 [E]")
         _same_device(logits, bias)
         bias = bias.contiguous()
-    shape = (*logits.shape[:-1], max(top_k, 0))
+    shape = (*logits.shape[:-1], min(max(top_k, 0), _MOST_TOP_K))    # (the library refuses others)
     weights = _empty_like(logits, shape, torch.float32)
     experts = _empty_like(logits, shape, torch.int32)
     _launch("moe_route", index, logits.data_ptr(), dt, T, E, ld, score,
@@ -807,7 +808,7 @@ def moe_dispatch(experts: torch.Tensor, E: int):
     index = _same_device(experts)
     experts = _int32(experts, index, "experts")
     P = experts.numel()
-    row_offsets = _empty_like(experts, (max(E, 0) + 1,), torch.int64)
+    row_offsets = _empty_like(experts, (min(max(E, 0), _MOST_EXPERTS) + 1,), torch.int64)   # (as above)
     order = _empty_like(experts, (P,), torch.int32)
     positions = _empty_like(experts, experts.shape, torch.int32)
     need = _fn["mxq_moe_dispatch_workspace_bytes"](P, E) if P > 4096 else 0

@@ -87,3 +87,30 @@ def test_one_row_with_a_stride_is_refused():
         with pytest.raises(ValueError, match="contiguous"):
             mxq._rows_view(x)
     assert mxq._rows_view(base[3]) == (1, 4, 4) and mxq._rows_view(base[:1, 0]) == (1, 1, 1)
+
+
+def test_refused_counts_allocate_no_outputs_of_their_size(monkeypatch):
+    """The library refuses the count; an output of that size may not fit."""
+    sizes = []
+
+    def allocate(shape, dtype, device):
+        sizes.append(torch.Size(shape).numel())
+        return torch.empty(min(sizes[-1], 4096), dtype=dtype)[:sizes[-1]].view(shape)
+
+    def launch(fn, index, *args):
+        mxq._check(fn, getattr(mxq.lib, fn)(*args, None))
+
+    monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
+    monkeypatch.setattr(mxq, "_int32", lambda t, index, what: t)
+    monkeypatch.setattr(mxq, "_launch", launch)
+    prev = mxq.set_output_allocator(allocate)
+    try:
+        for call in (lambda: mxq.moe_route(torch.zeros(4, 64), 2 ** 31 - 1), lambda: mxq.moe_route(torch.zeros(4, 64), 33),
+                     lambda: mxq.moe_route(torch.zeros(4, 64), -1), lambda: mxq.moe_dispatch(torch.zeros(4, 2, dtype=torch.int32), 2 ** 31 - 1),
+                     lambda: mxq.moe_dispatch(torch.zeros(4, 2, dtype=torch.int32), 1025),
+                     lambda: mxq.moe_dispatch(torch.zeros(4, 2, dtype=torch.int32), -1)):
+            with pytest.raises(mxq.MxqError, match="status 2"):
+                call()
+    finally:
+        mxq.set_output_allocator(prev)
+    assert max(sizes) <= 1025
