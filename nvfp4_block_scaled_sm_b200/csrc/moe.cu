@@ -105,6 +105,9 @@ template <typename F>
 __device__ __forceinline__ F exp_from(F l, F top) { return l == top ? F(1) : exp_of(l - top); }
 // The same for the weights and gradients.
 __device__ __forceinline__ float weight_from(float l, float top) { return l == top ? 1.f : expf(l - top); }
+// 1 / (1 + e^-l). Below -80 the 1 is far under e^-l's last bit, and e^-l soon has
+// no fp32 value where e^l still has one.
+__device__ __forceinline__ float sigmoid(float l) { return l < -80.f ? expf(l) : 1.f / (1.f + expf(-l)); }
 
 // The choice of one token in fp64: ordered keys (0: not there or left out);
 // lane j gets the j-th chosen expert in *id. One key a round.
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : V <= 8 ? 3 : 2) moe_rou
       if (a.renormalize) sum = warp_sum(w);
       w = sum > 0.f ? w / sum : 0.f;
     } else if (lj > neg_inf()) {
-      w = 1.f / (1.f + expf(-lj));
+      w = sigmoid(lj);
     }
     if (a.scoring == kSigmoid && a.renormalize) {
       // where every chosen score is small, all are taken e^-top times larger
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
         c = q * (g - minus);
       }
     } else {
-      const float q = 1.f / (1.f + expf(-lj)), other = 1.f / (1.f + expf(lj));   // p and 1 - p
+      const float q = sigmoid(lj), other = sigmoid(-lj);         // p and 1 - p
       if (a.renormalize) {
         float w = lj > neg_inf() ? (top < 0.f ? expf(lj - top) * other : q) : 0.f;
         const float sum = warp_sum(w);
