@@ -353,13 +353,14 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Scales are copied for several stages at a time (16 bytes of a row or more):
-// two blocks of 16 rows a warp. A block is overwritten when the second one
-// after it is begun, which is ST - 1 stages ahead of the reader.
-template <int FMT, int ST>
+// Scales are copied for two stages at a time (16 bytes of a row or more): two
+// blocks of 16 rows a warp. A block is overwritten when the second one after it
+// is begun, which is kRingStages - 1 stages ahead of the reader.
+constexpr int kRingStages = 3;
+template <int FMT>
 struct ScaleBlock {
-  static constexpr int stages = ST == 3 ? 2 : 4;
-  static_assert(ST - 1 <= stages, "two blocks do not cover the stages in flight");
+  static constexpr int stages = 2;
+  static_assert(kRingStages - 1 <= stages, "two blocks do not cover the stages in flight");
   static constexpr int stage = FMT == kMx ? 8 : 16;              // bytes of a row in one stage
   static constexpr int row = stages * stage;
   static constexpr int bytes = 16 * row;
@@ -370,11 +371,11 @@ struct ScaleBlock {
 // of the stage's first group at this lane's place; sx: their scales at this
 // lane's columns, sx_group bytes from group to group; even: all eight groups of
 // a column have the same one (the first pass).
-template <int FMT, int ST, int NC, int NA>
+template <int FMT, int NC, int NA>
 __device__ __forceinline__ void stage_math(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t xf,
                                            uint32_t xf_group, uint32_t sx, uint32_t sx_group, bool even,
                                            const float (&global)[2], int lane) {
-  constexpr int kRow = ScaleBlock<FMT, ST>::row;
+  constexpr int kRow = ScaleBlock<FMT>::row;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t rowA = codes + g * kRowPitch + t * 4, rowB = rowA + 8 * kRowPitch;
   float c[NC][4];
@@ -517,11 +518,11 @@ __device__ __forceinline__ void add_scaled(float (&acc)[4], const float (&c)[4],
 //              tiles of B for x's columns 2n and 2n + 1.
 // acc[n][i]: row g (i < 2) or g + 8. x0: x's pieces of this stage's first
 // group; zero: a place of zeros.
-template <int FMT, int ST, int COLS, int NA>
+template <int FMT, int COLS, int NA>
 __device__ __forceinline__ void stage_narrow(float (&acc)[NA][4], uint32_t codes, uint32_t scales, uint32_t x0,
                                              uint32_t x_group, uint32_t zero, uint32_t sx, uint32_t sx_group,
                                              const float (&global)[2], int lane) {
-  constexpr int kRow = ScaleBlock<FMT, ST>::row;
+  constexpr int kRow = ScaleBlock<FMT>::row;
   constexpr int NC = COLS <= 2 ? 1 : 2;
   const int g = lane >> 2, t = lane & 3;
   const bool diagonal = (g & 3) == t;
@@ -624,10 +625,10 @@ __device__ __forceinline__ void stage_narrow(float (&acc)[NA][4], uint32_t codes
   }
 }
 
-// Bytes of the warps' rings of ST stages of codes and two blocks of scales.
-template <int FMT, int W, int ST>
+// Bytes of the warps' rings of stages of codes and two blocks of scales.
+template <int FMT, int W>
 struct Ring {
-  static constexpr int warp = ST * kWarpTile + 2 * ScaleBlock<FMT, ST>::bytes;
+  static constexpr int warp = kRingStages * kWarpTile + 2 * ScaleBlock<FMT>::bytes;
   static constexpr int bytes = W * warp;
 };
 
@@ -676,12 +677,13 @@ __device__ __noinline__ float swiglu_far(float gate, float up) {
   return float(double(gate) / (1.0 + exp(-double(gate))) * double(up));
 }
 
-template <int FMT, typename XT, int NT, bool A16, int W, int ST>
+template <int FMT, typename XT, int NT, bool A16, int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(const MatvecArgs a) {
   constexpr int kTileRows = 16 * W;
+  constexpr int ST = kRingStages;
   constexpr int P = Pieces<XT>::n;
   constexpr uint32_t TT = 8 * NT / P;                  // rows of x in a tile
-  using Scales = ScaleBlock<FMT, ST>;
+  using Scales = ScaleBlock<FMT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int32_t found[3 + W];
   __shared__ const XT* source[TT];
@@ -732,7 +734,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
   const int64_t last = outs - (o0 + wrow);                          // outputs from the warp's first on
   const int64_t lastB = a.swiglu ? last : last - 8;                 // rows of the second eight
 
-  const uint32_t ring = smem_ptr(smem) + warp * Ring<FMT, W, ST>::warp;
+  const uint32_t ring = smem_ptr(smem) + warp * Ring<FMT, W>::warp;
   const uint32_t scale_ring = ring + ST * kWarpTile;
   const uint32_t s_begin = rank * a.share + min(rank, a.longer);
   const uint32_t s_end = s_begin + a.share + (rank < a.longer ? 1 : 0);
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
 
   // ---- x pieces of a chunk of stages, in shared memory: [group][column][32]
   // fp16 and [group][8] scales of each n-tile
-  const uint32_t xbase = smem_ptr(smem) + Ring<FMT, W, ST>::bytes;
+  const uint32_t xbase = smem_ptr(smem) + Ring<FMT, W>::bytes;
   const uint32_t gstride = NT == 1 ? a.colw * 64 : NT * 512;        // bytes of one group's pieces
   const uint32_t sbase = xbase + a.chunk * kStageGroups * gstride;
   const uint32_t sstride = NT == 1 ? a.colw * 4 : NT * 32;          // bytes of one group's scales
@@ -968,10 +970,10 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) fp4_matvec_kernel(cons
           const uint32_t scales =
               scale_ring + (s / Scales::stages & 1) * Scales::bytes + s % Scales::stages * Scales::stage;
           if constexpr (FORM < 0)
-            stage_narrow<FMT, ST, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, global,
+            stage_narrow<FMT, -FORM, NA>(acc, codes, scales, xg, gstride, zero, sg, sstride, global,
                                               lane);
           else
-            stage_math<FMT, ST, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride, pass == 0,
+            stage_math<FMT, FORM, NA>(acc, codes, scales, xg + lane_x, gstride, sg + t * 8, sstride, pass == 0,
                                           global, lane);
           xg += kStageGroups * gstride;
           sg += kStageGroups * sstride;
@@ -1199,7 +1201,7 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   // one n-tile: two CTAs of 8 warps a multiprocessor, 128 registers a thread
   // (three of 80 registers took 5 to 9 % more instructions and time); more: one
   // of 16 warps, whose 256 rows share the x pieces
-  constexpr int W = NT == 1 ? 8 : 16, ST = 3;
+  constexpr int W = NT == 1 ? 8 : 16;
   // the sums: a slice is rounded up, by one output (two weight rows) a CTA at
   // most
   constexpr uint32_t kSums = 8 * NT * (16 * W + 8 * 2) * 4;
@@ -1221,8 +1223,8 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   const uint64_t most = std::min<uint64_t>(TT, uint64_t(a.M)) * P;
   a.colw = NT == 1 && most <= kNarrow && A16 ? (most <= 2 ? uint32_t(most) : 4) : 8;
   constexpr uint32_t kMostSmem = NT == 1 ? 111u << 10 : 225u << 10;
-  constexpr uint32_t kPieces = kMostSmem - Ring<FMT, W, ST>::bytes - kSums;
-  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W, ST>;
+  constexpr uint32_t kPieces = kMostSmem - Ring<FMT, W>::bytes - kSums;
+  constexpr auto kernel = fp4_matvec_kernel<FMT, XT, NT, A16, W>;
   const cudaError_t attr_err = ensure_smem_limit<kernel>(int(kMostSmem));
   if (attr_err != cudaSuccess) {
     record_cuda_error(attr_err);
@@ -1237,9 +1239,9 @@ mxq_status launch_matvec(MatvecArgs a, cudaStream_t stream) {
   const uint32_t share = a.share + (a.longer ? 1 : 0);
   a.chunk = std::max(1u, std::min(share, kPieces / per_stage));
   a.red_at = (a.chunk * per_stage + 15) / 16 * 16;
-  const size_t smem = size_t(Ring<FMT, W, ST>::bytes) + a.red_at + kSums;
+  const size_t smem = size_t(Ring<FMT, W>::bytes) + a.red_at + kSums;
 
-  static_assert(kStageGroups * NT * 8 * (64 + 4) + 16 + kSums + Ring<FMT, W, ST>::bytes <= kMostSmem,
+  static_assert(kStageGroups * NT * 8 * (64 + 4) + 16 + kSums + Ring<FMT, W>::bytes <= kMostSmem,
                 "a stage of pieces has to fit");
   cudaLaunchConfig_t cfg = {};
   const uint64_t ny = std::min<uint64_t>(tiles, 65535), nz = (tiles + ny - 1) / ny;
@@ -1299,7 +1301,7 @@ constexpr int64_t kMostRows = 0x7fffffff, kMostK = 1 << 23;
 // The checks that one weight and the experts' weights share; MXQ_OK with
 // *done set when there is nothing to do.
 template <int FMT>
-mxq_status check_call(const Call& c, int64_t M, int64_t E, bool* done) {
+mxq_status check_call(const Call& c, int64_t M, bool* done) {
   constexpr int kBlock = FMT == kMx ? 32 : 16;
   *done = false;
   if (!valid_dtype(c.dt) || !valid_dtype(c.out_dt)) return MXQ_ERR_DTYPE;
@@ -1316,7 +1318,6 @@ mxq_status check_call(const Call& c, int64_t M, int64_t E, bool* done) {
   if (c.K > 0 && (!aligned16(c.x) || !aligned16(c.packed) || (c.ld_x * elem_size(c.dt)) % 16 != 0))
     return MXQ_ERR_ALIGN;                         // (without columns neither is read)
   if (FMT == kNv && (reinterpret_cast<uintptr_t>(c.g) & 3u)) return MXQ_ERR_ALIGN;
-  (void)E;
   return MXQ_OK;
 }
 
@@ -1350,7 +1351,7 @@ MatvecArgs make_args(const Call& c, int64_t M) {
 template <int FMT>
 mxq_status matvec_entry(const Call& c, mxq_stream_t stream) {
   bool done;
-  const mxq_status st = check_call<FMT>(c, c.x_rows, 1, &done);
+  const mxq_status st = check_call<FMT>(c, c.x_rows, &done);
   if (st != MXQ_OK || done) return st;
   return launch_fp4<FMT>(make_args<FMT>(c, c.x_rows), c.dt, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -1366,7 +1367,7 @@ mxq_status grouped_entry(const Call& c, int32_t E, int32_t scales_per_expert, co
   // an order of no rows may be NULL: an empty array need not have an address
   if (order ? top_k < 1 : R != 0 && (top_k != 1 || c.x_rows != R)) return MXQ_ERR_ARG;
   bool done;
-  const mxq_status st = check_call<FMT>(c, R, E, &done);
+  const mxq_status st = check_call<FMT>(c, R, &done);
   if (st != MXQ_OK || done) return st;
   if (!row_offsets) return MXQ_ERR_NULL;
   if ((reinterpret_cast<uintptr_t>(row_offsets) & 7u) || (reinterpret_cast<uintptr_t>(order) & 3u))
