@@ -114,3 +114,20 @@ def test_refused_counts_allocate_no_outputs_of_their_size(monkeypatch):
     finally:
         mxq.set_output_allocator(prev)
     assert max(sizes) <= 1025
+
+
+def test_global_scales_in_another_order_are_refused(monkeypatch):
+    """[2, E] holds the values of [E, 2] in another order: read as they lie, an
+    expert would get another's scales."""
+    calls = []
+    monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
+    monkeypatch.setattr(mxq, "_launch", lambda fn, index, *args: calls.append(args))
+    x, E = torch.zeros(3, 64, dtype=torch.bfloat16), 3
+    w, s = torch.zeros(E, 8, 32, dtype=torch.uint8), torch.zeros(E, 8, 4, dtype=torch.uint8)
+    for shape in ((2, E), (1, 2, E), (2 * E, 1)):
+        with pytest.raises(ValueError, match=r"must be \[E, 2\]"):
+            mxq.nvfp4_matvec_grouped(x, w, s, torch.ones(shape), [0, 1, 2, 3])
+    assert not calls
+    for shape, per in (((E,), 1), ((E, 1), 1), ((E, 2), 2), ((2 * E,), 2)):
+        mxq.nvfp4_matvec_grouped(x, w, s, torch.ones(shape), [0, 1, 2, 3])
+        assert calls[-1][8] == per
