@@ -329,9 +329,10 @@ mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
  *   y[m, n] = global_scale sum_k x[m, k] decode(packed[n, k])
  *                                decode_e4m3(block_scale[n, k/16])
  * The products of x and the codes are exact for every x (an fp32 x keeps all
- * its bits), they are summed in fp32 (groups of 32 by the tensor cores), and
- * y is rounded once. The order of the sum is fixed: repeated calls give
- * identical bytes. Infinities and NaNs of x, NaN block scales and the E8M0
+ * its bits), they are summed in fp32 (16 to 256 at a time by the tensor cores),
+ * and y is rounded once. global_scale multiplies these sums; one of any size
+ * keeps them in fp32's range where y is. The order of the sum is fixed: repeated
+ * calls give identical bytes. Infinities and NaNs of x, NaN block scales and the E8M0
  * byte 255 act as in that formula (inf * 0 is NaN).
  *  x       [M, K] of dt, row stride ld_x elements. Any M: rows are taken 8,
  *          16 or 32 at a time (a third of that for fp32), and each such tile
@@ -411,9 +412,10 @@ mxq_status moe_combine(const float* rows, int64_t R, int64_t N, const int32_t* p
  *           expert), and the choice is among the experts of the top_groups
  *           best groups (ties to the lowest group);
  *   weight  scale * p, or with renormalize scale * p / (sum of the chosen p).
- * The bias counts for the choice only. The choice is that of the exact p +
- * bias, not of their fp32 roundings (differences that fp32 cannot tell are
- * taken again in fp64). NaN logits count as -inf, NaN sums with a bias as the
+ * The bias counts for the choice only. The choice is that of p + bias in fp64,
+ * not of its fp32 roundings (differences that fp32 cannot tell are taken again
+ * in fp64; sums that fp64 cannot tell apart are ties); without a bias and groups
+ * it is that of the logits. NaN logits count as -inf, NaN sums with a bias as the
  * lowest; +inf logits share the softmax equally. Where the chosen p are all
  * zero (a row of -inf), the weights are zero.
  *  logits   [T, E] bf16 or fp32 (dt), row stride ld elements (ld >= E), no

@@ -583,7 +583,8 @@ def mxfp4_matvec(x: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
     ``packed`` [N, K/2] and ``scale`` [N, K/32] as :func:`mxfp4_quantize`
     returns them. Returns y [..., N] as ``dtype``: exact products of x and the
     decoded weight, summed in fp32, rounded once. Made for the few rows of
-    decoding; more rows are right and read the weight again every 8 to 32."""
+    decoding; more rows are right and read the weight again every 8 to 32.
+    Records no gradient: y is detached from an x that requires one."""
     return _matvec("mxfp4_matvec", x, packed, scale, None, dtype, 32)
 
 
@@ -682,7 +683,8 @@ def mxfp4_matvec_grouped(x: torch.Tensor, packed: torch.Tensor, scale: torch.Ten
     is [..., N].
 
     Returns [R, N] (see above) as ``dtype``. Rows that belong to no expert
-    (dropped pairs) are not written: what they hold is undefined."""
+    (dropped pairs) are not written: what they hold is undefined. Records no
+    gradient, for ``x`` or for the weights of ``combine``."""
     return _matvec_grouped("mxfp4_matvec_grouped", x, packed, scale, None, row_offsets, order, top_k,
                            swiglu, combine, dtype, 32)
 
@@ -704,7 +706,7 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
     """Each token's rows added up with its router weights, in fp32:
     ``y[t] = sum_j weights[t, j] * rows[positions[t, j]]`` for fp32 ``rows``
     [R, N]; a position outside [0, R) (:func:`moe_dispatch`'s -1) adds nothing.
-    Returns [..., N] as ``dtype``."""
+    Returns [..., N] as ``dtype``; records no gradient."""
     index = _same_device(rows, positions, weights)
     if rows.dtype != torch.float32 or weights.dtype != torch.float32:
         raise TypeError("rows and weights must be fp32")
@@ -751,7 +753,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
     best of that many consecutive groups of experts, a group's score being the
     sum of its two largest p + bias. Weights are ``scale`` times p, divided by
     the sum of the chosen p with ``renormalize``. The choice is that of the
-    exact scores, not of their fp32 roundings. For training,
+    scores in fp64, not of their fp32 roundings. For training,
     :func:`moe_route_backward` gives the logits' gradient (this call records
     none)."""
     top_k, groups = _count(top_k, "top_k"), _count(groups, "groups")

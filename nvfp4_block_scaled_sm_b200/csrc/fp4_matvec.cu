@@ -29,11 +29,16 @@
 // What bounds it: instructions issued, then memory. With the MMAs and scales
 // left out, 64 tokens' 512 rows against 64 experts' 2048 x 7168 (MXFP4, 500 MB)
 // take 108 us, without x's pieces too 87 us (5.8 TB/s); all of it takes 198 us.
-// One row against 100003 x 4096 takes 54 us (4.0 TB/s), against 4096 x 4096
-// 6.2 us, of which 3.5 us are the start, the pieces of x and the exchange of sums.
-// Tried and slower: x's pieces made once by a kernel before (8 rows against
-// 7168 x 7168 21 us for 18), 32 rows a warp with half the warps (the experts
-// 228 us for 198), three CTAs of 80 registers (5 to 9 %).
+// One row against 100003 x 4096 takes 56 us (3.9 TB/s), against 4096 x 4096
+// 6.9 us, of which 3.5 us are the start, the pieces of x and the exchange of sums.
+// A row that spans too much for one pass costs the CTAs that meet it their share
+// of the weight once more, and all their sums by groups: 8 rows against 7168 x 7168
+// take 38.5 us for 14.3, one row 17 for 10.7.
+// Tried and slower: 32 rows a warp with half the warps (the experts 228 us for
+// 198), three CTAs of 80 registers (5 to 9 %). x's pieces made once by a kernel
+// before, in a first version of this one: faster for the experts (64 tokens 210 us
+// for 227), slower for single weights (8 rows against 7168 x 7168 21 us for 18);
+// not taken up again since.
 #include <type_traits>
 
 #include "common.cuh"

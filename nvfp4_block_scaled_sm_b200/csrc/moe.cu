@@ -8,15 +8,20 @@
 // token, lane i the experts i V .. i V + V - 1, all in registers: one read of
 // the logits, no shared memory.
 //
-// The choice is that of the real numbers p + bias, not of their fp32 roundings
-// (neighbouring scores are often closer than fp32's error, and the choice
-// would then hang on the order of a sum). Without a bias the order of p is
-// that of the logits, which are compared as they are. With one, keys are
-// formed in fp32 with a bound on their error; a token whose choice some
-// difference below that bound could turn takes the same steps again in fp64.
+// The choice is that of p + bias in fp64, not of its fp32 roundings (neighbouring
+// scores are often closer than fp32's error, and the choice would then hang on
+// the order of a sum). Without a bias the order of p is that of the logits, which
+// are compared as they are. With one, keys are formed in fp32 with a bound on
+// their error; a token whose choice some difference below that bound could turn
+// takes the same steps again in fp64. So does a token with more than 32 keys
+// above the bound of choose_quick: of random ones none at top_k = 8 of 64 to 1024
+// or of 4 of 8 groups of 256, one in two thousand at 16 of 256, but most where the
+// keys lie in few lanes or top_k is large (84 % at 16 of one group of two of 256,
+// 92 % at 24 of 256, all at 32). 16384 tokens of 256 experts, sigmoid with a bias:
+// 31 us at top_k = 8, 38 at 16, 86 at 16 of one group of two, 96 at 24, 116 at 32.
 //
 // Bound by instructions: 16384 tokens of 256 experts with a bias and 4 of 8
-// groups take 33 us, 1090 instructions a token (0.5 TB/s of logits, where the
+// groups take 34 us, 1090 instructions a token (0.5 TB/s of logits, where the
 // read alone would take 2.8 us); choosing one expert a reduction, with full
 // exponentials, took 2090 and 68 us.
 #include "common.cuh"
@@ -471,7 +476,9 @@ __global__ void __launch_bounds__(kThreads, V <= 4 ? 4 : V <= 8 ? 3 : 2) moe_rou
 //   sigmoid, renormalized   dl_e = sum_{j chose e} w_j (g_j - sum_i g_i w_i) (1 - q_j)
 // One warp per token, the choices' parts joined to the experts' through shared
 // memory (a walk over the choices in registers took 17.5 us for 15); the choice
-// itself has no gradient. 16384 x 256 fp32: 13 to 15 us, 2.3 TB/s.
+// itself has no gradient. 16384 x 256 fp32: 13.6 us from memory (2.5 TB/s), 11.4
+// where L2 holds the logits. Only the plain softmax needs the whole row; the
+// other forms read it too (11.8 to 13.2 us).
 struct RouteGradArgs {
   RouteArgs r;
   const float* grad;
@@ -598,8 +605,8 @@ __global__ void __launch_bounds__(kThreads) moe_route_backward_kernel(const Rout
 // outside [0, E)). Up to 4096 ids one CTA does all of it; more are cut into
 // chunks, one a CTA: a first kernel ranks each id among its chunk's and counts
 // the chunk's buckets, a second adds up the counts of the chunks before and
-// places the ids (128 x 8 pairs of 256 experts on one cluster of 8 CTAs with
-// the counts in distributed shared memory took 24 us, in two kernels 12).
+// places the ids (131072 pairs of 256 experts on one cluster of 8 CTAs with
+// the counts in distributed shared memory took 24 us, in two kernels 11.4).
 //
 // Inside a CTA each warp takes a contiguous piece, 32 ids a walk: lanes with
 // the same id are found by a vote for each bit of it (11 votes at most;
