@@ -524,6 +524,9 @@ def _same_device(x: torch.Tensor, *ts: torch.Tensor) -> int:
     return index
 
 
+_MOST_TOP_K, _MOST_EXPERTS = 32, 1024           # MXQ_ROUTE_MAX_TOP_K, MXQ_GROUPED_MAX_EXPERTS
+
+
 def _count(v, what: str) -> int:
     """``v`` as the library's 32-bit count (ctypes would cut a larger one off)."""
     v = int(v)
@@ -622,10 +625,13 @@ def _int32(t: torch.Tensor, index: int, what: str) -> torch.Tensor:
 
 def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k, swiglu, combine,
                     dtype, block: int) -> torch.Tensor:
-    top_k = _count(top_k, "top_k")
+    if order is not None:
+        top_k = _count(top_k, "top_k")
     index = _same_device(x, packed, scale)
     N, K = _weight_args(x, packed, scale, block, 3)
-    E = _count(packed.shape[0], "E")
+    E = packed.shape[0]
+    if E > _MOST_EXPERTS:
+        _count(E, "E")                             # (others are the library's to refuse)
     if x.dim() != 2:
         raise ValueError("expected rows [R, K]")
     dt, out_dt = _code(x.dtype), _code(dtype)
@@ -646,10 +652,11 @@ def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k
     if scales is not None:
         if scales.dtype != torch.float32 or scales.numel() not in (E, 2 * E):
             raise TypeError("global_scales must be fp32 with one or two values per expert")
-        if scales.numel() != E and scales.dim() > 1 and scales.shape[-1] != 2:
+        per = scales.numel() // E
+        if per == 2 and scales.dim() > 1 and scales.shape[-1] != 2:
             raise ValueError("two global scales per expert must be [E, 2]")
         scales = scales.to(x.device).contiguous()
-        g = (scales.data_ptr(), scales.numel() // E)
+        g = (scales.data_ptr(), per)
     outs = N // 2 if swiglu else N
     if combine is not None:
         positions, weights = combine
@@ -728,7 +735,6 @@ def moe_combine(rows: torch.Tensor, positions: torch.Tensor, weights: torch.Tens
 # ------------------------------------------------------ routing to experts
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
-_MOST_TOP_K, _MOST_EXPERTS = 32, 1024           # MXQ_ROUTE_MAX_TOP_K, MXQ_GROUPED_MAX_EXPERTS
 
 
 def _route_rows(logits: torch.Tensor, scoring: str):
@@ -738,7 +744,9 @@ def _route_rows(logits: torch.Tensor, scoring: str):
         raise ValueError("expected logits [..., E]")
     dt = _code(logits.dtype)
     T, E, ld = _rows_view(logits)
-    return dt, T, _count(E, "E"), ld, _SCORES[scoring]
+    if E > _MOST_EXPERTS:
+        _count(E, "E")                             # (others are the library's to refuse)
+    return dt, T, E, ld, _SCORES[scoring]
 
 
 def moe_route(logits: torch.Tensor, top_k: int, *, scoring: str = "softmax",
