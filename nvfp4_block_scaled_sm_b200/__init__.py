@@ -652,7 +652,7 @@ def _matvec_grouped(fn: str, x, packed, scale, scales, row_offsets, order, top_k
     if scales is not None:
         if scales.dtype != torch.float32 or scales.numel() not in (E, 2 * E):
             raise TypeError("global_scales must be fp32 with one or two values per expert")
-        per = scales.numel() // E
+        per = 2 if scales.numel() > E else 1
         if per == 2 and scales.dim() > 1 and scales.shape[-1] != 2:
             raise ValueError("two global scales per expert must be [E, 2]")
         scales = scales.to(x.device).contiguous()

@@ -131,3 +131,14 @@ def test_global_scales_in_another_order_are_refused(monkeypatch):
     for shape, per in (((E,), 1), ((E, 1), 1), ((E, 2), 2), ((2 * E,), 2)):
         mxq.nvfp4_matvec_grouped(x, w, s, torch.ones(shape), [0, 1, 2, 3])
         assert calls[-1][8] == per
+
+
+def test_a_stack_of_no_experts_is_refused_by_the_library(monkeypatch):
+    monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
+    monkeypatch.setattr(mxq, "_launch", lambda fn, index, *args: mxq._check(fn, getattr(mxq.lib, fn)(*args, None)))
+    x = torch.zeros(3, 64, dtype=torch.bfloat16)
+    w, s = torch.zeros(0, 8, 32, dtype=torch.uint8), torch.zeros(0, 8, 4, dtype=torch.uint8)
+    with pytest.raises(mxq.MxqError, match="status 2"):
+        mxq.nvfp4_matvec_grouped(x, w, s, torch.ones(0), [0])
+    with pytest.raises(mxq.MxqError, match="status 2"):
+        mxq.mxfp4_matvec_grouped(x, w, s[..., :2].contiguous(), [0])
