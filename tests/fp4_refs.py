@@ -56,9 +56,14 @@ def bound(exact, size, K: int, bf16: bool):
     additions, each taken as off by 2^-22, four times the unit roundoff, for
     truncating hardware), scaled by two roundings and added to one of K / 32
     partial sums in fp32 (2^-24 each), which at most 8 more additions join;
-    bf16 outputs round once more by half a step, 2^-8 of the value. Below
-    fp32's normal range a rounding is off by 2^-150 instead: one for each block
-    of 16 at most (three where x has three pieces), besides the 8 + 2."""
+    bf16 outputs round once more by half a step, 2^-8 of the value. NVFP4's
+    general form sums 256 products in a chain of 16 MMAs instead: an MMA that
+    cuts off the sum of its 16 products and the accumulator once is off by
+    2^-23 of it, taken as 2^-21, which makes the same 32 2^-22 (sums of one
+    sign, where each cut goes the same way, are off by 40 2^-24 at most in
+    measurement). Below fp32's normal range a rounding is off by 2^-150
+    instead: one for each block of 16 at most (three where x has three pieces),
+    besides the 8 + 2."""
     acc = (32 * 2.0 ** -22 + (K / 32 + 10) * 2.0 ** -24) * size + (3 * K / 16 + 10) * 2.0 ** -150
     return acc + (2.0 ** -8 * (np.abs(exact) + acc) + 2.0 ** -134 if bf16 else 0)
 

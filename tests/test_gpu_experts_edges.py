@@ -175,3 +175,69 @@ def test_a_column_as_one_row_is_refused():
                  lambda: mxq.mxfp8_quantize(base[:, 1]), lambda: mxq.mxfp4_quantize(base.to(BF16)[:, 0])):
         with pytest.raises(ValueError, match="contiguous"):
             call()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("xd", [BF16, FP32])
+@pytest.mark.parametrize("M", [1, 4, 8, 30])
+def test_sums_of_one_sign(fmt, xd, M):
+    """What the tensor cores cut off of a sum goes one way: nothing cancels."""
+    rng = np.random.default_rng(M)
+    for K in (256, 4096):
+        p, s = R.weight(rng, fmt, 96, K)
+        p &= 0x77                                             # no signs
+        x = torch.from_numpy(np.abs(rng.standard_normal((M, K)))).to(xd).cuda()
+        args = () if fmt == "mxfp4" else (torch.ones((), device="cuda"),)
+        f = mxq.mxfp4_matvec if fmt == "mxfp4" else mxq.nvfp4_matvec
+        R.check(f(x, cuda(p), cuda(s), *args, dtype=FP32), *R.product(R.f64(x), R.decode(p, s, fmt)), K, f"{fmt} one sign")
+
+
+# ------------------------------------------------------------ first calls
+
+FIRST_CALLS = """
+import sys
+import torch
+import nvfp4_block_scaled_sm_b200 as mxq
+
+torch.manual_seed(0)
+E, k, D, H, T = 8, 2, 256, 64, {T}
+x = torch.randn(T, D, device="cuda").to(torch.bfloat16)
+logits, bias = torch.randn(T, E, device="cuda"), torch.randn(E, device="cuda") * 0.1
+p1 = torch.randint(0, 256, (E, 2 * H, D // 2), dtype=torch.uint8, device="cuda")
+s1 = torch.randint(118, 124, (E, 2 * H, D // 32), dtype=torch.uint8, device="cuda")
+p2 = torch.randint(0, 256, (E, D, H // 2), dtype=torch.uint8, device="cuda")
+s2 = torch.randint(40, 90, (E, D, H // 16), dtype=torch.uint8, device="cuda")
+g2 = torch.full((E,), 0.01, device="cuda")
+
+
+def layer():
+    w, e = mxq.moe_route(logits, k, scoring="sigmoid", bias=bias)
+    off, order, pos = mxq.moe_dispatch(e, E)
+    h = mxq.mxfp4_matvec_grouped(x, p1, s1, off, order=order, top_k=k, swiglu=True)
+    y = mxq.nvfp4_matvec_grouped(h, p2, s2, g2, off, combine=(pos, w))
+    return y, mxq.moe_route_backward(w, logits, e, scoring="sigmoid"), mxq.mxfp4_matvec(x, p1[0], s1[0])
+
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = layer()
+graph.replay()
+torch.cuda.synchronize()
+captured = [t.clone() for t in captured]
+for a, b in zip(captured, layer()):
+    assert torch.equal(a, b)
+print("first calls ok")
+"""
+
+
+@pytest.mark.parametrize("T", [3, 3000])
+def test_first_calls_of_a_process_inside_a_capture(T):
+    """Nothing that a first call sets up (limits of shared memory, queries of
+    the device) needs an eager call before."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(mxq.__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(T=T)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first calls ok" in r.stdout, r.stderr[-2000:]
