@@ -320,6 +320,141 @@ mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
                       const uint8_t* sb_swz, int64_t M, int64_t N, int64_t K, void* d,
                       int out_dt, int32_t* error_flag, mxq_stream_t stream);
 
+/* ------------------------------------------------ experts' MXFP8 products */
+
+/* The experts' products for rows sorted by expert, on the tensor cores
+ * (tcgen05 kind::mxf8f6f4.block_scale): for the rows r of expert e,
+ * row_offsets[e] <= r < row_offsets[e + 1],
+ *   D[r, n] = sum_k decode(qa[r, k]) 2^(sa[r, k/32] - 127)
+ *                 * decode(qb[e, n, k]) 2^(sb[e, n, k/32] - 127),
+ * products exact, accumulated in fp32 in an order of the hardware's choosing
+ * (the same for every call with the same arguments).
+ *  qa      [M, K] uint8 E4M3 codes of the sorted rows.
+ *  sa_swz  each expert's scales in its own 128x4 tiles, expert after expert,
+ *          as mxfp8_quantize_grouped_swizzled writes them for these offsets;
+ *          sa_bytes is the array's size, a multiple of 512 and at least
+ *          mxq_swizzled_scale_bytes(M, K/32). Nothing behind it is read.
+ *  qb      [E, N, K] uint8 codes of the experts' weights, sb_swz their scales,
+ *          mxq_swizzled_scale_bytes(N, K/32) bytes an expert
+ *          (mxfp8_quantize_grouped_swizzled of the stack). Weights of experts
+ *          without rows are not read. The rows' gradients are the same product
+ *          with the weights of mxfp8_quantize_columnwise_stacked.
+ *  row_offsets  DEVICE int64 [E + 1], 8-byte aligned. The first is taken as 0;
+ *          the others are clamped into a rising sequence within M. Experts may
+ *          be empty. Rows from the last offset on belong to no expert: their
+ *          rows of d are left as they were. 1 <= E <= MXQ_GROUPED_MAX_EXPERTS.
+ *  swiglu  0, or 1: the first N/2 rows of each weight are the gate, the others
+ *          the up projection, and d [M, N/2] is silu(gate) * up, computed from
+ *          the fp32 sums and rounded once.
+ *  d       [M, N] (or [M, N/2]) row-major, bf16 or fp32 (out_dt).
+ *  error_flag  as for mxfp8_gemm.
+ * K % 32 == 0; N % 16 == 0, with swiglu N % 256 == 0 (each half is whole scale
+ * tiles); pointers 16-byte aligned. K == 0 writes zeros into the experts' rows.
+ * M, N, K and E * N are below 2^31 - 256, and the scales of either side below
+ * 2^38 bytes. One launch of persistent CTAs of 320 threads: pairs over 256 x
+ * 256 output tiles when the experts have more than 128 rows on average, single
+ * CTAs over 128 x 256 tiles otherwise (128 x 128 when those are too few for
+ * the multiprocessors). */
+mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t sa_bytes,
+                              const uint8_t* qb, const uint8_t* sb_swz, int32_t E,
+                              const int64_t* row_offsets, int64_t M, int64_t N, int64_t K, int swiglu,
+                              void* d, int out_dt, int32_t* error_flag, mxq_stream_t stream);
+
+/* Columns of the transposed codes of E experts with M_total rows in all, each
+ * expert padded to a multiple of 128: floor((M_total + 127 E) / 128) * 128;
+ * -1 for negative sizes. */
+int64_t mxq_grouped_padded_rows(int32_t E, int64_t M_total);
+
+/* MXFP8 of the experts' rows in groups of 32 consecutive rows of one column
+ * and one expert, transposed: the operands of mxfp8_gemm_grouped_wgrad.
+ *  x            [M_total, N] bf16 or fp32 (dt), rows sorted by expert, row
+ *               stride ld_x elements; N % 16 == 0.
+ *  row_offsets  as for mxfp8_gemm_grouped (M = M_total).
+ *  qweight_t    [N, P] uint8 E4M3 codes, P = mxq_grouped_padded_rows(E,
+ *               M_total): expert e's rows are the columns from P_e on, P_0 = 0
+ *               and P_e+1 = P_e + its rows rounded up to a multiple of 128.
+ *               Columns of no row count as zeros (code 0x00; a group without
+ *               rows has byte 127).
+ *  scale_swz    mxq_swizzled_scale_bytes(N, P/32) bytes: the scales [N, P/32]
+ *               in 128x4 tiles.
+ * The groups' rule is that of mxfp8_quantize. One launch. */
+mxq_status mxfp8_quantize_columnwise_grouped(const void* x, int dt, int32_t E,
+                                             const int64_t* row_offsets, int64_t M_total, int64_t N,
+                                             int64_t ld_x, uint8_t* qweight_t, uint8_t* scale_swz,
+                                             mxq_stream_t stream);
+
+/* The same for a stack of E weights x [E, R, N] (contiguous; R % 32 == 0,
+ * N % 16 == 0): each expert's transpose, qweight_t [E, N, R], and its scales
+ * [N, R/32] in tiles of its own, scale_swz E * mxq_swizzled_scale_bytes(N,
+ * R/32) bytes: the weights that give the rows' gradients in
+ * mxfp8_gemm_grouped. One launch. */
+mxq_status mxfp8_quantize_columnwise_stacked(const void* x, int dt, int32_t E, int64_t R, int64_t N,
+                                             uint8_t* qweight_t, uint8_t* scale_swz,
+                                             mxq_stream_t stream);
+
+/* The experts' products over their rows, the gradients of their weights:
+ *   D[e, a, b] = sum over expert e's rows r of A[r, a] B[r, b]
+ * with A and B the values of codes and scales as
+ * mxfp8_quantize_columnwise_grouped leaves them for the same offsets (products
+ * exact, fp32 sums).
+ *  qa_t [Na, P], sa_swz its scales; qb_t [Nb, P], sb_swz its scales;
+ *  P % 128 == 0 (mxq_grouped_padded_rows), Nb % 16 == 0.
+ *  row_offsets  as above; columns from P on are not read, whatever the offsets.
+ *  d       [E, Na, Nb] row-major, bf16 or fp32; experts without rows get zeros.
+ *  error_flag  as for mxfp8_gemm.
+ * Limits and launch as for mxfp8_gemm_grouped (pairs of CTAs when Na > 128 and
+ * Nb > 128, otherwise 128 x 128 tiles). */
+mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, const uint8_t* qb_t,
+                                    const uint8_t* sb_swz, int32_t E, const int64_t* row_offsets,
+                                    int64_t P, int64_t Na, int64_t Nb, void* d, int out_dt,
+                                    int32_t* error_flag, mxq_stream_t stream);
+
+/* ------------------------------------- norm with an MXFP8 output, gradient */
+
+/* Root-mean-square norm of rows, quantized to MXFP8 in the same pass:
+ *   h = x, or x + residual (fp32 sum rounded to x's type)
+ *   rstd = fp32(1 / sqrt(mean(h^2) + eps)), squares and mean in fp64
+ *   y = fp32(fp32(h * rstd) * weight)
+ * and qweight, scale = mxfp8_quantize's rule on the fp32 y (never rounded to
+ * 16 bits on the way).
+ *  x, residual  [M, N] bf16 or fp32 (dt, both), row strides ld_x and ld_res
+ *               elements; residual may be NULL.
+ *  weight       [N] bf16 or fp32 (weight_dt).
+ *  hidden       with a residual: [M, N] of dt, receives h (it may be x or
+ *               residual itself where that is compact; no other outputs may
+ *               overlap inputs). NULL without one.
+ *  qweight [M, N], scale [M, N/32], scale_swz NULL or the scales in 128x4
+ *               tiles: as for mxfp8_quantize.
+ *  normed       NULL, or [M, N] of dt: y rounded to nearest even.
+ *  rstd         [M] fp32, for mxq_rmsnorm_backward.
+ * N % 32 == 0, eps >= 0. One launch. */
+mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld_x, const void* residual,
+                         int64_t ld_res, const void* weight, int weight_dt, double eps, void* hidden,
+                         uint8_t* qweight, uint8_t* scale, uint8_t* scale_swz, void* normed, float* rstd,
+                         mxq_stream_t stream);
+
+/* Gradient of the norm (of y, as if y were not quantized):
+ *   dx = grad_hidden + rstd (g w - h rstd^2 mean(g w h)),
+ *   dweight = sum over the rows of g h rstd,
+ * computed in fp32.
+ *  grad    [M, N] of dt, row stride ld_g: the gradient of y.
+ *  hidden  [M, N] of dt, row stride ld_h: h; rstd [M] as the norm left it.
+ *  grad_hidden  NULL, or [M, N] of dt, row stride ld_gh: the gradient that
+ *          reaches h on another way, added to dx.
+ *  dx      [M, N] of dt, compact (it may be grad or grad_hidden itself where
+ *          that is compact). With a residual it is the gradient of both summands.
+ *  dweight [N] of weight_dt, or NULL (not computed).
+ *  workspace  with dweight: mxq_rmsnorm_backward_workspace_bytes(M, N) bytes,
+ *          16-byte aligned, no initialization needed; not shared by calls that
+ *          may overlap.
+ * N % 8 == 0. Two launches (one without dweight). */
+size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
+mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, int64_t ld_g,
+                                const void* hidden, int64_t ld_h, const void* weight, int weight_dt,
+                                const float* rstd, const void* grad_hidden, int64_t ld_gh, void* dx,
+                                void* dweight, void* workspace, size_t workspace_bytes,
+                                mxq_stream_t stream);
+
 /* ------------------------------------- products with weights in 4 bits */
 
 /* y = x W^T for the weights that mxfp4_quantize and nvfp4_quantize leave,

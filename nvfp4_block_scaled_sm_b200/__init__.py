@@ -18,7 +18,7 @@ import ctypes
 import functools
 import math
 import os
-from typing import Sequence
+from typing import NamedTuple, Sequence
 
 import torch
 
@@ -26,7 +26,8 @@ __all__ = [
     "MxqError", "lib", "library_path",
     "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped", "mxfp8_quantize_columnwise",
     "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_quantize_grouped", "mx_fake_quantize",
-    "mxfp8_gemm",
+    "mxfp8_gemm", "mxfp8_gemm_grouped", "mxfp8_gemm_grouped_wgrad",
+    "mxfp8_quantize_columnwise_grouped", "RmsNorm", "mxfp8_rmsnorm", "rmsnorm_backward",
     "mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
     "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
     "nvfp4_amax", "nvfp4_quantize", "nvfp4_dequantize",
@@ -103,7 +104,20 @@ def _load() -> ctypes.CDLL:
     L.moe_dispatch.argtypes = [vp, i64, i32, vp, vp, vp, vp, sz, vp]
     L.mxq_moe_dispatch_workspace_bytes.argtypes = [i64, i32]
     L.mxq_moe_dispatch_workspace_bytes.restype = sz
-    for f in ("mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
+    f64 = ctypes.c_double
+    L.mxq_grouped_padded_rows.argtypes, L.mxq_grouped_padded_rows.restype = [i32, i64], i64
+    L.mxfp8_gemm_grouped.argtypes = [vp, vp, i64, vp, vp, i32, vp, i64, i64, i64, i32, vp, i32, vp, vp]
+    L.mxfp8_gemm_grouped_wgrad.argtypes = [vp, vp, vp, vp, i32, vp, i64, i64, i64, vp, i32, vp, vp]
+    L.mxfp8_quantize_columnwise_grouped.argtypes = [vp, i32, i32, vp, i64, i64, i64, vp, vp, vp]
+    L.mxfp8_quantize_columnwise_stacked.argtypes = [vp, i32, i32, i64, i64, vp, vp, vp]
+    L.mxfp8_rmsnorm.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, f64, vp, vp, vp, vp, vp, vp, vp]
+    L.mxq_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.mxq_rmsnorm_backward_workspace_bytes.restype = sz
+    L.mxq_rmsnorm_backward.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i32, vp, vp, i64, vp, vp, vp,
+                                       sz, vp]
+    for f in ("mxfp8_gemm_grouped", "mxfp8_gemm_grouped_wgrad", "mxfp8_quantize_columnwise_grouped",
+              "mxfp8_quantize_columnwise_stacked", "mxfp8_rmsnorm", "mxq_rmsnorm_backward",
+              "mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
               "moe_combine", "moe_route", "moe_route_backward", "moe_dispatch",
               "mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped",
               "mxfp8_quantize_grouped_swizzled", "mxfp8_quantize_grouped_ptrs",
@@ -830,6 +844,250 @@ def moe_dispatch(experts: torch.Tensor, E: int):
     return row_offsets, order, positions
 
 
+# ------------------------------------------------ experts' MXFP8 products
+
+def _bytes(t: torch.Tensor, what: str) -> torch.Tensor:
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        raise TypeError(f"{what} must be contiguous uint8 tensors")
+    return t
+
+
+def _error_flag(error_flag, index: int):
+    if error_flag is None:
+        return None
+    if error_flag.dtype is not torch.int32 or error_flag.numel() < 1:
+        raise TypeError("error_flag must be an int32 CUDA tensor")
+    if error_flag.get_device() != index:
+        raise ValueError("tensors must live on one CUDA device")
+    return error_flag.data_ptr()
+
+
+def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Tensor,
+                       sb_swizzled: torch.Tensor, row_offsets, dtype: torch.dtype = torch.bfloat16, *,
+                       swiglu: bool = False, error_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """The experts' products in MXFP8 on the tensor cores, for rows sorted by
+    expert: row r of the result is row r of ``qa`` times the weight of the expert
+    e with ``row_offsets[e] <= r < row_offsets[e + 1]``.
+
+    ``qa`` [M, K] and ``sa_swizzled``: the codes of the sorted rows and each
+    expert's scales in tiles of its own, as ``mxfp8_quantize_grouped(x,
+    row_offsets=..., swizzled=True)`` returns them for these offsets. ``qb`` [E,
+    N, K] and ``sb_swizzled``: a stack of weights,
+    ``mxfp8_quantize_grouped(w, swizzled=True)``; with the stack of
+    :func:`mxfp8_quantize_columnwise_grouped` the product is the gradient of the
+    rows. ``row_offsets``: E + 1 offsets from 0, int64 on the device (as
+    :func:`moe_dispatch` returns them; clamped to the rows), or a list.
+    ``swiglu=True``: the first N/2 rows of each weight are the gate, the others
+    the up projection (N a multiple of 256), and the result [M, N/2] is
+    silu(gate) * up, rounded once. ``error_flag`` as for :func:`mxfp8_gemm`.
+
+    Returns [M, N] (or [M, N/2]) as ``dtype``. Rows that belong to no expert are
+    not written: what they hold is undefined. Records no gradient."""
+    index = _same_device(qa, sa_swizzled, qb, sb_swizzled)
+    for t in (qa, sa_swizzled, qb, sb_swizzled):
+        _bytes(t, "codes and scales")
+    if qa.dim() != 2 or qb.dim() != 3 or qa.shape[1] != qb.shape[2]:
+        raise ValueError("expected qa [M, K] and qb [E, N, K]")
+    (M, K), (E, N) = qa.shape, qb.shape[:2]
+    _count(E, "E")
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    if swiglu and N % 256:
+        raise ValueError("halves of an expert need whole scale tiles: N a multiple of 256")
+    if sb_swizzled.numel() < E * swizzled_scale_bytes(N, K // 32):
+        raise ValueError("swizzled scales are smaller than the operands need")
+    offsets = _device_offsets(qa, row_offsets, E, M)
+    if not isinstance(row_offsets, torch.Tensor) or not row_offsets.is_cuda:
+        host = [int(v) for v in row_offsets]
+        if host and host[0] != 0:
+            raise ValueError("row_offsets must start at 0")
+        need = sum(swizzled_scale_bytes(b - a, K // 32) for a, b in zip(host[:-1], host[1:]))
+    else:
+        need = swizzled_scale_bytes(M, K // 32)          # whatever the experts' padding adds
+    if sa_swizzled.numel() < need:
+        raise ValueError("swizzled scales are smaller than the operands need")
+    flag = _error_flag(error_flag, index)
+    d = _empty_like(qa, (M, N // 2 if swiglu else N), dtype)
+    _launch("mxfp8_gemm_grouped", index, qa.data_ptr(), sa_swizzled.data_ptr(),
+            sa_swizzled.numel() // 512 * 512, qb.data_ptr(), sb_swizzled.data_ptr(), E,
+            offsets.data_ptr(), M, N, K, 1 if swiglu else 0, d.data_ptr(), _code(dtype), flag)
+    return d
+
+
+def mxfp8_quantize_columnwise_grouped(xs: torch.Tensor, *, row_offsets=None):
+    """MXFP8 of experts' transposes, the operands of their gradients, in one
+    launch: groups of 32 consecutive rows of one expert's column.
+
+    ``xs`` [M_total, N] with ``row_offsets`` (as for :func:`mxfp8_gemm_grouped`):
+    rows sorted by expert. Returns ``(qweight_t, scale_swizzled)`` for
+    :func:`mxfp8_gemm_grouped_wgrad`: uint8 [N, P] codes, each expert's rows as
+    columns from a multiple of 128 on (P the most that this padding can come to;
+    columns of no row are zeros), and the scales [N, P/32] in 128x4 tiles.
+
+    ``xs`` [E, R, N] without offsets: a stack of weights (R a multiple of 32).
+    Returns uint8 [E, N, R] codes and each expert's scales [N, R/32] in tiles of
+    its own: the stack for the rows' gradients in :func:`mxfp8_gemm_grouped`."""
+    index = _same_device(xs)
+    dt = _code(xs.dtype)
+    if row_offsets is None:
+        if xs.dim() != 3:
+            raise ValueError("expected a stack [E, R, N], or rows [M_total, N] with row_offsets")
+        if not xs.is_contiguous():
+            raise ValueError("the stacked tensor must be contiguous")
+        E, R, N = xs.shape
+        _count(E, "E")
+        if R % 32 or N % 16:
+            raise ValueError("expected R a multiple of 32 and N of 16")
+        q = _empty_like(xs, (E, N, R), torch.uint8)
+        s = _empty_like(xs, (E * swizzled_scale_bytes(N, R // 32),), torch.uint8)
+        _launch("mxfp8_quantize_columnwise_stacked", index, xs.data_ptr(), dt, E, R, N, q.data_ptr(),
+                s.data_ptr())
+        return q, s
+    if xs.dim() != 2:
+        raise ValueError("row_offsets go with a 2-D [M_total, N] tensor")
+    M, N, ld = _rows_view(xs)
+    E = (row_offsets.numel() if isinstance(row_offsets, torch.Tensor) else len(row_offsets)) - 1
+    if not 1 <= E <= _MOST_EXPERTS:
+        raise ValueError(f"row_offsets must have 2 to {_MOST_EXPERTS + 1} entries")
+    if N % 16:
+        raise ValueError("N must be a multiple of 16")
+    offsets = _device_offsets(xs, row_offsets, E, M)
+    P = int(lib.mxq_grouped_padded_rows(E, M))
+    q = _empty_like(xs, (N, P), torch.uint8)
+    s = _empty_like(xs, (swizzled_scale_bytes(N, P // 32),), torch.uint8)
+    _launch("mxfp8_quantize_columnwise_grouped", index, xs.data_ptr(), dt, E, offsets.data_ptr(), M, N,
+            ld, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def mxfp8_gemm_grouped_wgrad(qa_t: torch.Tensor, sa_swizzled: torch.Tensor, qb_t: torch.Tensor,
+                             sb_swizzled: torch.Tensor, row_offsets,
+                             dtype: torch.dtype = torch.bfloat16, *,
+                             error_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradients of the experts' weights in MXFP8 on the tensor cores:
+    ``D[e] = A_e^T B_e`` over expert e's rows, from A's and B's transposes as
+    :func:`mxfp8_quantize_columnwise_grouped` returns them for the same
+    ``row_offsets``: ``qa_t`` [Na, P], ``qb_t`` [Nb, P] and their scales. With A
+    the gradient of an experts' product and B its rows, D is the gradient of the
+    weights [E, Na, Nb].
+
+    Returns [E, Na, Nb] as ``dtype``; experts without rows get zeros."""
+    index = _same_device(qa_t, sa_swizzled, qb_t, sb_swizzled)
+    for t in (qa_t, sa_swizzled, qb_t, sb_swizzled):
+        _bytes(t, "codes and scales")
+    if qa_t.dim() != 2 or qb_t.dim() != 2 or qa_t.shape[1] != qb_t.shape[1]:
+        raise ValueError("expected qa_t [Na, P] and qb_t [Nb, P]")
+    (Na, P), Nb = qa_t.shape, qb_t.shape[0]
+    if P % 128 or Nb % 16:
+        raise ValueError("expected P a multiple of 128 and Nb of 16")
+    E = (row_offsets.numel() if isinstance(row_offsets, torch.Tensor) else len(row_offsets)) - 1
+    if not 1 <= E <= _MOST_EXPERTS:
+        raise ValueError(f"row_offsets must have 2 to {_MOST_EXPERTS + 1} entries")
+    if sa_swizzled.numel() < swizzled_scale_bytes(Na, P // 32) or \
+            sb_swizzled.numel() < swizzled_scale_bytes(Nb, P // 32):
+        raise ValueError("swizzled scales are smaller than the operands need")
+    offsets = _device_offsets(qa_t, row_offsets, E, P)
+    flag = _error_flag(error_flag, index)
+    d = _empty_like(qa_t, (E, Na, Nb), dtype)
+    _launch("mxfp8_gemm_grouped_wgrad", index, qa_t.data_ptr(), sa_swizzled.data_ptr(), qb_t.data_ptr(),
+            sb_swizzled.data_ptr(), E, offsets.data_ptr(), P, Na, Nb, d.data_ptr(), _code(dtype), flag)
+    return d
+
+
+# ------------------------------------------- norm with an MXFP8 output
+
+class RmsNorm(NamedTuple):
+    """Results of :func:`mxfp8_rmsnorm`; None where not asked for."""
+    qweight: torch.Tensor                  # uint8 E4M3 codes, shaped like x
+    scale: torch.Tensor                    # uint8 E8M0 bytes [..., N/32]
+    scale_swizzled: torch.Tensor | None    # the scales in 128x4 tiles, flat
+    hidden: torch.Tensor                   # x + residual in x's dtype; x itself without a residual
+    rstd: torch.Tensor                     # fp32 [...]: 1 / rms of each row
+    normed: torch.Tensor | None            # y, rounded to x's dtype
+
+
+def mxfp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                  residual: torch.Tensor | None = None, swizzled: bool = False,
+                  normed: bool = False) -> RmsNorm:
+    """Root-mean-square norm of the rows of a bf16/fp32 tensor, with the
+    residual's addition before it, quantized to MXFP8 in the same pass:
+
+    ``h = x + residual`` (rounded to x's dtype), ``rstd = 1 / sqrt(mean(h^2) +
+    eps)`` (the mean in fp64, rounded to fp32), ``y = (h * rstd) * weight`` in
+    fp32, and the codes and scales are :func:`mxfp8_quantize`'s of that fp32 y.
+    ``x`` and ``residual`` [..., N] share shape and dtype, N a multiple of 32;
+    ``weight`` [N] is bf16 or fp32. ``swizzled=True`` adds the scales in 128x4
+    tiles (for :func:`mxfp8_gemm`), ``normed=True`` y itself in x's dtype.
+    Returns an :class:`RmsNorm`. Records no gradient: :func:`rmsnorm_backward`
+    computes it."""
+    index = _same_device(x, weight)
+    dt, wdt = _code(x.dtype), _code(weight.dtype)
+    M, N, ld = _rows_view(x)
+    if weight.dim() != 1 or weight.shape[0] != N or not weight.is_contiguous():
+        raise ValueError(f"expected a contiguous weight of {N} elements")
+    if N % 32:
+        raise ValueError("N must be a multiple of 32")
+    lead = x.shape[:-1]
+    hidden, ld_res = x, 0
+    if residual is not None:
+        _same_device(x, residual)
+        if residual.shape != x.shape or residual.dtype is not x.dtype:
+            raise ValueError("residual must have x's shape and dtype")
+        ld_res = _rows_view(residual)[2]
+        hidden = _empty_like(x, x.shape, x.dtype)
+    q = _empty_like(x, x.shape, torch.uint8)
+    s = _empty_like(x, (*lead, N // 32), torch.uint8)
+    swz = _empty_like(x, (swizzled_scale_bytes(M, N // 32),), torch.uint8) if swizzled else None
+    y = _empty_like(x, x.shape, x.dtype) if normed else None
+    rstd = _empty_like(x, lead, torch.float32)
+    if N == 0:
+        rstd.fill_(float(eps) ** -0.5 if eps > 0 else math.inf)      # the mean of nothing is 0
+    _launch("mxfp8_rmsnorm", index, x.data_ptr(), dt, M, N, ld,
+            None if residual is None else residual.data_ptr(), ld_res, weight.data_ptr(), wdt, float(eps),
+            None if residual is None else hidden.data_ptr(), q.data_ptr(), s.data_ptr(),
+            None if swz is None else swz.data_ptr(), None if y is None else y.data_ptr(), rstd.data_ptr())
+    return RmsNorm(q, s, swz, hidden, rstd, y)
+
+
+def rmsnorm_backward(grad: torch.Tensor, hidden: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
+                     grad_hidden: torch.Tensor | None = None):
+    """The norm's gradient, as if its output were not quantized: ``grad`` [...,
+    N] is the gradient of y, ``hidden`` and ``rstd`` are what
+    :func:`mxfp8_rmsnorm` returned, ``weight`` [N] its weight, and
+    ``grad_hidden`` the gradient that reaches h on another way (the residual
+    stream), added to the result.
+
+    Returns ``(grad_x, grad_weight)``: the gradient of h, and so of x and of
+    the residual, like ``hidden``; the weight's like ``weight``. Computed in
+    fp32; the sum over the rows has a fixed order. N a multiple of 8."""
+    index = _same_device(grad, hidden, weight, rstd)
+    dt, wdt = _code(hidden.dtype), _code(weight.dtype)
+    M, N, ld_h = _rows_view(hidden)
+    if weight.dim() != 1 or weight.shape[0] != N or not weight.is_contiguous():
+        raise ValueError(f"expected a contiguous weight of {N} elements")
+    if N % 8:
+        raise ValueError("N must be a multiple of 8")
+    if rstd.dtype is not torch.float32 or rstd.shape != hidden.shape[:-1] or not rstd.is_contiguous():
+        raise TypeError("rstd must be contiguous fp32, one value a row")
+    lds = []
+    for t in (grad, grad_hidden):
+        if t is None:
+            lds.append(0)
+            continue
+        _same_device(hidden, t)
+        if t.shape != hidden.shape or t.dtype is not hidden.dtype:
+            raise ValueError("the gradients must have hidden's shape and dtype")
+        lds.append(_rows_view(t)[2])
+    dx = _empty_like(hidden, hidden.shape, hidden.dtype)
+    dw = _empty_like(hidden, (N,), weight.dtype)
+    n = int(lib.mxq_rmsnorm_backward_workspace_bytes(M, N))
+    work = _empty_like(hidden, (n,), torch.uint8)
+    _launch("mxq_rmsnorm_backward", index, grad.data_ptr(), dt, M, N, lds[0], hidden.data_ptr(), ld_h,
+            weight.data_ptr(), wdt, rstd.data_ptr(), None if grad_hidden is None else grad_hidden.data_ptr(),
+            lds[1], dx.data_ptr(), dw.data_ptr(), work.data_ptr(), n)
+    return dx, dw
+
+
 def check_bounded_wait(timeout_ns: int = 2_000_000, device=None) -> dict:
     """Runs the self-check of the GEMM's bounded barrier wait on a CUDA device
     (``mxq_check_bounded_wait``): a wait on a barrier that nothing arrives on
@@ -1048,6 +1306,8 @@ def _traced(fn):
 for _name in ("mxfp8_quantize", "mxfp8_dequantize", "mxfp8_quantize_grouped",
               "mxfp8_quantize_columnwise", "mxfp4_quantize", "mxfp4_dequantize",
               "mxfp4_quantize_grouped", "mx_fake_quantize", "mxfp8_gemm", "nvfp4_amax",
+              "mxfp8_gemm_grouped", "mxfp8_gemm_grouped_wgrad", "mxfp8_quantize_columnwise_grouped",
+              "mxfp8_rmsnorm", "rmsnorm_backward",
               "mxfp4_matvec", "nvfp4_matvec", "mxfp4_matvec_grouped", "nvfp4_matvec_grouped",
               "moe_route", "moe_route_backward", "moe_dispatch", "moe_combine",
               "nvfp4_quantize", "nvfp4_dequantize", "nvfp4_amax_sliced", "nvfp4_quantize_sliced",

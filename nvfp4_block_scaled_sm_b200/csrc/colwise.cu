@@ -88,7 +88,60 @@ struct ColArgs {
   bool q_t_aligned;      // every q_t row start is 16-byte aligned (M % 16 == 0)
   bool scale_words;      // scale_t 4-byte aligned and ceil(M/32) % 4 == 0
   bool row_scale_words;  // fused mode: scale 4-byte aligned and (N / 32) % 4 == 0
+  // experts' forms (scale_t in 128x4 tiles)
+  const int64_t* offsets;  // ragged: device row offsets [E + 1]
+  int32_t E;
+  uint32_t n_rt;           // row tiles (stacked: of one expert)
+  uint32_t S4;             // 4-column tiles of a scale row: P / 128, or ceil(R / 128)
+  uint64_t swz_bytes;      // stacked: scale bytes of an expert
 };
+
+// What a tile's rows are and where its codes go.
+//  kPlain:   one tensor: row tile rt is rows 128 rt ..
+//  kRagged:  sorted rows of experts: row tile rt is rows of one expert, which
+//            start on a tile in the output; columns of no row are written as zeros
+//  kStacked: a stack of [M, N] tensors, each transposed on its own
+enum Form { kPlain, kRagged, kStacked };
+
+struct TilePlace {
+  int64_t r0;        // first row of x
+  int rows;          // rows of x in the tile
+  int64_t q0;        // q_t + q0: the tile's first code of column 0
+  uint64_t s0;       // kRagged, kStacked: scale_t + s0: the scale tile of column block 0
+};
+
+template <Form FORM>
+__device__ __forceinline__ TilePlace place_of(const ColArgs& a, uint32_t rt, const int64_t* off,
+                                              const int64_t* pb) {
+  TilePlace p{};
+  if constexpr (FORM == kPlain) {
+    p.r0 = int64_t(rt) * kTileRows;
+    p.rows = a.M - p.r0 < kTileRows ? int(a.M - p.r0) : kTileRows;
+    p.q0 = p.r0;
+  } else if constexpr (FORM == kRagged) {
+    const int64_t at = int64_t(rt) * kTileRows;
+    p.q0 = at;
+    p.s0 = uint64_t(rt) * 512;
+    if (at < pb[a.E]) {
+      int lo = 0, hi = a.E;  // invariant: pb[lo] <= at < pb[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pb[mid] <= at) lo = mid; else hi = mid;
+      }
+      p.r0 = off[lo] + (at - pb[lo]);
+      const int64_t left = off[lo + 1] - p.r0;
+      p.rows = left < kTileRows ? int(left) : kTileRows;
+    }
+  } else {
+    const uint32_t e = rt / a.n_rt, rb = rt - e * a.n_rt;
+    const int64_t at = int64_t(rb) * kTileRows;
+    p.r0 = int64_t(e) * a.M + at;
+    p.rows = a.M - at < kTileRows ? int(a.M - at) : kTileRows;
+    p.q0 = int64_t(e) * a.M * a.N + at;
+    p.s0 = e * a.swz_bytes + uint64_t(rb) * 512;
+  }
+  return p;
+}
 
 // max.xorsign.abs over N bf16 pairs as a pairwise tree (depth log2 N rather
 // than a chain of N - 1 dependent maxima); the result's sign bits are junk.
@@ -149,9 +202,10 @@ __device__ __forceinline__ void column_codes_bf16(const uint32_t (&v)[32], float
   pack_codes(c, lo, hi);
 }
 
-template <typename InT, bool ROW>
+template <typename InT, bool ROW, Form FORM>
 __global__ void __launch_bounds__(kThreads, 2)
 mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
+  static_assert(FORM == kPlain || !ROW, "the experts' forms have no rowwise outputs");
   pdl_enter();
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kEsize = sizeof(InT);
@@ -161,13 +215,17 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
   uint8_t* const qr = ss + kSsBytes;        // fused mode: rowwise codes [row][column]
   uint8_t* const sr = qr + kQrBytes;        // fused mode: rowwise scales [row][group]
   const int t = threadIdx.x;
+  int64_t* const off = reinterpret_cast<int64_t*>(qr);   // ragged: the experts' rows, and where they go
+  int64_t* const pb = off + (FORM == kRagged ? a.E + 1 : 0);
+  if constexpr (FORM == kRagged) load_expert_rows<false>(a.offsets, a.E, a.M, off, pb);
 
   // stages tile `tile` into input buffer `b`: 128 rows x 16 chunks of 16
   // bytes, 8 chunks per thread, zeros past M and N
   auto stage = [&](uint32_t tile, int b) {
-    const uint32_t ct = tile % a.n_ct, rt = tile / a.n_ct;
-    const int64_t r0 = int64_t(rt) * kTileRows, c0 = int64_t(ct) * kTileCols;
-    const int rows = a.M - r0 < kTileRows ? int(a.M - r0) : kTileRows;
+    const uint32_t ct = tile % a.n_ct;
+    const TilePlace p = place_of<FORM>(a, tile / a.n_ct, off, pb);
+    const int64_t r0 = p.r0, c0 = int64_t(ct) * kTileCols;
+    const int rows = p.rows;
     const int row_bytes = (a.N - c0 < kTileCols ? int(a.N - c0) : kTileCols) * kEsize;
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(smem + b * kInBytes));
 #pragma unroll
@@ -190,9 +248,11 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
     __syncthreads();  // this tile is in shared memory; the previous one's outputs are written
 
     const uint8_t* in = smem + b * kInBytes;
-    const uint32_t ct = tile % a.n_ct, rt = tile / a.n_ct;
-    const int64_t r0 = int64_t(rt) * kTileRows, c0 = int64_t(ct) * kTileCols;
-    const int rows = a.M - r0 < kTileRows ? int(a.M - r0) : kTileRows;
+    const uint32_t ct = tile % a.n_ct;
+    const TilePlace p = place_of<FORM>(a, tile / a.n_ct, off, pb);
+    const int64_t r0 = p.r0, c0 = int64_t(ct) * kTileCols;
+    // rows of the output: ragged tiles are whole, with zeros behind the expert's rows
+    const int rows = FORM == kRagged ? kTileRows : p.rows;
     const int row_bytes = (a.N - c0 < kTileCols ? int(a.N - c0) : kTileCols) * kEsize;  // multiple of 32
     // row phase (fused mode): (row, 32-column group) pairs of the tile
     if constexpr (ROW) {
@@ -287,7 +347,7 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
         const int idx = i * kThreads + t, col = idx >> 3, ch = idx & 7;
         const int nbytes = rows - 16 * ch;  // valid bytes of this 16-byte chunk
         if (col < cols && nbytes > 0) {
-          uint8_t* dst = a.q_t + (c0 + col) * a.M + r0 + 16 * ch;
+          uint8_t* dst = a.q_t + (c0 + col) * (FORM == kRagged ? int64_t(a.S4) * 128 : a.M) + p.q0 + 16 * ch;
           const uint4 val = lds128(qs + col * kOutPitch + 16 * ch);
           if (a.q_t_aligned && nbytes >= 16) {
             st_v4(dst, val);
@@ -298,15 +358,28 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
           }
         }
       }
-      // scales: the tile's 4 groups of a column are 4 consecutive bytes of scale_t
-      if (t < cols) {
-        const int ng = (rows + 31) / 32;
-        uint8_t* dst = a.scale_t + (c0 + t) * a.gt + r0 / 32;
-        if (ng == 4 && a.scale_words) {
-          st_u32(dst, *reinterpret_cast<const uint32_t*>(ss + 4 * t));
-        } else {
-          for (int j = 0; j < ng; j++) st_u8(dst + j, ss[4 * t + j]);
+      if constexpr (FORM == kPlain) {
+        // scales: the tile's 4 groups of a column are 4 consecutive bytes of scale_t
+        if (t < cols) {
+          const int ng = (rows + 31) / 32;
+          uint8_t* dst = a.scale_t + (c0 + t) * a.gt + r0 / 32;
+          if (ng == 4 && a.scale_words) {
+            st_u32(dst, *reinterpret_cast<const uint32_t*>(ss + 4 * t));
+          } else {
+            for (int j = 0; j < ng; j++) st_u8(dst + j, ss[4 * t + j]);
+          }
         }
+      } else if (t < kTileCols) {
+        // scales: the tile's 4 groups of a column are one word of a 128x4
+        // tile; groups past the rows and columns past N (up to the next
+        // multiple of 128) are zeros
+        const int64_t col = c0 + t;
+        const uint32_t ng = uint32_t(rows + 31) / 32;
+        uint32_t w = 0;
+        if (t < cols) w = *reinterpret_cast<const uint32_t*>(ss + 4 * t) & (0xffffffffu >> (32 - 8 * ng));
+        uint8_t* dst = a.scale_t + p.s0 + uint64_t(col >> 7) * a.S4 * 512 + (col & 31) * 16 + ((col >> 5) & 3) * 4;
+        st_u32(dst, w);
+        if (kTileCols == 64 && !(c0 & 64) && c0 + kTileCols >= a.N) st_u32(dst + 8, 0);
       }
     }
     // fused mode: the rowwise codes of the tile, one row's segment (128 or 64
@@ -334,15 +407,17 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
   }
 }
 
-template <typename InT, bool ROW>
+template <typename InT, bool ROW, Form FORM = kPlain>
 mxq_status launch_colwise(const ColArgs& a, uint32_t grid, cudaStream_t s) {
-  constexpr uint32_t kSmem = ROW ? kFusedSmem : kColSmem;
-  const cudaError_t attr_err = ensure_smem_limit<mxfp8_colwise_kernel<InT, ROW>>(int(kSmem));
+  // (with the tables of the most experts: two CTAs still fit a multiprocessor)
+  constexpr uint32_t kSmem =
+      ROW ? kFusedSmem : kColSmem + (FORM == kRagged ? 16 * (MXQ_GROUPED_MAX_EXPERTS + 1) : 0);
+  const cudaError_t attr_err = ensure_smem_limit<mxfp8_colwise_kernel<InT, ROW, FORM>>(int(kSmem));
   if (attr_err != cudaSuccess) {
     record_cuda_error(attr_err);
     return MXQ_ERR_CUDA;
   }
-  return launched(launch_pdl_ex(mxfp8_colwise_kernel<InT, ROW>, grid, kThreads, kSmem, s, a));
+  return launched(launch_pdl_ex(mxfp8_colwise_kernel<InT, ROW, FORM>, grid, kThreads, kSmem, s, a));
 }
 
 }  // namespace
@@ -388,4 +463,83 @@ extern "C" mxq_status mxfp8_quantize_columnwise(const void* x, int dt, int64_t M
   if (dt == MXQ_BF16)
     return fused ? launch_colwise<uint16_t, true>(a, grid, s) : launch_colwise<uint16_t, false>(a, grid, s);
   return fused ? launch_colwise<float, true>(a, grid, s) : launch_colwise<float, false>(a, grid, s);
+}
+
+namespace mxq {
+namespace {
+
+// Checks and launch of the experts' forms: rows [rows, N] of x, `n_rt` row tiles in all.
+mxq_status columnwise_experts(ColArgs& a, const void* x, int dt, int64_t ld_x, uint64_t n_rt, bool ragged,
+                              cudaStream_t s) {
+  const int es = elem_size(dt);
+  const uint64_t tile_cols = uint64_t(kRowBytes / es);
+  const uint64_t n_ct = (uint64_t(a.N) + tile_cols - 1) / tile_cols;
+  if (n_rt > 0x7fffffffull || n_rt * n_ct > 0x7fffffffull) return MXQ_ERR_SHAPE;
+  a.x = static_cast<const uint8_t*>(x);
+  a.ld_bytes = ld_x * es;
+  a.n_ct = uint32_t(n_ct);
+  a.ntiles = uint32_t(n_rt * n_ct);
+  const uint64_t resident = uint64_t(sm_count()) * 2;
+  const uint32_t grid = uint32_t(std::min<uint64_t>(a.ntiles, resident));
+  if (ragged)
+    return dt == MXQ_BF16 ? launch_colwise<uint16_t, false, kRagged>(a, grid, s)
+                          : launch_colwise<float, false, kRagged>(a, grid, s);
+  return dt == MXQ_BF16 ? launch_colwise<uint16_t, false, kStacked>(a, grid, s)
+                        : launch_colwise<float, false, kStacked>(a, grid, s);
+}
+
+}  // namespace
+}  // namespace mxq
+
+extern "C" mxq_status mxfp8_quantize_columnwise_grouped(const void* x, int dt, int32_t E,
+                                                        const int64_t* row_offsets, int64_t M_total,
+                                                        int64_t N, int64_t ld_x, uint8_t* qweight_t,
+                                                        uint8_t* scale_swz, mxq_stream_t stream) {
+  using namespace mxq;
+  if (!valid_dtype(dt)) return MXQ_ERR_DTYPE;
+  if (E < 1 || E > MXQ_GROUPED_MAX_EXPERTS || M_total < 0 || N < 0 || N % 16 != 0 || ld_x < N)
+    return MXQ_ERR_SHAPE;
+  if (M_total > 0x7fffff00ll || N > 0x7fffff00ll || ld_x > (int64_t(1) << 56)) return MXQ_ERR_SHAPE;
+  const int64_t P = mxq_grouped_padded_rows(E, M_total);
+  if (P == 0 || N == 0) return MXQ_OK;
+  if ((M_total > 0 && !x) || !row_offsets || !qweight_t || !scale_swz) return MXQ_ERR_NULL;
+  const int es = elem_size(dt);
+  if (!aligned16(x) || (uint64_t(ld_x) * es) % 16 != 0 || !aligned16(qweight_t) || !aligned16(scale_swz) ||
+      (reinterpret_cast<uintptr_t>(row_offsets) & 7u))
+    return MXQ_ERR_ALIGN;
+  ColArgs a{};
+  a.M = M_total;
+  a.N = N;
+  a.q_t = qweight_t;
+  a.scale_t = scale_swz;
+  a.q_t_aligned = true;
+  a.offsets = row_offsets;
+  a.E = E;
+  a.S4 = uint32_t(P / 128);
+  if (!x) x = qweight_t;  // no rows: only an address for copies of no bytes
+  return columnwise_experts(a, x, dt, ld_x, uint64_t(P / 128), true, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" mxq_status mxfp8_quantize_columnwise_stacked(const void* x, int dt, int32_t E, int64_t R,
+                                                        int64_t N, uint8_t* qweight_t, uint8_t* scale_swz,
+                                                        mxq_stream_t stream) {
+  using namespace mxq;
+  if (!valid_dtype(dt)) return MXQ_ERR_DTYPE;
+  if (E < 1 || E > MXQ_GROUPED_MAX_EXPERTS || R < 0 || N < 0 || R % 32 != 0 || N % 16 != 0)
+    return MXQ_ERR_SHAPE;
+  if (R > 0x7fffff00ll || N > 0x7fffff00ll) return MXQ_ERR_SHAPE;
+  if (R == 0 || N == 0) return MXQ_OK;
+  if (!x || !qweight_t || !scale_swz) return MXQ_ERR_NULL;
+  if (!aligned16(x) || !aligned16(qweight_t) || !aligned16(scale_swz)) return MXQ_ERR_ALIGN;
+  ColArgs a{};
+  a.M = R;
+  a.N = N;
+  a.q_t = qweight_t;
+  a.scale_t = scale_swz;
+  a.q_t_aligned = true;
+  a.E = E;
+  a.n_rt = uint32_t((R + 127) / 128);
+  a.S4 = a.n_rt;
+  a.swz_bytes = uint64_t(mxq_swizzled_scale_bytes(N, R / 32));
+  return columnwise_experts(a, x, dt, N, uint64_t(a.n_rt) * E, false, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -503,4 +503,55 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return r;
 }
 
+// ------------------------------------------------------- experts' rows
+
+// Row offsets of a stacked tensor's experts in shared memory: off[e] = the
+// device offsets clamped into a non-decreasing sequence from off[0] = 0 to
+// off[E] = M (so no write can leave the layout, whatever the offsets hold; with
+// ALL false the last one too is the caller's, and rows behind it are no
+// expert's),
+// and pb[e] = first row of expert e in the per-expert padded layout,
+// pb[e + 1] = pb[e] + ceil((off[e + 1] - off[e]) / 128) * 128. All threads
+// load the offsets (one global round trip), then one warp scans them in
+// shared memory, 32 entries at a time.
+template <bool ALL>
+__device__ __forceinline__ void load_expert_rows(const int64_t* __restrict__ g_off, int E,
+                                                 int64_t M, int64_t* off, int64_t* pb) {
+  for (int e = threadIdx.x; e <= E; e += kThreads) {
+    int64_t v = e == 0 ? 0 : (ALL && e == E ? M : g_off[e]);
+    off[e] = v < 0 ? 0 : (v > M ? M : v);
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t carry_off = 0, carry_pb = 0;
+    for (int base = 0; base <= E; base += 32) {
+      const int e = base + lane;
+      int64_t v = e <= E ? off[e] : M;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) v = t > v ? t : v;
+      }
+      v = carry_off > v ? carry_off : v;
+      int64_t prev = __shfl_up_sync(kFull, v, 1);
+      if (lane == 0) prev = carry_off;
+      int64_t d = (e == 0 || e > E) ? 0 : ((v - prev + 127) & ~int64_t(127));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(kFull, d, o);
+        if (lane >= o) d += t;
+      }
+      d += carry_pb;
+      if (e <= E) {
+        off[e] = v;
+        pb[e] = d;
+      }
+      carry_off = __shfl_sync(kFull, v, 31);
+      carry_pb = __shfl_sync(kFull, d, 31);
+    }
+  }
+  __syncthreads();
+}
+
 }  // namespace mxq

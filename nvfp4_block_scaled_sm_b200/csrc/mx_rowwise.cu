@@ -111,52 +111,6 @@ struct QuantArgs {
 constexpr int kSwzNone = 0;
 constexpr int kSwzTensor = 1;
 
-// Row offsets of a stacked tensor's experts in shared memory: off[e] = the
-// device offsets clamped into a non-decreasing sequence from off[0] = 0 to
-// off[E] = M (so no write can leave the layout, whatever the offsets hold),
-// and pb[e] = first row of expert e in the per-expert padded layout,
-// pb[e + 1] = pb[e] + ceil((off[e + 1] - off[e]) / 128) * 128. All threads
-// load the offsets (one global round trip), then one warp scans them in
-// shared memory, 32 entries at a time.
-__device__ __forceinline__ void load_expert_rows(const int64_t* __restrict__ g_off, int E,
-                                              int64_t M, int64_t* off, int64_t* pb) {
-  for (int e = threadIdx.x; e <= E; e += kThreads) {
-    int64_t v = e == 0 ? 0 : (e == E ? M : g_off[e]);
-    off[e] = v < 0 ? 0 : (v > M ? M : v);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int64_t carry_off = 0, carry_pb = 0;
-    for (int base = 0; base <= E; base += 32) {
-      const int e = base + lane;
-      int64_t v = e <= E ? off[e] : M;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(kFull, v, o);
-        if (lane >= o) v = t > v ? t : v;
-      }
-      v = carry_off > v ? carry_off : v;
-      int64_t prev = __shfl_up_sync(kFull, v, 1);
-      if (lane == 0) prev = carry_off;
-      int64_t d = (e == 0 || e > E) ? 0 : ((v - prev + 127) & ~int64_t(127));
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(kFull, d, o);
-        if (lane >= o) d += t;
-      }
-      d += carry_pb;
-      if (e <= E) {
-        off[e] = v;
-        pb[e] = d;
-      }
-      carry_off = __shfl_sync(kFull, v, 31);
-      carry_pb = __shfl_sync(kFull, d, 31);
-    }
-  }
-  __syncthreads();
-}
-
 // Swizzled scales are limited to S <= 2^27 - 4 columns (2^25 - 1 four-column
 // tiles): the gather counts the 4-byte words of a 128-row output block,
 // 128 ceil(S/4), in 32 bits (2^25 tiles would make that count wrap to 0), and
@@ -197,7 +151,7 @@ mx_swizzle_experts_kernel(const uint8_t* __restrict__ scale, uint8_t* __restrict
   __shared__ uint32_t tile[128 * kSwzPitch + 3 * 8];
   int64_t* off = s_rows;
   int64_t* pb = s_rows + (E + 1);
-  load_expert_rows(offs, E, M, off, pb);
+  load_expert_rows<true>(offs, E, M, off, pb);
   const uint64_t blocks = uint64_t(pb[E]) >> 7;
   const uint32_t words = 128 * Sp4;  // 4-byte words per output block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

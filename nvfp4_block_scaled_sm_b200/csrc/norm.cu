@@ -1,0 +1,722 @@
+// norm.cu -- root-mean-square norm of rows with the residual's addition, its
+// output quantized to MXFP8 in the same pass, and the norm's gradient, for
+// sm_100a.
+//
+//   h = x (+ residual, rounded to x's type), rstd = fp32(1 / sqrt(mean(h^2) + eps))
+//   y = fp32(fp32(h rstd) weight), codes and scales of y by mx_rowwise.cu's rule
+//
+// The squares are added up in fp64 (the square of a bf16 or fp32 value leaves
+// fp32's range long before the value does), so that rstd is the correctly
+// rounded fp32 number but for sums that fp64 leaves on a border, and every
+// step after it is one IEEE operation: codes and scales are functions of the
+// inputs' bits whatever the order of the sum.
+//
+// Gradient: dx = grad_hidden + rstd (g w - xh mean(g w xh)) with xh = h rstd,
+// dweight = sum over the rows of g xh.
+#include "common.cuh"
+
+namespace mxq {
+namespace {
+
+// ------------------------------------------------------------- forward
+//
+// HBM-bound: per bf16 element 2 bytes read (4 with a residual), 1 + 1/32
+// written (3 + 1/32). A row lies in the registers of its warps: a lane owns 16
+// consecutive elements (a 256-bit load of bf16), two lanes a group of 32, C
+// such pieces a lane; the warps of a row exchange their sums through shared
+// memory once. Small rows share a CTA. Rows of more than 32 * 1024 elements are
+// read twice instead (LOOP), the second time from L2.
+
+struct NormArgs {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* hidden;
+  uint8_t* q;
+  uint8_t* scale;
+  uint8_t* swz;
+  void* normed;
+  float* rstd;
+  int64_t ld_x, ld_res;
+  int64_t M;
+  uint32_t N;
+  uint32_t S4;            // ceil(N / 128)
+  uint32_t row_threads;   // threads of a row, a multiple of 32
+  double eps;
+  int weight_bf16;
+  bool v8;                // x, residual, hidden and normed: rows on 32-byte boundaries
+  bool scale_words;       // compact scales can be written as words
+};
+
+// As In16::load, by plain loads: hidden may be x or residual itself, and LOOP
+// reads what this thread has written.
+template <typename T>
+__device__ __forceinline__ void load16(In16<T>& v, const T* p, bool v8) {
+  constexpr int kWords = sizeof(v.w) / 4;
+  if (v8) {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 8)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v.w[i]), "=r"(v.w[i + 1]), "=r"(v.w[i + 2]), "=r"(v.w[i + 3]), "=r"(v.w[i + 4]),
+                     "=r"(v.w[i + 5]), "=r"(v.w[i + 6]), "=r"(v.w[i + 7])
+                   : "l"(reinterpret_cast<const uint32_t*>(p) + i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.w[i]), "=r"(v.w[i + 1]), "=r"(v.w[i + 2]), "=r"(v.w[i + 3])
+                   : "l"(reinterpret_cast<const uint32_t*>(p) + i));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const In16<T>& v, bool v8) {
+  constexpr int kWords = sizeof(v.w) / 4;
+  uint32_t* o = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+  for (int i = 0; i < kWords; i += 8) {
+    if (v8) {
+      const uint32_t w[8] = {v.w[i], v.w[i + 1], v.w[i + 2], v.w[i + 3], v.w[i + 4], v.w[i + 5], v.w[i + 6], v.w[i + 7]};
+      st_v8(o + i, w);
+    } else {
+      st_v4(o + i, make_uint4(v.w[i], v.w[i + 1], v.w[i + 2], v.w[i + 3]));
+      st_v4(o + i + 4, make_uint4(v.w[i + 4], v.w[i + 5], v.w[i + 6], v.w[i + 7]));
+    }
+  }
+}
+
+__device__ __forceinline__ void set_pair(In16<uint16_t>& v, int k, float lo, float hi) { v.w[k] = cvt_bf16x2(lo, hi); }
+__device__ __forceinline__ void set_pair(In16<float>& v, int k, float lo, float hi) {
+  v.w[2 * k] = __float_as_uint(lo);
+  v.w[2 * k + 1] = __float_as_uint(hi);
+}
+
+// Rounded to T and back in registers: h = x + residual.
+template <typename T>
+__device__ __forceinline__ void add16(In16<T>& v, const In16<T>& r) {
+#pragma unroll
+  for (int k = 0; k < 8; k++) set_pair(v, k, v.lo(k) + r.lo(k), v.hi(k) + r.hi(k));
+}
+
+template <typename T>
+__device__ __forceinline__ double squares(const In16<T>& v) {
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const double a = double(v.lo(k)), b = double(v.hi(k));
+    s = fma(a, a, s);
+    s = fma(b, b, s);
+  }
+  return s;
+}
+
+// The 16 weights from element c on, in fp32.
+__device__ __forceinline__ void load_weight(float (&w)[16], const NormArgs& a, uint32_t c) {
+  if (a.weight_bf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c);
+    const uint4 q0 = __ldg(p), q1 = __ldg(p + 1);
+    const uint32_t u[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      w[2 * k] = bf16_lo(u[k]);
+      w[2 * k + 1] = bf16_hi(u[k]);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float4 q = __ldg(p + k);
+      w[4 * k] = q.x; w[4 * k + 1] = q.y; w[4 * k + 2] = q.z; w[4 * k + 3] = q.w;
+    }
+  }
+}
+
+// y of 16 elements of a row, their codes, the group's scale (two lanes a
+// group; the lanes of a warp call together) and, where asked for, y itself.
+template <typename T>
+__device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, int64_t row, uint32_t c, float rstd,
+                                         bool active) {
+  const uint32_t lane = threadIdx.x & 31;
+  float w[16], y[16];
+  if (active) load_weight(w, a, c);
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const float2 u = mul2(h.lo(k), h.hi(k), rstd);
+    y[2 * k] = active ? u.x * w[2 * k] : 0.f;
+    y[2 * k + 1] = active ? u.y * w[2 * k + 1] : 0.f;
+    amax = fmaxf(amax, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));   // NaN raises no maximum
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+  const uint32_t b = mx_scale_byte<8>(amax);
+  const float mul = pow2_quant(b);
+  uint32_t code[8];
+#pragma unroll
+  for (int k = 0; k < 8; k++) {
+    const float2 u = mul2(y[2 * k], y[2 * k + 1], mul);
+    code[k] = cvt_e4m3x2(u.x, u.y);
+  }
+  // a word of the row's next four groups in every eighth lane; groups past N are zeros
+  uint32_t word = active ? b : 0;
+  word |= __shfl_down_sync(kFull, word, 2) << 8;
+  word |= __shfl_down_sync(kFull, word, 4) << 16;
+  if (!active) return;
+  st_v4(a.q + row * a.N + c,
+        make_uint4(__byte_perm(code[0], code[1], 0x5410), __byte_perm(code[2], code[3], 0x5410),
+                   __byte_perm(code[4], code[5], 0x5410), __byte_perm(code[6], code[7], 0x5410)));
+  const uint32_t g = c >> 5;
+  uint8_t* s = a.scale + row * (a.N >> 5) + g;
+  if (a.scale_words) {
+    if ((lane & 7) == 0) st_u32(s, word);
+  } else if ((lane & 1) == 0) {
+    st_u8(s, b);
+  }
+  if (a.swz && (lane & 7) == 0)
+    st_u32(a.swz + (((uint64_t(row) >> 7) * a.S4 + (g >> 2)) << 9) + ((row & 31) << 4) + (((row >> 5) & 3) << 2), word);
+  if (a.normed) {
+    In16<T> o;
+#pragma unroll
+    for (int k = 0; k < 8; k++) set_pair(o, k, y[2 * k], y[2 * k + 1]);
+    store16(static_cast<T*>(a.normed) + row * a.N + c, o, a.v8);
+  }
+}
+
+template <typename T, bool RES, int C, bool LOOP>
+__global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
+  pdl_enter();
+  __shared__ double sums[32];
+  __shared__ float rstds[32];
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t row_warps = a.row_threads >> 5, sub = warp / row_warps;
+  const uint32_t rows = (blockDim.x >> 5) / row_warps;                 // rows of a CTA
+  const uint32_t t = threadIdx.x - sub * a.row_threads;
+  const int64_t row = int64_t(blockIdx.x) * rows + sub;
+  const bool have = row < a.M;
+  const T* x = static_cast<const T*>(a.x) + row * a.ld_x;
+  const T* res = static_cast<const T*>(a.residual) + (RES ? row * a.ld_res : 0);
+  T* hidden = static_cast<T*>(a.hidden) + (RES ? row * int64_t(a.N) : 0);
+
+  In16<T> v[C];
+  double ss = 0.0;
+  if constexpr (LOOP) {
+    for (uint32_t c = t * 16; have && c < a.N; c += a.row_threads * 16) {
+      load16(v[0], x + c, a.v8);
+      if constexpr (RES) {
+        In16<T> r;
+        load16(r, res + c, a.v8);
+        add16(v[0], r);
+        store16(hidden + c, v[0], a.v8);
+      }
+      ss += squares(v[0]);
+    }
+  } else {
+    In16<T> r[C];
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      const uint32_t c = (i * a.row_threads + t) * 16;
+      if (have && c < a.N) {
+        load16(v[i], x + c, a.v8);
+        if constexpr (RES) load16(r[i], res + c, a.v8);
+      } else {
+        v[i].zero();
+        if constexpr (RES) r[i].zero();
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      const uint32_t c = (i * a.row_threads + t) * 16;
+      if constexpr (RES) {
+        add16(v[i], r[i]);
+        if (have && c < a.N) store16(hidden + c, v[i], a.v8);
+      }
+      ss += squares(v[i]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+  if (lane == 0) sums[warp] = ss;
+  __syncthreads();
+  // one thread a row: the other warps' fp64 pipes stay free
+  if (t == 0) {
+    double s = 0.0;
+    for (uint32_t i = 0; i < row_warps; i++) s += sums[warp + i];
+    const float r = float(1.0 / sqrt(s / double(a.N) + a.eps));
+    rstds[sub] = r;
+    if (have) a.rstd[row] = r;
+  }
+  __syncthreads();
+  const float rstd = rstds[sub];
+  if constexpr (LOOP) {
+    const T* h = RES ? hidden : x;
+    for (uint32_t c0 = (t & ~31u) * 16; c0 < a.N; c0 += a.row_threads * 16) {   // warps stay together
+      const uint32_t c = c0 + lane * 16;
+      const bool active = have && c < a.N;
+      if (active) load16(v[0], h + c, a.v8); else v[0].zero();
+      finish16(a, v[0], row, c, rstd, active);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      const uint32_t c = (i * a.row_threads + t) * 16;
+      finish16(a, v[i], row, c, rstd, have && c < a.N);
+    }
+  }
+  // the tiles' rows past M are zeros
+  if (a.swz) {
+    const uint64_t pad = (uint64_t(a.M + 127) & ~127ull) - uint64_t(a.M);
+    const uint64_t words = pad * a.S4;
+    for (uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += uint64_t(gridDim.x) * blockDim.x) {
+      const uint64_t r = uint64_t(a.M) + i / a.S4;
+      st_u32(a.swz + (((r >> 7) * a.S4 + i % a.S4) << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2), 0);
+    }
+  }
+}
+
+template <typename T, bool RES, int C, bool LOOP>
+mxq_status launch_norm(const NormArgs& a, uint32_t rows, cudaStream_t s) {
+  const uint64_t grid = (uint64_t(a.M) + rows - 1) / rows;
+  if (grid > 0x7fffffffull) return MXQ_ERR_SHAPE;
+  return launched(launch_pdl_ex(mxfp8_rmsnorm_kernel<T, RES, C, LOOP>, uint32_t(grid), a.row_threads * rows, 0, s, a));
+}
+
+template <typename T, bool RES>
+mxq_status norm_dispatch(NormArgs& a, cudaStream_t s) {
+  const uint32_t pieces = a.N / 16;
+  if (pieces > 2048) {
+    a.row_threads = 1024;
+    return launch_norm<T, RES, 1, true>(a, 1, s);
+  }
+  const int C = pieces <= 128 ? 1 : 2;
+  a.row_threads = ((pieces + C - 1) / C + 31) / 32 * 32;
+  const uint32_t rows = std::max(1u, 128 / a.row_threads);
+  return C == 1 ? launch_norm<T, RES, 1, false>(a, rows, s) : launch_norm<T, RES, 2, false>(a, rows, s);
+}
+
+// ------------------------------------------------------------ gradient
+//
+// HBM-bound: per bf16 element 4 bytes read (6 with grad_hidden), 2 written.
+// Persistent CTAs take rows blockIdx.x, + grid, ...: a thread owns the same C
+// pieces of 8 columns in every row, so that the weight's gradient stays in its
+// registers until the end. Rows are copied into a ring of DEPTH rows in shared
+// memory with cp.async, each thread its own pieces: no thread waits for
+// another's copies, and the only barrier of a row is that of the sum
+// mean(g w xh). The CTAs' sums of dweight go to the workspace [grid, N] and a
+// second kernel adds them up in a fixed order. Rows of more than 16384
+// elements take a kernel that reads them twice, and dweight one of its own.
+
+struct GradArgs {
+  const void *g, *h, *gh, *weight;
+  const float* rstd;
+  void* dx;
+  float* part;            // [grid, N], or NULL
+  int64_t ld_g, ld_h, ld_gh;
+  int64_t M;
+  uint32_t N;
+  int weight_bf16;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Eight values of T from 16 (bf16) or 32 bytes.
+template <typename T>
+struct Row8 {
+  float f[8];
+  __device__ __forceinline__ void unpack(const uint4& q) {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      f[2 * k] = bf16_lo(u[k]);
+      f[2 * k + 1] = bf16_hi(u[k]);
+    }
+  }
+  __device__ __forceinline__ void load(const uint4* p) {
+    if constexpr (sizeof(T) == 2) {
+      unpack(p[0]);
+    } else {
+      const uint4 a = p[0], b = p[1];
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 8; k++) f[k] = __uint_as_float(u[k]);
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (sizeof(T) == 2) {
+      st_v4(p, make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7])));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; k += 4)
+        st_v4(p + k, make_uint4(__float_as_uint(f[k]), __float_as_uint(f[k + 1]), __float_as_uint(f[k + 2]), __float_as_uint(f[k + 3])));
+    }
+  }
+};
+
+__device__ __forceinline__ void weight8(float (&w)[8], const GradArgs& a, uint32_t c) {
+  if (a.weight_bf16) {
+    Row8<uint16_t> r;
+    r.unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c)));
+#pragma unroll
+    for (int k = 0; k < 8; k++) w[k] = r.f[k];
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c);
+    const float4 q0 = __ldg(p), q1 = __ldg(p + 1);
+    w[0] = q0.x; w[1] = q0.y; w[2] = q0.z; w[3] = q0.w;
+    w[4] = q1.x; w[5] = q1.y; w[6] = q1.z; w[7] = q1.w;
+  }
+}
+
+// Sum over the CTA of s; `red` is 32 floats that the next call does not use.
+__device__ __forceinline__ float block_sum(float s, float* red) {
+  const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+  if (lane == 0) red[warp] = s;
+  __syncthreads();
+  float r = lane < warps ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
+  return r;
+}
+
+template <typename T, bool GH, int C, int DEPTH>
+__global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs a) {
+  pdl_enter();
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][32];
+  constexpr uint32_t kPiece = 8 * sizeof(T);                       // bytes
+  const uint32_t t = threadIdx.x, T0 = blockDim.x;
+  const uint32_t plane = T0 * C * kPiece;                          // one tensor's row in a stage
+  const uint32_t stage = plane * (GH ? 3 : 2);
+  const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  auto fetch = [&](int64_t row, uint32_t s) {
+    if (row < a.M) {
+#pragma unroll
+      for (int i = 0; i < C; i++) {
+        const uint32_t c = (i * T0 + t) * 8;
+        if (c < a.N) {
+          const uint32_t dst = ring0 + s * stage + (i * T0 + t) * kPiece;
+          const T* g = static_cast<const T*>(a.g) + row * a.ld_g + c;
+          const T* h = static_cast<const T*>(a.h) + row * a.ld_h + c;
+          const T* gh = static_cast<const T*>(a.gh) + (GH ? row * a.ld_gh + c : 0);
+#pragma unroll
+          for (uint32_t b = 0; b < kPiece; b += 16) {
+            copy16(dst + b, reinterpret_cast<const uint8_t*>(g) + b);
+            copy16(dst + plane + b, reinterpret_cast<const uint8_t*>(h) + b);
+            if constexpr (GH) copy16(dst + 2 * plane + b, reinterpret_cast<const uint8_t*>(gh) + b);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < DEPTH - 1; s++) fetch(int64_t(blockIdx.x) + int64_t(s) * gridDim.x, s);
+
+  float w[C][8], dw[C][8];
+#pragma unroll
+  for (int i = 0; i < C; i++) {
+    const uint32_t c = (i * T0 + t) * 8;
+    if (c < a.N) weight8(w[i], a, c);
+#pragma unroll
+    for (int k = 0; k < 8; k++) dw[i][k] = 0.f;
+  }
+  const float inv_n = 1.f / float(a.N);
+  uint32_t s = 0, par = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, par ^= 1) {
+    // the stage that was read last is filled again (each thread's own pieces)
+    fetch(row + int64_t(DEPTH - 1) * gridDim.x, s == 0 ? DEPTH - 1 : s - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    const float rstd = __ldg(a.rstd + row);
+    const uint8_t* at = ring + s * stage;
+    Row8<T> gw[C], xh[C];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      if ((i * T0 + t) * 8 < a.N) {
+        gw[i].load(reinterpret_cast<const uint4*>(at + (i * T0 + t) * kPiece));
+        xh[i].load(reinterpret_cast<const uint4*>(at + plane + (i * T0 + t) * kPiece));
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          xh[i].f[k] *= rstd;
+          dw[i][k] = fmaf(gw[i].f[k], xh[i].f[k], dw[i][k]);
+          gw[i].f[k] *= w[i][k];
+          sum = fmaf(gw[i].f[k], xh[i].f[k], sum);
+        }
+      }
+    }
+    const float mean = block_sum(sum, red[par]) * inv_n;
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      const uint32_t c = (i * T0 + t) * 8;
+      if (c < a.N) {
+        Row8<T> o;
+        if constexpr (GH) o.load(reinterpret_cast<const uint4*>(at + 2 * plane + (i * T0 + t) * kPiece));
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          const float d = fmaf(-xh[i].f[k], mean, gw[i].f[k]);
+          o.f[k] = GH ? fmaf(rstd, d, o.f[k]) : rstd * d;
+        }
+        o.store(static_cast<T*>(a.dx) + row * int64_t(a.N) + c);
+      }
+    }
+    if (++s == DEPTH) s = 0;
+  }
+  if (a.part) {
+#pragma unroll
+    for (int i = 0; i < C; i++) {
+      const uint32_t c = (i * T0 + t) * 8;
+      if (c < a.N) {
+        float* p = a.part + uint64_t(blockIdx.x) * a.N + c;
+#pragma unroll
+        for (int k = 0; k < 8; k += 4)
+          st_v4(p + k, make_uint4(__float_as_uint(dw[i][k]), __float_as_uint(dw[i][k + 1]), __float_as_uint(dw[i][k + 2]), __float_as_uint(dw[i][k + 3])));
+      }
+    }
+  }
+}
+
+// dx of long rows, one row a CTA at a time, read twice.
+template <typename T, bool GH>
+__global__ void __launch_bounds__(1024) rmsnorm_grad_long_kernel(const __grid_constant__ GradArgs a) {
+  pdl_enter();
+  __shared__ float red[2][32];
+  const float inv_n = 1.f / float(a.N);
+  uint32_t par = 0;
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, par ^= 1) {
+    const float rstd = __ldg(a.rstd + row);
+    const T* g = static_cast<const T*>(a.g) + row * a.ld_g;
+    const T* h = static_cast<const T*>(a.h) + row * a.ld_h;
+    float sum = 0.f, w[8];
+    Row8<T> gw, xh;
+    for (uint32_t c = threadIdx.x * 8; c < a.N; c += blockDim.x * 8) {
+      gw.load(reinterpret_cast<const uint4*>(g + c));
+      xh.load(reinterpret_cast<const uint4*>(h + c));
+      weight8(w, a, c);
+#pragma unroll
+      for (int k = 0; k < 8; k++) sum = fmaf(gw.f[k] * w[k], xh.f[k] * rstd, sum);
+    }
+    const float mean = block_sum(sum, red[par]) * inv_n;
+    for (uint32_t c = threadIdx.x * 8; c < a.N; c += blockDim.x * 8) {
+      gw.load(reinterpret_cast<const uint4*>(g + c));
+      xh.load(reinterpret_cast<const uint4*>(h + c));
+      weight8(w, a, c);
+      Row8<T> o;
+      if constexpr (GH) o.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.gh) + row * a.ld_gh + c));
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        const float d = fmaf(-(xh.f[k] * rstd), mean, gw.f[k] * w[k]);
+        o.f[k] = GH ? fmaf(rstd, d, o.f[k]) : rstd * d;
+      }
+      o.store(static_cast<T*>(a.dx) + row * int64_t(a.N) + c);
+    }
+  }
+}
+
+// dweight's partial sums of long rows: CTA (column block, share of the rows).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rmsnorm_dweight_kernel(const __grid_constant__ GradArgs a) {
+  pdl_enter();
+  const uint32_t c = (blockIdx.x * kThreads + threadIdx.x) * 8;
+  if (c >= a.N) return;
+  float dw[8] = {};
+  for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
+    const float rstd = __ldg(a.rstd + row);
+    Row8<T> g, h;
+    g.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.g) + row * a.ld_g + c));
+    h.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.h) + row * a.ld_h + c));
+#pragma unroll
+    for (int k = 0; k < 8; k++) dw[k] = fmaf(g.f[k], h.f[k] * rstd, dw[k]);
+  }
+  float* p = a.part + uint64_t(blockIdx.y) * a.N + c;
+#pragma unroll
+  for (int k = 0; k < 8; k++) p[k] = dw[k];
+}
+
+// dweight[c] = the sum of `parts` partial sums, 32 columns a CTA, eight shares
+// of the parts joined in a fixed order.
+__global__ void __launch_bounds__(kThreads) rmsnorm_join_kernel(const float* __restrict__ part, uint32_t parts,
+                                                                uint32_t N, void* dweight, int bf16) {
+  pdl_enter();
+  __shared__ float red[8][33];
+  const uint32_t lane = threadIdx.x & 31, share = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < N)
+    for (uint32_t p = share; p < parts; p += 8) s += part[uint64_t(p) * N + c];
+  red[share][lane] = s;
+  __syncthreads();
+  if (share != 0 || c >= N) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) s += red[i][lane];
+  if (bf16)
+    static_cast<uint16_t*>(dweight)[c] = uint16_t(cvt_bf16x2(s, 0.f));
+  else
+    static_cast<float*>(dweight)[c] = s;
+}
+
+constexpr uint32_t kLongRow = 16384;     // elements
+constexpr uint32_t kSms = 148;
+constexpr uint32_t kRingBytes = 200 * 1024;
+
+// CTAs of the gradient, rows of the workspace: short rows need more CTAs on a
+// multiprocessor for as many bytes in flight.
+uint32_t grad_parts(int64_t M, int64_t N) {
+  const uint32_t per = N > 4096 ? 1 : N > 2048 ? 2 : N > 1024 ? 4 : 8;
+  return uint32_t(std::min<int64_t>(M, int64_t(kSms) * per));
+}
+
+template <typename T, bool GH, int C, int DEPTH>
+mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaStream_t s) {
+  const uint32_t smem = DEPTH * threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
+  const cudaError_t e = ensure_smem_limit<rmsnorm_grad_kernel<T, GH, C, DEPTH>>(int(kRingBytes));
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return MXQ_ERR_CUDA;
+  }
+  return launched(launch_pdl_ex(rmsnorm_grad_kernel<T, GH, C, DEPTH>, grid, threads, smem, s, a));
+}
+
+template <typename T, bool GH, int C>
+mxq_status grad_depth(const GradArgs& a, uint32_t grid, uint32_t per, uint32_t threads, cudaStream_t s) {
+  const uint32_t stage = threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
+  const uint32_t room = kRingBytes / per;
+  if (stage * 4 <= room) return launch_grad<T, GH, C, 4>(a, grid, threads, s);
+  if (stage * 2 <= room) return launch_grad<T, GH, C, 2>(a, grid, threads, s);
+  return launch_grad<T, GH, C, 1>(a, grid, threads, s);
+}
+
+template <typename T, bool GH>
+mxq_status grad_dispatch(const GradArgs& a, uint32_t grid, cudaStream_t s) {
+  const uint32_t pieces = a.N / 8;
+  if (a.N > kLongRow) {
+    const mxq_status st = launched(launch_pdl_ex(rmsnorm_grad_long_kernel<T, GH>, grid, 1024, 0, s, a));
+    if (st != MXQ_OK || !a.part) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((pieces + kThreads - 1) / kThreads, grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel<T>, a));
+  }
+  const uint32_t per = (grid + kSms - 1) / kSms;
+  if (pieces <= 512) return grad_depth<T, GH, 1>(a, grid, per, (pieces + 31) / 32 * 32, s);
+  return grad_depth<T, GH, 2>(a, grid, per, ((pieces + 1) / 2 + 31) / 32 * 32, s);
+}
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+}  // namespace
+}  // namespace mxq
+
+extern "C" {
+
+mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld_x, const void* residual,
+                         int64_t ld_res, const void* weight, int weight_dt, double eps, void* hidden,
+                         uint8_t* qweight, uint8_t* scale, uint8_t* scale_swz, void* normed, float* rstd,
+                         mxq_stream_t stream) {
+  using namespace mxq;
+  if (!valid_dtype(dt) || !valid_dtype(weight_dt)) return MXQ_ERR_DTYPE;
+  if (M < 0 || N < 0 || N % 32 != 0 || ld_x < N || (residual && ld_res < N)) return MXQ_ERR_SHAPE;
+  // a row's elements are counted in 32 bits; rows on the grid's first axis
+  if (N > 0x3fffffe0ll || M > 0x7fffffffll || ld_x > (int64_t(1) << 40) || ld_res > (int64_t(1) << 40))
+    return MXQ_ERR_SHAPE;
+  if (!(eps >= 0.0)) return MXQ_ERR_ARG;
+  if ((residual == nullptr) != (hidden == nullptr)) return MXQ_ERR_ARG;
+  if (M == 0 || N == 0) return MXQ_OK;
+  if (!x || !weight || !qweight || !scale || !rstd) return MXQ_ERR_NULL;
+  const int es = elem_size(dt);
+  if (!aligned16(x) || (uint64_t(ld_x) * es) % 16 != 0 || !aligned16(weight) || !aligned16(qweight) ||
+      !aligned16(hidden) || !aligned16(normed) || !aligned16(residual) || !aligned16(scale_swz) ||
+      (residual && (uint64_t(ld_res) * es) % 16 != 0) || (reinterpret_cast<uintptr_t>(rstd) & 3u))
+    return MXQ_ERR_ALIGN;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.hidden = hidden;
+  a.q = qweight;
+  a.scale = scale;
+  a.swz = scale_swz;
+  a.normed = normed;
+  a.rstd = rstd;
+  a.ld_x = ld_x;
+  a.ld_res = ld_res;
+  a.M = M;
+  a.N = uint32_t(N);
+  a.S4 = uint32_t((N + 127) / 128);
+  a.eps = eps;
+  a.weight_bf16 = weight_dt == MXQ_BF16;
+  a.v8 = aligned32(x) && (uint64_t(ld_x) * es) % 32 == 0 && aligned32(hidden) && aligned32(normed) &&
+         aligned32(residual) && (!residual || (uint64_t(ld_res) * es) % 32 == 0);
+  a.scale_words = (reinterpret_cast<uintptr_t>(scale) & 3u) == 0 && (N / 32) % 4 == 0;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dt == MXQ_BF16) return residual ? norm_dispatch<uint16_t, true>(a, s) : norm_dispatch<uint16_t, false>(a, s);
+  return residual ? norm_dispatch<float, true>(a, s) : norm_dispatch<float, false>(a, s);
+}
+
+size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0) return 0;
+  return size_t(mxq::grad_parts(M, N)) * size_t(N) * sizeof(float);
+}
+
+mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, int64_t ld_g, const void* hidden,
+                                int64_t ld_h, const void* weight, int weight_dt, const float* rstd,
+                                const void* grad_hidden, int64_t ld_gh, void* dx, void* dweight, void* workspace,
+                                size_t workspace_bytes, mxq_stream_t stream) {
+  using namespace mxq;
+  if (!valid_dtype(dt) || !valid_dtype(weight_dt)) return MXQ_ERR_DTYPE;
+  if (M < 0 || N < 0 || N % 8 != 0 || ld_g < N || ld_h < N || (grad_hidden && ld_gh < N)) return MXQ_ERR_SHAPE;
+  if (N > 0x3fffffe0ll || M > 0x7fffffffll || ld_g > (int64_t(1) << 40) || ld_h > (int64_t(1) << 40) ||
+      ld_gh > (int64_t(1) << 40))
+    return MXQ_ERR_SHAPE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (N == 0) return MXQ_OK;
+  const int es = elem_size(dt);
+  if (M == 0) {                                       // a sum of no rows
+    if (!dweight) return MXQ_OK;
+    const cudaError_t e = cudaMemsetAsync(dweight, 0, size_t(N) * elem_size(weight_dt), s);
+    if (e != cudaSuccess) {
+      record_cuda_error(e);
+      return MXQ_ERR_CUDA;
+    }
+    return MXQ_OK;
+  }
+  if (!grad || !hidden || !weight || !rstd || !dx) return MXQ_ERR_NULL;
+  if (!aligned16(grad) || !aligned16(hidden) || !aligned16(weight) || !aligned16(grad_hidden) || !aligned16(dx) ||
+      (uint64_t(ld_g) * es) % 16 != 0 || (uint64_t(ld_h) * es) % 16 != 0 ||
+      (grad_hidden && (uint64_t(ld_gh) * es) % 16 != 0) || (reinterpret_cast<uintptr_t>(rstd) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dweight) & (weight_dt == MXQ_BF16 ? 1u : 3u)) || (dweight && !aligned16(workspace)))
+    return MXQ_ERR_ALIGN;
+  if (dweight && (!workspace || workspace_bytes < mxq_rmsnorm_backward_workspace_bytes(M, N)))
+    return MXQ_ERR_WORKSPACE;
+  GradArgs a{};
+  a.g = grad;
+  a.h = hidden;
+  a.gh = grad_hidden;
+  a.weight = weight;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.ld_g = ld_g;
+  a.ld_h = ld_h;
+  a.ld_gh = ld_gh;
+  a.M = M;
+  a.N = uint32_t(N);
+  a.weight_bf16 = weight_dt == MXQ_BF16;
+  const uint32_t parts = grad_parts(M, N);
+  mxq_status st;
+  if (dt == MXQ_BF16)
+    st = grad_hidden ? grad_dispatch<uint16_t, true>(a, parts, s) : grad_dispatch<uint16_t, false>(a, parts, s);
+  else
+    st = grad_hidden ? grad_dispatch<float, true>(a, parts, s) : grad_dispatch<float, false>(a, parts, s);
+  if (st != MXQ_OK || !dweight) return st;
+  return launched(launch_pdl_ex(rmsnorm_join_kernel, (a.N + 31) / 32, kThreads, 0, s,
+                                static_cast<const float*>(workspace), parts, a.N, dweight, a.weight_bf16));
+}
+
+}  // extern "C"
