@@ -171,6 +171,12 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// As above, after this thread's reads of shared memory that the other CTA
+// writes next.
+__device__ __forceinline__ void mbar_release_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // TMA load into this CTA's shared memory whose completion is counted on a
 // barrier of the pair (given by its shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map,
@@ -180,6 +186,23 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       " [%0], [%1, {%3, %4}], [%2];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
       : "memory");
+}
+
+// The same for a converged warp: issued by the lane that elect.sync picks.
+__device__ __forceinline__ void tma_elect_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t cluster_bar, int32_t x,
+                                                  int32_t y) {
+  asm volatile(
+      "{ .reg .pred e; elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2]; }"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_elect_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff;\n\t"
+               "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1; }" ::"r"(bar), "r"(bytes)
+               : "memory");
 }
 
 // The pair forms of mma_mxf8, tmem_copy_scales and mma_commit, for a

@@ -24,21 +24,6 @@
 // beyond an expert's rows only reaches output rows or columns that are not
 // stored: rows and columns of a product do not mix.
 //
-// One kernel, three shapes of tile:
-//  - PAIR: 256 x 256 over a cluster of two CTAs (tcgen05 cta_group::2), six
-//    stages of 32 KiB and 1.5 KiB of scales in each CTA;
-//  - 128 x 256 and 128 x 128 in one CTA, four and six stages.
-// Warps: 0 loads (TMA), 1 issues the MMAs, 2-9 are the epilogue: two warps a
-// quarter of the accumulator's lanes, each with half of its columns. Each
-// takes its columns into registers in one go (at most 128 fp32), hands the
-// accumulator back, and does everything else (SwiGLU, rounding, stores)
-// while the next tile's MMAs run: tensor memory has no room for a second
-// accumulator beside the scales.
-//  - SWIGLU: the B tile is 128 rows of the gate and the 128 rows of the up
-//    half with the same places (the pair's CTAs load one each), so a thread
-//    holds both factors of its outputs: D[r, h] = silu(gate) up is written
-//    and the halves never are.
-//
 // Waits are bounded as in mxfp8_gemm.cu.
 #include "common.cuh"
 #include "mxf8_mma.cuh"
@@ -53,6 +38,7 @@ constexpr uint32_t kSlicePitch = 80;
 constexpr uint32_t kSliceBytes = 32 * kSlicePitch;
 constexpr uint32_t kBarrierBytes = 256;
 
+// Tiles of the weights' gradients.
 template <bool PAIR, int BN>
 struct TileCfg {
   static constexpr uint32_t kRows = PAIR ? 256 : 128;                  // output rows of a tile
@@ -85,6 +71,9 @@ struct GroupArgs {
   uint32_t nb128;           // rows: 128-row blocks of an expert's B scales
   uint32_t tiles_m;         // wgrad: output tiles along Na
   uint32_t tiles_n;         // output tiles along the columns
+  uint32_t k;               // rows: K
+  const uint8_t* w;         // rows: the weights' codes and scales
+  const uint8_t* sfw;
 };
 
 // Walks the experts in order, 32 at a time in the lanes of a converged warp.
@@ -146,15 +135,14 @@ struct ExpertCursor {
 // An output tile's place: all lanes of a warp hold the same.
 struct Place {
   uint32_t expert;
-  uint32_t a_row, a_block;     // first row of A (rows) or of the tile along Na (wgrad), its 128-row scale block
-  uint32_t n_blk;
-  uint32_t kb0, nk;            // K blocks
-  uint32_t left;               // rows of D from the tile's first one on
-  uint64_t d_row;              // D's row of the tile's first one
+  uint32_t row, block;         // rows: its first row, and that row's 128-row scale block
+  uint32_t left;               // rows: rows of the expert from there on
+  uint32_t n_blk;              // tile along the columns
+  uint32_t m_blk;              // wgrad: tile along Na
+  uint32_t kb0, nk;            // wgrad: K blocks
 };
 
 // rows: the tile t of the list (rising from call to call); false behind the last.
-template <uint32_t ROWS>
 __device__ __forceinline__ bool find_rows(const GroupArgs& a, ExpertCursor& c, uint32_t t, uint32_t lane,
                                           Place& p) {
   for (;;) {
@@ -163,18 +151,15 @@ __device__ __forceinline__ bool find_rows(const GroupArgs& a, ExpertCursor& c, u
       const int j = __ffs(hit) - 1;
       const uint32_t incl = __shfl_sync(kFull, c.tiles, j), off0 = __shfl_sync(kFull, c.off0, j),
                      off1 = __shfl_sync(kFull, c.off1, j), blocks = __shfl_sync(kFull, c.blocks, j);
-      const uint32_t n = off1 - off0, tm = (n + ROWS - 1) / ROWS;
+      const uint32_t n = off1 - off0, tm = (n + c.unit - 1) / c.unit;
       const uint32_t local = t - (incl - tm) * a.tiles_n;
-      // row tiles first: neighbouring CTAs read the same rows of B
-      const uint32_t m = local % tm;
+      // row tiles first: neighbouring pairs read the same rows of B
       p.n_blk = local / tm;
+      const uint32_t m0 = (local - p.n_blk * tm) * c.unit;
       p.expert = c.first + j;
-      p.a_row = off0 + m * ROWS;
-      p.a_block = blocks - (n + 127) / 128 + m * (ROWS / 128);
-      p.kb0 = 0;
-      p.nk = a.nk;
-      p.left = n - m * ROWS;
-      p.d_row = p.a_row;
+      p.row = off0 + m0;
+      p.block = blocks - (n + 127) / 128 + m0 / 128;
+      p.left = n - m0;
       return true;
     }
     if (c.first + 32 >= c.E) return false;
@@ -183,7 +168,6 @@ __device__ __forceinline__ bool find_rows(const GroupArgs& a, ExpertCursor& c, u
 }
 
 // wgrad: every expert has the same tiles; what differs is where its columns lie.
-template <uint32_t ROWS>
 __device__ __forceinline__ bool find_wgrad(const GroupArgs& a, ExpertCursor& c, uint32_t t, uint32_t lane,
                                            Place& p) {
   const uint32_t per = a.tiles_m * a.tiles_n;
@@ -194,15 +178,11 @@ __device__ __forceinline__ bool find_wgrad(const GroupArgs& a, ExpertCursor& c, 
   const uint32_t blocks = __shfl_sync(kFull, c.blocks, j), off0 = __shfl_sync(kFull, c.off0, j),
                  off1 = __shfl_sync(kFull, c.off1, j);
   const uint32_t nk = (off1 - off0 + 127) / 128, total = a.rows / 128;
-  const uint32_t m = rest % a.tiles_m;
   p.n_blk = rest / a.tiles_m;
+  p.m_blk = rest - p.n_blk * a.tiles_m;
   p.expert = e;
-  p.a_row = m * ROWS;
-  p.a_block = m * (ROWS / 128);
   p.kb0 = min(blocks - nk, total);
   p.nk = min(nk, total - p.kb0);
-  p.left = a.rows_a - m * ROWS;
-  p.d_row = uint64_t(e) * a.rows_a + m * ROWS;
   return true;
 }
 
@@ -219,15 +199,366 @@ __device__ __forceinline__ float swiglu(float g, float u) {
   return __fdividef(g, 1.f + t * t) * u;
 }
 
-template <bool PAIR, int BN, bool WGRAD, bool SWIGLU, typename OutT>
+// ---------------------------------------------------------- rows
+//
+// The product is formed transposed: a pair of CTAs (tcgen05 cta_group::2)
+// holds 256 rows of the weight as the MMA's M side, and up to 256 of the
+// expert's rows as its N side, in steps of 32. The ragged side is so the one
+// whose size an MMA may choose: a tile of 20 rows costs an eighth of one of
+// 256, where rows on the M side would fill 128 or 256 whatever they are (the
+// first version's form: 32768 rows of 64 experts, 512 on average, padded by a
+// quarter).
+//
+// Per K block of 128 each CTA loads its 128 rows of the weight (16 KiB), its
+// half of the tile's rows (up to 16 KiB: one box of 128 rows for whole tiles,
+// else boxes of 16), and the scale tiles of both; six stages. The accumulator
+// has a weight row per lane and a row of the experts' per column.
+//
+// Warps: 0 loads, 1 (of the even CTA) issues the MMAs, 2-9 are the epilogue:
+// two a quarter of the lanes, each with half of the columns. Each takes its
+// columns into registers in one go (at most 128 fp32), hands the accumulator
+// back, and does everything else while the next tile's MMAs run: tensor memory
+// has no room for a second accumulator beside the scales. A column of 32 lanes
+// is 32 neighbouring outputs of a row, stored as 64 (bf16, lanes exchanging
+// halves of column pairs) or 128 bytes.
+//
+// SWIGLU: the even CTA holds 128 rows of the gate, the odd one the same rows of
+// the up half, so a pair of factors meets across the CTAs: of every 16 columns
+// the even CTA finishes the first eight and the odd one the last, and each
+// warp sends the other eight to its like in the peer's shared memory (st.async,
+// two slots of 1 KiB a warp, counted on a barrier of the receiver). The halves
+// are never written to memory.
+
+constexpr uint32_t kRowTile = 256;                          // most rows of a tile
+constexpr int kRowStages = 6;
+constexpr int kRowThreads = kGroupThreads + 64;             // and two more producers
+constexpr uint32_t kWeightTile = 128 * kBK;                 // a CTA's rows of the weight
+constexpr uint32_t kRowStage = 2 * kWeightTile;             // and the room for its half of the rows
+constexpr uint32_t kRowScales = 3 * kSfTile;                // weight, two tiles of rows
+constexpr uint32_t kRowSfCols = 12;
+constexpr uint32_t kSendBytes = 32 * 8 * 4;                 // eight columns of a warp
+constexpr uint32_t kRowBars = 512;
+constexpr uint32_t kRowSmem = kRowStages * (kRowStage + kRowScales) + kRowBars + 2 * kEpiWarps * kSendBytes + 1024;
+static_assert(256 + kRowStages * kRowSfCols <= 512, "tensor memory");
+static_assert(kRowSmem <= 232448, "shared memory");
+static_assert(8 * (2 * kRowStages + 2 + 4 * kEpiWarps) + 8 <= kRowBars, "barriers");
+
+// The rows in boxes of 128, 64, 32 and 16.
+struct RowMaps {
+  CUtensorMap box[4];
+};
+
+// Instruction descriptor as instr_desc_pair for N columns (a multiple of 32), k = 0.
+__device__ __forceinline__ uint32_t instr_desc_n(uint32_t n) {
+  return ((n >> 3) << 17) | (1u << 23) | (uint32_t(256 >> 4) << 24);
+}
+
+// Four words into a CTA's shared memory of the cluster, counted on its barrier.
+__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];"
+      ::"r"(dst), "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
+      : "memory");
+}
+
+// COLS columns v of this lane's weight row, the tile's rows t .. (COLS even): p is
+// this lane's output of row t (fp32), or of row t, t + 1 for an even, odd lane
+// the pair of outputs that its pair of lanes has (bf16). Rows from `left` on
+// are not written; left is 0 for lanes without outputs.
+template <int COLS, typename OutT>
+__device__ __forceinline__ void store_columns(OutT* p, uint32_t ld, const uint32_t* v, int32_t left) {
+  if constexpr (sizeof(OutT) == 2) {
+    const uint32_t odd = threadIdx.x & 1;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 2) {
+      const uint32_t x = __shfl_xor_sync(kFull, odd ? v[c] : v[c + 1], 1);
+      const uint32_t w = odd ? cvt_bf16x2(__uint_as_float(x), __uint_as_float(v[c + 1]))
+                             : cvt_bf16x2(__uint_as_float(v[c]), __uint_as_float(x));
+      if (c + int32_t(odd) < left) st_u32(p + uint64_t(uint32_t(c)) * ld, w);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < COLS; c++)
+      if (c < left) st_u32(p + uint64_t(uint32_t(c)) * ld, v[c]);
+  }
+}
+
+template <bool SWIGLU, typename OutT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowThreads, 1)
+mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ RowMaps rows,
+                  const __grid_constant__ CUtensorMap tma_sfw,
+                  const __grid_constant__ CUtensorMap tma_sfx, const __grid_constant__ GroupArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;           // operand tiles: 128-byte swizzle atoms of 1 KiB
+  uint8_t* smem = smem_raw + (base - raw);
+  const uint32_t scales = base + kRowStages * kRowStage;
+  const uint32_t slots = scales + kRowStages * kRowScales;          // what the peer sends
+  const uint32_t bars = slots + 2 * kEpiWarps * kSendBytes;
+  auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bars + 8u * (kRowStages + s); };
+  const uint32_t acc_full = bars + 8u * (2 * kRowStages);
+  const uint32_t acc_empty = acc_full + 8u;
+  const uint32_t sent0 = acc_empty + 8u;                            // [warp][slot]: the peer's columns are here
+  const uint32_t free0 = sent0 + 8u * 2 * kEpiWarps;                // [warp][slot]: the peer has read mine
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (free0 - base) + 8 * 2 * kEpiWarps);
+
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();                // 0: issues the MMAs
+  const uint32_t step = gridDim.x >> 1;
+  uint32_t tile = blockIdx.x >> 1;
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kRowStages; s++) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 2 * kEpiWarps);
+    for (int i = 0; i < 2 * kEpiWarps; i++) {
+      mbar_init(sent0 + 8u * i, 1);
+      mbar_init(free0 + 8u * i, 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  ExpertCursor cursor;
+  cursor.start(a.offsets, a.E, a.rows, kRowTile, lane);
+  Place p{};
+  // columns of a tile's accumulator: its rows, a multiple of 32
+  auto columns = [&]() { return min(kRowTile, (p.left + 31u) & ~31u); };
+
+  // rows of the weight and their scale block of this CTA in a tile
+  auto w_row_of = [&](const Place& q) {
+    return q.expert * a.b_rows + (SWIGLU ? q.n_blk * 128 + rank * a.n : q.n_blk * 256 + rank * 128);
+  };
+  auto w_blk_of = [&](const Place& q) {
+    return q.expert * a.nb128 + (SWIGLU ? q.n_blk + rank * (a.n / 128) : q.n_blk * 2 + rank);
+  };
+
+  if (warp == 0 || warp >= 2 + kEpiWarps) {
+    // --------------------------------------------------------- producers
+    // warp 0 loads the weight and its scales, warp 10 the rows, warp 11 their
+    // scales: the issue of a TMA load holds a warp for 100 cycles and more
+    const bool weights = warp == 0, scale_warp = warp == 3 + kEpiWarps;
+    const uint32_t bar0 = cluster_addr(full_bar(0), 0);
+    uint32_t s = 0, phase = 1;
+    bool ok = true;
+    for (; ok && find_rows(a, cursor, tile, lane, p); tile += step) {
+      const uint32_t n = columns(), mine = n / 2;         // this CTA's share of the rows, a multiple of 16
+      const uint32_t x_row = p.row + rank * mine;
+      const uint32_t w_row = w_row_of(p), w_sf = 4 * w_blk_of(p) * a.kp4;
+      const uint32_t x_sf = 4 * p.block * a.kp4;
+      const uint32_t tx = 2 * (kWeightTile + mine * kBK + kSfTile * (n > 128 ? 3 : 2));
+      for (uint32_t kb = 0; kb < a.nk; kb++) {
+        if (!__all_sync(kFull, mbar_wait(empty_bar(s), phase, kWaitNs))) {
+          if (lane == 0) record_error(a.err, kErrEmptyWait);
+          ok = false;
+          break;
+        }
+        const uint32_t bar = bar0 + 8u * s, x = kb * kBK;
+        const uint32_t st = base + s * kRowStage, sf = scales + s * kRowScales;
+        if (weights) {
+          if (rank == 0) mbar_elect_expect_tx(full_bar(s), tx);
+          tma_elect_2d_pair(st, &tma_w, bar, int32_t(x), int32_t(w_row));
+          tma_elect_2d_pair(sf, &tma_sfw, bar, 0, int32_t(w_sf + 4 * kb));
+        } else if (!scale_warp) {
+          uint32_t r = 0;
+#pragma unroll
+          for (int b = 0; b < 4; b++)
+            if (mine & (128u >> b)) {
+              tma_elect_2d_pair(st + kWeightTile + r * kBK, &rows.box[b], bar, int32_t(x), int32_t(x_row + r));
+              r += 128u >> b;
+            }
+        } else {
+          tma_elect_2d_pair(sf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
+          if (n > 128) tma_elect_2d_pair(sf + 2 * kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
+        }
+        if (++s == kRowStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer
+    // a converged warp with descriptors as 32-bit words plus offsets, as in
+    // mxfp8_gemm.cu
+    if (rank == 0 && a.nk > 0) {
+      const uint64_t op0 = operand_desc(base), sc0 = scale_desc(scales);
+      const uint32_t op_lo = uint32_t(op0), op_hi = uint32_t(op0 >> 32);
+      const uint32_t sc_lo = uint32_t(sc0), sc_hi = uint32_t(sc0 >> 32);
+      constexpr uint32_t kStageW = kRowStage >> 4, kTileW = kWeightTile >> 4;
+      constexpr uint32_t kScaleW = kRowScales >> 4, kSfW = kSfTile >> 4;
+      uint32_t s = 0, phase = 0, done = 0;
+      for (; find_rows(a, cursor, tile, lane, p); tile += step, done++) {
+        const uint32_t n = columns(), idesc = instr_desc_n(n);
+        // the epilogue must have read the previous tile's accumulator
+        if (done > 0 && !__all_sync(kFull, mbar_wait(acc_empty, (done - 1) & 1u, kWaitNs))) {
+          if (lane == 0) record_error(a.err, kErrAccumWait);
+          break;
+        }
+        tc_fence_after();
+        bool ok = true;
+        for (uint32_t kb = 0; kb < a.nk; kb++) {
+          if (!__all_sync(kFull, mbar_wait(full_bar(s), phase, kWaitNs))) {
+            if (lane == 0) record_error(a.err, kErrFullWait);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t so = s * kStageW, sc = sc_lo + s * kScaleW;
+          const uint32_t sfw_t = tmem + 256 + kRowSfCols * s, sfx_t = sfw_t + 4u;
+          tmem_copy_scales_pair(sfx_t, sc + kSfW, sc_hi);
+          if (n > 128) tmem_copy_scales_pair(sfx_t + 4u, sc + 2 * kSfW, sc_hi);
+          tmem_copy_scales_pair(sfw_t, sc, sc_hi);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; k++)
+            mma_mxf8_pair(tmem, op_lo + so + 2 * k, op_lo + so + kTileW + 2 * k, op_hi, idesc | (k << 4) | (k << 29),
+                          sfw_t | (k << 30), sfx_t | (k << 30), (kb | k) != 0u);
+          mma_commit_pair(empty_bar(s));
+          if (++s == kRowStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(acc_full);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    // warp w reads accumulator lanes (weight rows) 32 (w % 4) .. + 31; the
+    // second four warps take the second half of the columns
+    const uint32_t quarter = warp & 3, half = (warp - 2) >> 2, w = warp - 2;
+    const uint32_t lead_acc_empty = cluster_addr(acc_empty, 0);
+    const uint32_t peer_slots = cluster_addr(slots + w * 2 * kSendBytes, rank ^ 1u);
+    const uint32_t peer_sent = cluster_addr(sent0 + 16u * w, rank ^ 1u);
+    const uint32_t peer_free = cluster_addr(free0 + 16u * w, rank ^ 1u);
+    uint32_t done = 0, sends = 0, takes = 0;
+    bool ok = true;
+    for (; ok && find_rows(a, cursor, tile, lane, p); tile += step, done++) {
+      const uint32_t cols = columns() / 2;                // of this warp, a multiple of 16
+      const uint32_t taddr = tmem + ((quarter * 32) << 16) + half * cols;
+      uint32_t v[128];
+      if (a.nk > 0) {
+        // the phase completes once for everyone: a lane that saw it lets the warp go
+        if (!__any_sync(kFull, mbar_wait(acc_full, done & 1u, kWaitNs))) {
+          if (lane == 0) record_error(a.err, kErrAccumWait);
+          break;
+        }
+        tc_fence_after();
+        // (columns that the tile does not have are read and not used)
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32_start(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(lead_acc_empty);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 128; c++) v[c] = 0;
+      }
+      const uint32_t f = (SWIGLU ? p.n_blk * 128 : p.n_blk * 256 + rank * 128) + quarter * 32 + lane;
+      const uint32_t t0 = half * cols;
+      int32_t left = f < a.n ? int32_t(min(p.left, kRowTile)) - int32_t(t0) : 0;
+      OutT* d = static_cast<OutT*>(a.d) + uint64_t(p.row + t0 + (SWIGLU ? 8 * rank : 0)) * a.n + f;
+      if constexpr (sizeof(OutT) == 2) d += int64_t(lane & 1) * (int64_t(a.n) - 1);
+      if constexpr (!SWIGLU) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (uint32_t(c) >= cols) break;
+          store_columns<16>(d, a.n, &v[c], left);
+          d += 16 * uint64_t(a.n);
+          left -= 16;
+        }
+      } else {
+        // chunk i is columns 16 i .. + 15: this CTA finishes v[own + 0 .. 7] of
+        // it and sends the others; the next chunk is sent before this one's
+        // factors are waited for
+        left -= int32_t(8 * rank);
+        auto send = [&](const uint32_t* x) {
+          const uint32_t slot = sends & 1u;
+          if (sends >= 2 && !__all_sync(kFull, mbar_wait(free0 + 16u * w + 8u * slot, ((sends >> 1) - 1) & 1u, kWaitNs)))
+            return false;
+          if (lane == 0) mbar_expect_tx(sent0 + 16u * w + 8u * slot, kSendBytes);   // what the peer sends to this slot
+          const uint32_t dst = peer_slots + slot * kSendBytes + lane * 16, bar = peer_sent + 8u * slot;
+          send16(dst, bar, x[0], x[1], x[2], x[3]);
+          send16(dst + 512, bar, x[4], x[5], x[6], x[7]);
+          sends++;
+          return true;
+        };
+        ok = rank ? send(&v[0]) : send(&v[8]);
+#pragma unroll
+        for (int c = 0; c < 128; c += 16) {
+          if (uint32_t(c) >= cols || !ok) break;
+          if (c + 16 < 128 && uint32_t(c + 16) < cols) {
+            ok = rank ? send(&v[(c + 16) % 128]) : send(&v[(c + 24) % 128]);
+            if (!ok) break;
+          }
+          const uint32_t slot = takes & 1u;
+          ok = __all_sync(kFull, mbar_wait(sent0 + 16u * w + 8u * slot, (takes >> 1) & 1u, kWaitNs));
+          if (!ok) break;
+          const uint32_t src = slots + (2 * w + slot) * kSendBytes + lane * 16;
+          const uint4 q0 = lds128_u32(src), q1 = lds128_u32(src + 512);
+          __syncwarp();
+          if (lane == 0) mbar_release_remote(peer_free + 8u * slot);
+          takes++;
+          const uint32_t o[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const float mine = __uint_as_float(rank ? v[c + 8 + i] : v[c + i]), other = __uint_as_float(o[i]);
+            y[i] = __float_as_uint(rank ? swiglu(other, mine) : swiglu(mine, other));
+          }
+          store_columns<8>(d, a.n, y, left);
+          d += 16 * uint64_t(a.n);
+          left -= 16;
+        }
+        if (!ok && lane == 0) record_error(a.err, kErrAccumWait);
+      }
+    }
+  }
+
+  // neither CTA leaves while the other may still reach its shared memory or
+  // tensor memory (barrier arrivals, MMA operand reads, scale copies, sends)
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// --------------------------------------------------------- wgrad
+//
+// Output tiles of 256 x 256 over a pair of CTAs (cta_group::2, six stages of 32
+// KiB of operands in each CTA), or 128 x 128 in one CTA where a side has at
+// most 128: every expert has the same tiles, with as many K blocks as its rows
+// come to, and none for an expert without rows (zeros are written). Warps as
+// above; the accumulator has a row of D per lane, a warp's bf16 columns go
+// through 32 staging rows of its own.
+
+template <bool PAIR, int BN, typename OutT>
 __global__ void __launch_bounds__(kGroupThreads, 1)
-mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
+mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                    const __grid_constant__ CUtensorMap tma_sfa,
                    const __grid_constant__ CUtensorMap tma_sfb, const __grid_constant__ GroupArgs a) {
   using C = TileCfg<PAIR, BN>;
-  static_assert(!SWIGLU || BN == 256, "halves of 128 columns");
   constexpr int kStages = C::kStages;
-  constexpr uint32_t kOutCols = SWIGLU ? BN / 2 : BN;     // columns of D in a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;           // operand tiles: 128-byte swizzle atoms of 1 KiB
@@ -273,13 +604,8 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
   const uint32_t tmem = *tmem_slot;
 
   ExpertCursor cursor;
-  cursor.start(a.offsets, a.E, WGRAD ? 0x7fffff00u : a.rows, C::kRows, lane);
-  auto find = [&](Place& p) {
-    if constexpr (WGRAD)
-      return find_wgrad<C::kRows>(a, cursor, tile, lane, p);
-    else
-      return find_rows<C::kRows>(a, cursor, tile, lane, p);
-  };
+  // (rows are clamped by K blocks, in find_wgrad)
+  cursor.start(a.offsets, a.E, 0x7fffff00u, 128, lane);
   Place p;
 
   if (warp == 0) {
@@ -292,27 +618,11 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
         tma_load_2d(dst, map, bar, int32_t(x), int32_t(y));
     };
     uint32_t s = 0, phase = 1;
-    for (; find(p); tile += step) {
+    for (; find_wgrad(a, cursor, tile, lane, p); tile += step) {
       bool ok = true;
       if (lane == 0) {
-        // rows of B of this CTA's box(es) and the 128-row blocks of its scale tiles
-        uint32_t b_row, b_row1 = 0, b_blk, b_blk1;
-        if constexpr (WGRAD) {
-          b_row = p.n_blk * BN + (PAIR ? 128 * rank : 0);
-          b_blk = p.n_blk * C::kSfbTiles;
-          b_blk1 = b_blk + 1;
-        } else if constexpr (SWIGLU) {
-          const uint32_t gate = p.expert * a.b_rows + p.n_blk * 128, up = gate + a.n;
-          b_row = rank == 0 ? gate : up;
-          b_row1 = up;
-          b_blk = p.expert * a.nb128 + p.n_blk;
-          b_blk1 = b_blk + a.n / 128;
-        } else {
-          b_row = p.expert * a.b_rows + p.n_blk * BN + (PAIR ? 128 * rank : 0);
-          b_blk = p.expert * a.nb128 + p.n_blk * C::kSfbTiles;
-          b_blk1 = b_blk + 1;
-        }
-        const uint32_t a_row = p.a_row + 128 * rank, a_blk = p.a_block + rank;
+        const uint32_t a_row = p.m_blk * C::kRows + 128 * rank, a_blk = p.m_blk * (C::kRows / 128) + rank;
+        const uint32_t b_row = p.n_blk * BN + 128 * rank, b_blk = p.n_blk * C::kSfbTiles;
         for (uint32_t i = 0; i < p.nk; i++) {
           if (!mbar_wait(empty_bar(s), phase, kWaitNs)) {
             record_error(a.err, kErrEmptyWait);
@@ -324,11 +634,10 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
           const uint32_t st = base + s * C::kOperands, sf = scales + s * C::kScales;
           load(st, &tma_a, bar, kb * kBK, a_row);
           load(st + C::kTileA, &tma_b, bar, kb * kBK, b_row);
-          if constexpr (SWIGLU && !PAIR) load(st + C::kTileA + 128 * kBK, &tma_b, bar, kb * kBK, b_row1);
           load(sf, &tma_sfa, bar, 0, 4 * (a_blk * a.kp4 + kb));
           load(sf + kSfTile, &tma_sfb, bar, 0, 4 * (b_blk * a.kp4 + kb));
           if constexpr (C::kSfbTiles == 2)
-            load(sf + 2 * kSfTile, &tma_sfb, bar, 0, 4 * (b_blk1 * a.kp4 + kb));
+            load(sf + 2 * kSfTile, &tma_sfb, bar, 0, 4 * ((b_blk + 1) * a.kp4 + kb));
           if (++s == kStages) {
             s = 0;
             phase ^= 1u;
@@ -348,7 +657,7 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
       constexpr uint32_t kStageW = C::kOperands >> 4, kTileAW = C::kTileA >> 4;
       constexpr uint32_t kScaleW = C::kScales >> 4, kSfW = kSfTile >> 4;
       uint32_t s = 0, phase = 0, done = 0;
-      for (; find(p); tile += step) {
+      for (; find_wgrad(a, cursor, tile, lane, p); tile += step) {
         if (p.nk == 0) continue;
         // the epilogue must have read the previous tile's accumulator
         if (done > 0 && !__all_sync(kFull, mbar_wait(acc_empty, (done - 1) & 1u, kWaitNs))) {
@@ -403,16 +712,14 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
   } else {
     // ------------------------------------------------------------ epilogue
     // warp w reads accumulator lanes (rows) 32 (w % 4) .. + 31; the warps of
-    // the second four take the second half of the columns (SWIGLU: of each
-    // half's columns)
-    constexpr int kCols = BN / 2;                                     // accumulator columns of a warp
-    constexpr uint32_t kOut = kOutCols / 2;                           // columns of D of a warp
+    // the second four take the second half of the columns
+    constexpr int kCols = BN / 2;                                     // columns of a warp
     const uint32_t quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem + ((quarter * 32) << 16);
     const uint32_t slice = bars + kBarrierBytes + kSliceBytes * (warp - 2);
     const uint32_t lead_acc_empty = PAIR ? cluster_addr(acc_empty, 0) : acc_empty;
     uint32_t done = 0;
-    for (; find(p); tile += step) {
+    for (; find_wgrad(a, cursor, tile, lane, p); tile += step) {
       uint32_t v[kCols];
       if (p.nk > 0) {
         // the phase completes once for everyone: a lane that saw it lets the warp go
@@ -423,8 +730,7 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kCols; c += 32)
-          tmem_ld32_start(taddr + (SWIGLU ? (c < 64 ? 64 * half + c : 128 + 64 * half + c - 64) : kCols * half + c),
-                          *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+          tmem_ld32_start(taddr + kCols * half + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&v[c]));
         tc_fence_before();
@@ -440,24 +746,20 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
 #pragma unroll
         for (int c = 0; c < kCols; c++) v[c] = 0;
       }
-      if constexpr (SWIGLU) {
-#pragma unroll
-        for (int c = 0; c < 64; c++)
-          v[c] = __float_as_uint(swiglu(__uint_as_float(v[c]), __uint_as_float(v[c + 64])));
-      }
       const uint32_t r0 = 128 * rank + 32 * quarter;                  // the warp's first row of the tile
-      if (r0 >= p.left) continue;
-      const uint32_t rows = min(32u, p.left - r0);
-      const uint32_t col0 = p.n_blk * kOutCols + kOut * half;
+      const uint32_t row0 = p.m_blk * C::kRows + r0;
+      if (row0 >= a.rows_a) continue;
+      const uint32_t rows = min(32u, a.rows_a - row0);
+      const uint32_t col0 = p.n_blk * BN + kCols * half;
       if (col0 >= a.n) continue;
-      const uint32_t cols = min(kOut, a.n - col0);                    // a multiple of 16
-      OutT* d = static_cast<OutT*>(a.d) + (p.d_row + r0) * a.n + col0;
+      const uint32_t cols = min(uint32_t(kCols), a.n - col0);         // a multiple of 16
+      OutT* d = static_cast<OutT*>(a.d) + (uint64_t(p.expert) * a.rows_a + row0) * a.n + col0;
       if constexpr (sizeof(OutT) == 2) {
         // 32-column slices through the warp's staging rows, so that a store
         // instruction writes 64 bytes of each of eight rows
         const uint32_t rsub = lane >> 2, ch = lane & 3;
 #pragma unroll
-        for (uint32_t c0 = 0; c0 < kOut; c0 += 32) {
+        for (uint32_t c0 = 0; c0 < uint32_t(kCols); c0 += 32) {
 #pragma unroll
           for (int q = 0; q < 4; q++) {
             uint32_t w[4];
@@ -480,7 +782,7 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
         if (lane < rows) {
           OutT* drow = d + uint64_t(lane) * a.n;
 #pragma unroll
-          for (uint32_t c = 0; c < kOut; c += 4)
+          for (uint32_t c = 0; c < uint32_t(kCols); c += 4)
             if (c < cols) st_v4(drow + c, make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]));
         }
         __syncwarp();
@@ -509,10 +811,11 @@ mxfp8_group_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
 
 struct GroupMaps {
   CUtensorMap a, b, sfa, sfb;
+  RowMaps rows;                // rows: A
 };
 
 template <auto Kernel>
-uint32_t max_group_clusters(size_t smem) {
+uint32_t max_group_clusters(int threads, size_t smem) {
   static std::atomic<int> cached[256];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) dev = 0;
@@ -520,7 +823,7 @@ uint32_t max_group_clusters(size_t smem) {
   if (n > 0) return uint32_t(n);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 256);
-  cfg.blockDim = dim3(kGroupThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -537,20 +840,18 @@ uint32_t max_group_clusters(size_t smem) {
   return uint32_t(n);
 }
 
-// `most`: an upper bound of the output tiles.
-template <bool PAIR, int BN, bool WGRAD, bool SWIGLU, typename OutT>
-mxq_status launch_group(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
-  constexpr auto kernel = mxfp8_group_kernel<PAIR, BN, WGRAD, SWIGLU, OutT>;
-  constexpr uint32_t smem = TileCfg<PAIR, BN>::kSmem;
-  const cudaError_t attr_err = ensure_smem_limit<kernel>(int(smem));
+// Launches a persistent kernel of pairs (or of single CTAs) for at most `most` output tiles.
+template <auto Kernel, bool PAIR, int THREADS, typename... Args>
+mxq_status launch_group(uint32_t smem, uint64_t most, cudaStream_t s, const Args&... args) {
+  const cudaError_t attr_err = ensure_smem_limit<Kernel>(int(smem));
   if (attr_err != cudaSuccess) {
     record_cuda_error(attr_err);
     return MXQ_ERR_CUDA;
   }
-  const uint64_t resident = PAIR ? max_group_clusters<kernel>(smem) : uint64_t(sm_count());
+  const uint64_t resident = PAIR ? max_group_clusters<Kernel>(THREADS, smem) : uint64_t(sm_count());
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t(std::min(most, resident)) * (PAIR ? 2 : 1));
-  cfg.blockDim = dim3(kGroupThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -560,13 +861,18 @@ mxq_status launch_group(const GroupMaps& m, const GroupArgs& args, uint64_t most
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launched(cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, m.sfa, m.sfb, args));
+  return launched(cudaLaunchKernelEx(&cfg, Kernel, args...));
 }
 
-template <bool PAIR, int BN, bool WGRAD, bool SWIGLU>
-mxq_status launch_group(const GroupMaps& m, const GroupArgs& args, uint64_t most, int out_dt, cudaStream_t s) {
-  return out_dt == MXQ_BF16 ? launch_group<PAIR, BN, WGRAD, SWIGLU, uint16_t>(m, args, most, s)
-                            : launch_group<PAIR, BN, WGRAD, SWIGLU, float>(m, args, most, s);
+template <bool SWIGLU, typename OutT>
+mxq_status launch_rows(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
+  return launch_group<mxfp8_rows_kernel<SWIGLU, OutT>, true, kRowThreads>(kRowSmem, most, s, m.b, m.rows, m.sfb, m.sfa, args);
+}
+
+template <bool PAIR, int BN, typename OutT>
+mxq_status launch_wgrad(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
+  return launch_group<mxfp8_wgrad_kernel<PAIR, BN, OutT>, PAIR, kGroupThreads>(TileCfg<PAIR, BN>::kSmem, most, s, m.a, m.b, m.sfa,
+                                                                m.sfb, args);
 }
 
 }  // namespace
@@ -610,33 +916,29 @@ mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t 
   args.b_rows = uint32_t(N);
   args.nk = args.kp4 = uint32_t(kp4);
   args.nb128 = uint32_t(nb128);
+  args.k = uint32_t(K);
+  args.w = qb;
+  args.sfw = sb_swz;
   // experts that can have rows, and the tiles that they can have
   const uint64_t active = uint64_t(std::min<int64_t>(E, M));
-  const bool pair = M > 128 * int64_t(E);
-  const uint32_t sms = uint32_t(sm_count());
-  const bool narrow = !pair && !swiglu && active * ((uint64_t(N) + 255) / 256) < sms;
-  const uint32_t bn = narrow ? 128 : 256;
   if (K > 0) {
     if (!qa || !qb || !sa_swz || !sb_swz) return MXQ_ERR_NULL;
     if (!aligned16(qa) || !aligned16(qb) || !aligned16(sa_swz) || !aligned16(sb_swz)) return MXQ_ERR_ALIGN;
     // the blocks of no more than M rows, whatever the experts' padding
     if (sa_bytes < (M + 127) / 128 * kp4 * int64_t(kSfTile) || sa_bytes % int64_t(kSfTile) != 0) return MXQ_ERR_SHAPE;
-    if (!make_operand_map(&maps.a, qa, uint64_t(M), uint64_t(K), 128) ||
-        !make_operand_map(&maps.b, qb, uint64_t(N) * E, uint64_t(K), pair || swiglu ? 128u : bn) ||
+    for (int b = 0; b < 4; b++)
+      if (!make_operand_map(&maps.rows.box[b], qa, uint64_t(M), uint64_t(K), 128u >> b)) return MXQ_ERR_CUDA;
+    if (!make_operand_map(&maps.b, qb, uint64_t(N) * E, uint64_t(K), 128) ||
         !make_scale_map(&maps.sfa, sa_swz, uint64_t(sa_bytes)) ||
         !make_scale_map(&maps.sfb, sb_swz, uint64_t(nb128) * E * kp4 * kSfTile))
       return MXQ_ERR_CUDA;
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  args.tiles_n = swiglu ? uint32_t(N / 256) : uint32_t((N + bn - 1) / bn);
-  const uint64_t rows = pair ? 256 : 128;
-  const uint64_t most = (uint64_t(M) / rows + active) * args.tiles_n;
-  if (pair)
-    return swiglu ? launch_group<true, 256, false, true>(maps, args, most, out_dt, s)
-                  : launch_group<true, 256, false, false>(maps, args, most, out_dt, s);
-  if (swiglu) return launch_group<false, 256, false, true>(maps, args, most, out_dt, s);
-  return narrow ? launch_group<false, 128, false, false>(maps, args, most, out_dt, s)
-                : launch_group<false, 256, false, false>(maps, args, most, out_dt, s);
+  args.tiles_n = uint32_t((N + 255) / 256);               // swiglu: 128 rows of each half
+  const uint64_t most = (uint64_t(M) / kRowTile + active) * args.tiles_n;
+  if (out_dt == MXQ_BF16)
+    return swiglu ? launch_rows<true, uint16_t>(maps, args, most, s) : launch_rows<false, uint16_t>(maps, args, most, s);
+  return swiglu ? launch_rows<true, float>(maps, args, most, s) : launch_rows<false, float>(maps, args, most, s);
 }
 
 mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, const uint8_t* qb_t,
@@ -682,8 +984,9 @@ mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, 
   args.tiles_n = uint32_t(tiles_n);
   const uint64_t most = uint64_t(tiles_m) * uint64_t(tiles_n) * uint64_t(E);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return pair ? launch_group<true, 256, true, false>(maps, args, most, out_dt, s)
-              : launch_group<false, 128, true, false>(maps, args, most, out_dt, s);
+  if (out_dt == MXQ_BF16)
+    return pair ? launch_wgrad<true, 256, uint16_t>(maps, args, most, s) : launch_wgrad<false, 128, uint16_t>(maps, args, most, s);
+  return pair ? launch_wgrad<true, 256, float>(maps, args, most, s) : launch_wgrad<false, 128, float>(maps, args, most, s);
 }
 
 }  // extern "C"
