@@ -1021,31 +1021,33 @@ def mxfp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
     Returns an :class:`RmsNorm`. Records no gradient: :func:`rmsnorm_backward`
     computes it."""
     index = _same_device(x, weight)
-    dt, wdt = _code(x.dtype), _code(weight.dtype)
+    dtype, shape = x.dtype, x.shape
+    dt, wdt = _code(dtype), _code(weight.dtype)
     M, N, ld = _rows_view(x)
-    if weight.dim() != 1 or weight.shape[0] != N or not weight.is_contiguous():
+    if weight.shape != (N,) or not weight.is_contiguous():
         raise ValueError(f"expected a contiguous weight of {N} elements")
     if N % 32:
         raise ValueError("N must be a multiple of 32")
-    lead = x.shape[:-1]
-    hidden, ld_res = x, 0
+    lead = shape[:-1]
+    hidden, res, ld_res, out = x, None, 0, None
     if residual is not None:
-        _same_device(x, residual)
-        if residual.shape != x.shape or residual.dtype is not x.dtype:
+        if residual.get_device() != index:
+            raise ValueError("tensors must live on one CUDA device")
+        if residual.shape != shape or residual.dtype is not dtype:
             raise ValueError("residual must have x's shape and dtype")
         ld_res = _rows_view(residual)[2]
-        hidden = _empty_like(x, x.shape, x.dtype)
-    q = _empty_like(x, x.shape, torch.uint8)
+        hidden = _empty_like(x, shape, dtype)
+        res, out = residual.data_ptr(), hidden.data_ptr()
+    q = _empty_like(x, shape, torch.uint8)
     s = _empty_like(x, (*lead, N // 32), torch.uint8)
-    swz = _empty_like(x, (swizzled_scale_bytes(M, N // 32),), torch.uint8) if swizzled else None
-    y = _empty_like(x, x.shape, x.dtype) if normed else None
+    swz = _empty_like(x, ((M + 127) // 128 * 128 * ((N + 127) // 128 * 4),), torch.uint8) if swizzled else None
+    y = _empty_like(x, shape, dtype) if normed else None
     rstd = _empty_like(x, lead, torch.float32)
     if N == 0:
         rstd.fill_(float(eps) ** -0.5 if eps > 0 else math.inf)      # the mean of nothing is 0
-    _launch("mxfp8_rmsnorm", index, x.data_ptr(), dt, M, N, ld,
-            None if residual is None else residual.data_ptr(), ld_res, weight.data_ptr(), wdt, float(eps),
-            None if residual is None else hidden.data_ptr(), q.data_ptr(), s.data_ptr(),
-            None if swz is None else swz.data_ptr(), None if y is None else y.data_ptr(), rstd.data_ptr())
+    _launch("mxfp8_rmsnorm", index, x.data_ptr(), dt, M, N, ld, res, ld_res, weight.data_ptr(), wdt, eps, out,
+            q.data_ptr(), s.data_ptr(), None if swz is None else swz.data_ptr(),
+            None if y is None else y.data_ptr(), rstd.data_ptr())
     return RmsNorm(q, s, swz, hidden, rstd, y)
 
 
@@ -1060,31 +1062,32 @@ def rmsnorm_backward(grad: torch.Tensor, hidden: torch.Tensor, weight: torch.Ten
     Returns ``(grad_x, grad_weight)``: the gradient of h, and so of x and of
     the residual, like ``hidden``; the weight's like ``weight``. Computed in
     fp32; the sum over the rows has a fixed order. N a multiple of 8."""
-    index = _same_device(grad, hidden, weight, rstd)
-    dt, wdt = _code(hidden.dtype), _code(weight.dtype)
+    index = _same_device(hidden, grad, weight, rstd)
+    dtype, shape = hidden.dtype, hidden.shape
+    dt, wdt = _code(dtype), _code(weight.dtype)
     M, N, ld_h = _rows_view(hidden)
-    if weight.dim() != 1 or weight.shape[0] != N or not weight.is_contiguous():
+    if weight.shape != (N,) or not weight.is_contiguous():
         raise ValueError(f"expected a contiguous weight of {N} elements")
     if N % 8:
         raise ValueError("N must be a multiple of 8")
-    if rstd.dtype is not torch.float32 or rstd.shape != hidden.shape[:-1] or not rstd.is_contiguous():
+    if rstd.dtype is not torch.float32 or rstd.shape != shape[:-1] or not rstd.is_contiguous():
         raise TypeError("rstd must be contiguous fp32, one value a row")
-    lds = []
-    for t in (grad, grad_hidden):
-        if t is None:
-            lds.append(0)
-            continue
-        _same_device(hidden, t)
-        if t.shape != hidden.shape or t.dtype is not hidden.dtype:
+    if grad.shape != shape or grad.dtype is not dtype:
+        raise ValueError("the gradients must have hidden's shape and dtype")
+    ld_g = _rows_view(grad)[2]
+    gh, ld_gh = None, 0
+    if grad_hidden is not None:
+        if grad_hidden.get_device() != index:
+            raise ValueError("tensors must live on one CUDA device")
+        if grad_hidden.shape != shape or grad_hidden.dtype is not dtype:
             raise ValueError("the gradients must have hidden's shape and dtype")
-        lds.append(_rows_view(t)[2])
-    dx = _empty_like(hidden, hidden.shape, hidden.dtype)
+        gh, ld_gh = grad_hidden.data_ptr(), _rows_view(grad_hidden)[2]
+    dx = _empty_like(hidden, shape, dtype)
     dw = _empty_like(hidden, (N,), weight.dtype)
-    n = int(lib.mxq_rmsnorm_backward_workspace_bytes(M, N))
+    n = lib.mxq_rmsnorm_backward_workspace_bytes(M, N)
     work = _empty_like(hidden, (n,), torch.uint8)
-    _launch("mxq_rmsnorm_backward", index, grad.data_ptr(), dt, M, N, lds[0], hidden.data_ptr(), ld_h,
-            weight.data_ptr(), wdt, rstd.data_ptr(), None if grad_hidden is None else grad_hidden.data_ptr(),
-            lds[1], dx.data_ptr(), dw.data_ptr(), work.data_ptr(), n)
+    _launch("mxq_rmsnorm_backward", index, grad.data_ptr(), dt, M, N, ld_g, hidden.data_ptr(), ld_h,
+            weight.data_ptr(), wdt, rstd.data_ptr(), gh, ld_gh, dx.data_ptr(), dw.data_ptr(), work.data_ptr(), n)
     return dx, dw
 
 

@@ -221,11 +221,11 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
 
   // stages tile `tile` into input buffer `b`: 128 rows x 16 chunks of 16
   // bytes, 8 chunks per thread, zeros past M and N
-  auto stage = [&](uint32_t tile, int b) {
+  auto stage = [&](uint32_t tile, const TilePlace& p, int b) {
     const uint32_t ct = tile % a.n_ct;
-    const TilePlace p = place_of<FORM>(a, tile / a.n_ct, off, pb);
     const int64_t r0 = p.r0, c0 = int64_t(ct) * kTileCols;
     const int rows = p.rows;
+    if (FORM == kRagged && rows == 0) return;  // written as zeros below
     const int row_bytes = (a.N - c0 < kTileCols ? int(a.N - c0) : kTileCols) * kEsize;
     const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(smem + b * kInBytes));
 #pragma unroll
@@ -238,18 +238,25 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
   };
 
   int b = 0;
-  if (blockIdx.x < a.ntiles) stage(blockIdx.x, 0);
+  TilePlace next{};
+  if (blockIdx.x < a.ntiles) {
+    next = place_of<FORM>(a, blockIdx.x / a.n_ct, off, pb);
+    stage(blockIdx.x, next, 0);
+  }
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (uint32_t tile = blockIdx.x; tile < a.ntiles; tile += gridDim.x, b ^= 1) {
     // the next tile's copies go out before this one is worked on
-    if (tile + gridDim.x < a.ntiles) stage(tile + gridDim.x, b ^ 1);
+    const TilePlace p = next;
+    if (tile + gridDim.x < a.ntiles) {
+      next = place_of<FORM>(a, (tile + gridDim.x) / a.n_ct, off, pb);
+      stage(tile + gridDim.x, next, b ^ 1);
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();  // this tile is in shared memory; the previous one's outputs are written
 
     const uint8_t* in = smem + b * kInBytes;
     const uint32_t ct = tile % a.n_ct;
-    const TilePlace p = place_of<FORM>(a, tile / a.n_ct, off, pb);
     const int64_t r0 = p.r0, c0 = int64_t(ct) * kTileCols;
     // rows of the output: ragged tiles are whole, with zeros behind the expert's rows
     const int rows = FORM == kRagged ? kTileRows : p.rows;
@@ -298,7 +305,10 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
     }
     // column phase: word column w, group g (rows 32g .. 32g + 31 of the tile);
     // the codes go to the transposed tile qs[column][row].
-    {
+    if (FORM == kRagged && p.rows == 0) {  // columns of no row: zeros
+      for (int i = t; i < int(kQsBytes) / 16; i += kThreads) sts128(qs + 16 * i, make_uint4(0, 0, 0, 0));
+      if (t < int(kSsBytes) / 4) *reinterpret_cast<uint32_t*>(ss + 4 * t) = 0x7f7f7f7fu;
+    } else {
       const int w = t & (kWordCols - 1), g = t >> 6;
       const bool active = 32 * g < rows && w * 4 < row_bytes;
       uint4 code[kEsize == 2 ? 4 : 2];

@@ -199,6 +199,14 @@ __device__ __forceinline__ void tma_elect_2d_pair(uint32_t dst, const CUtensorMa
       : "memory");
 }
 
+__device__ __forceinline__ void tma_elect_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "{ .reg .pred e; elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2]; }"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
 __device__ __forceinline__ void mbar_elect_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("{ .reg .pred e; elect.sync _|e, 0xffffffff;\n\t"
                "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1; }" ::"r"(bar), "r"(bytes)

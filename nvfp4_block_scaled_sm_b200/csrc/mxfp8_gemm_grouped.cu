@@ -32,8 +32,8 @@ namespace mxq {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kGroupThreads = 32 * (2 + kEpiWarps);
-// staging of a warp's bf16 stores: 32 rows x 32 columns (64 bytes), pitch 80
+constexpr int kGroupThreads = 32 * (4 + kEpiWarps);   // warps: 0, 10, 11 load, 1 issues the MMAs, 2-9 are the epilogue
+// staging of a warp's stores: 32 rows x 64 bytes, pitch 80
 constexpr uint32_t kSlicePitch = 80;
 constexpr uint32_t kSliceBytes = 32 * kSlicePitch;
 constexpr uint32_t kBarrierBytes = 256;
@@ -231,7 +231,6 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 
 constexpr uint32_t kRowTile = 256;                          // most rows of a tile
 constexpr int kRowStages = 6;
-constexpr int kRowThreads = kGroupThreads + 64;             // and two more producers
 constexpr uint32_t kWeightTile = 128 * kBK;                 // a CTA's rows of the weight
 constexpr uint32_t kRowStage = 2 * kWeightTile;             // and the room for its half of the rows
 constexpr uint32_t kRowScales = 3 * kSfTile;                // weight, two tiles of rows
@@ -284,7 +283,7 @@ __device__ __forceinline__ void store_columns(OutT* p, uint32_t ld, const uint32
 }
 
 template <bool SWIGLU, typename OutT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kRowThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupThreads, 1)
 mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ RowMaps rows,
                   const __grid_constant__ CUtensorMap tma_sfw,
                   const __grid_constant__ CUtensorMap tma_sfx, const __grid_constant__ GroupArgs a) {
@@ -549,8 +548,8 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
 // KiB of operands in each CTA), or 128 x 128 in one CTA where a side has at
 // most 128: every expert has the same tiles, with as many K blocks as its rows
 // come to, and none for an expert without rows (zeros are written). Warps as
-// above; the accumulator has a row of D per lane, a warp's bf16 columns go
-// through 32 staging rows of its own.
+// above; the accumulator has a row of D per lane, a warp's columns go through
+// 32 staging rows of its own.
 
 template <bool PAIR, int BN, typename OutT>
 __global__ void __launch_bounds__(kGroupThreads, 1)
@@ -608,43 +607,44 @@ mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
   cursor.start(a.offsets, a.E, 0x7fffff00u, 128, lane);
   Place p;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
+  if (warp == 0 || warp >= 2 + kEpiWarps) {
+    // --------------------------------------------------------- producers
+    // (A and its scales, B, B's scales)
     const uint32_t bar0 = PAIR ? cluster_addr(full_bar(0), 0) : full_bar(0);
     auto load = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, uint32_t x, uint32_t y) {
       if constexpr (PAIR)
-        tma_load_2d_pair(dst, map, bar, int32_t(x), int32_t(y));
+        tma_elect_2d_pair(dst, map, bar, int32_t(x), int32_t(y));
       else
-        tma_load_2d(dst, map, bar, int32_t(x), int32_t(y));
+        tma_elect_2d(dst, map, bar, int32_t(x), int32_t(y));
     };
     uint32_t s = 0, phase = 1;
-    for (; find_wgrad(a, cursor, tile, lane, p); tile += step) {
-      bool ok = true;
-      if (lane == 0) {
-        const uint32_t a_row = p.m_blk * C::kRows + 128 * rank, a_blk = p.m_blk * (C::kRows / 128) + rank;
-        const uint32_t b_row = p.n_blk * BN + 128 * rank, b_blk = p.n_blk * C::kSfbTiles;
-        for (uint32_t i = 0; i < p.nk; i++) {
-          if (!mbar_wait(empty_bar(s), phase, kWaitNs)) {
-            record_error(a.err, kErrEmptyWait);
-            ok = false;
-            break;
-          }
-          if (rank == 0) mbar_expect_tx(full_bar(s), (PAIR ? 2 : 1) * C::kStageTx);
-          const uint32_t kb = p.kb0 + i, bar = bar0 + 8u * s;
-          const uint32_t st = base + s * C::kOperands, sf = scales + s * C::kScales;
+    bool ok = true;
+    for (; ok && find_wgrad(a, cursor, tile, lane, p); tile += step) {
+      const uint32_t a_row = p.m_blk * C::kRows + 128 * rank, a_blk = p.m_blk * (C::kRows / 128) + rank;
+      const uint32_t b_row = p.n_blk * BN + 128 * rank, b_blk = p.n_blk * C::kSfbTiles;
+      for (uint32_t i = 0; i < p.nk; i++) {
+        if (!__all_sync(kFull, mbar_wait(empty_bar(s), phase, kWaitNs))) {
+          if (lane == 0) record_error(a.err, kErrEmptyWait);
+          ok = false;
+          break;
+        }
+        const uint32_t kb = p.kb0 + i, bar = bar0 + 8u * s;
+        const uint32_t st = base + s * C::kOperands, sf = scales + s * C::kScales;
+        if (warp == 0) {
+          if (rank == 0) mbar_elect_expect_tx(full_bar(s), (PAIR ? 2 : 1) * C::kStageTx);
           load(st, &tma_a, bar, kb * kBK, a_row);
-          load(st + C::kTileA, &tma_b, bar, kb * kBK, b_row);
           load(sf, &tma_sfa, bar, 0, 4 * (a_blk * a.kp4 + kb));
+        } else if (warp == 2 + kEpiWarps) {
+          load(st + C::kTileA, &tma_b, bar, kb * kBK, b_row);
+        } else {
           load(sf + kSfTile, &tma_sfb, bar, 0, 4 * (b_blk * a.kp4 + kb));
-          if constexpr (C::kSfbTiles == 2)
-            load(sf + 2 * kSfTile, &tma_sfb, bar, 0, 4 * ((b_blk + 1) * a.kp4 + kb));
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1u;
-          }
+          if constexpr (C::kSfbTiles == 2) load(sf + 2 * kSfTile, &tma_sfb, bar, 0, 4 * ((b_blk + 1) * a.kp4 + kb));
+        }
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1u;
         }
       }
-      if (!__shfl_sync(kFull, int(ok), 0)) break;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
@@ -754,36 +754,33 @@ mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
       if (col0 >= a.n) continue;
       const uint32_t cols = min(uint32_t(kCols), a.n - col0);         // a multiple of 16
       OutT* d = static_cast<OutT*>(a.d) + (uint64_t(p.expert) * a.rows_a + row0) * a.n + col0;
-      if constexpr (sizeof(OutT) == 2) {
-        // 32-column slices through the warp's staging rows, so that a store
-        // instruction writes 64 bytes of each of eight rows
-        const uint32_t rsub = lane >> 2, ch = lane & 3;
+      // slices of 64 bytes a row (32 bf16 columns or 16 fp32) through the warp's
+      // staging rows, so that a store instruction writes 64 bytes of each of
+      // eight rows
+      constexpr uint32_t kSlice = 64 / sizeof(OutT);
+      const uint32_t rsub = lane >> 2, ch = lane & 3;
 #pragma unroll
-        for (uint32_t c0 = 0; c0 < uint32_t(kCols); c0 += 32) {
+      for (uint32_t c0 = 0; c0 < uint32_t(kCols); c0 += kSlice) {
+        if (c0 >= cols) break;
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            uint32_t w[4];
+        for (uint32_t q = 0; q < 4; q++) {
+          uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+          for (uint32_t i = 0; i < 4; i++) {
+            if constexpr (sizeof(OutT) == 2)
               w[i] = cvt_bf16x2(__uint_as_float(v[c0 + 8 * q + 2 * i]), __uint_as_float(v[c0 + 8 * q + 2 * i + 1]));
-            sts128_u32(slice + lane * kSlicePitch + 16 * q, make_uint4(w[0], w[1], w[2], w[3]));
+            else
+              w[i] = v[c0 + 4 * q + i];
           }
-          __syncwarp();
-          const uint32_t col = c0 + 8 * ch;
-#pragma unroll
-          for (uint32_t j = 0; j < 4; j++) {
-            const uint32_t rr = 8 * j + rsub;
-            const uint4 x = lds128_u32(slice + rr * kSlicePitch + 16 * ch);
-            if (rr < rows && col < cols) st_v4(d + uint64_t(rr) * a.n + col, x);
-          }
-          __syncwarp();
+          sts128_u32(slice + lane * kSlicePitch + 16 * q, make_uint4(w[0], w[1], w[2], w[3]));
         }
-      } else {
-        if (lane < rows) {
-          OutT* drow = d + uint64_t(lane) * a.n;
+        __syncwarp();
+        const uint32_t col = c0 + kSlice / 4 * ch;
 #pragma unroll
-          for (uint32_t c = 0; c < uint32_t(kCols); c += 4)
-            if (c < cols) st_v4(drow + c, make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]));
+        for (uint32_t j = 0; j < 4; j++) {
+          const uint32_t rr = 8 * j + rsub;
+          const uint4 x = lds128_u32(slice + rr * kSlicePitch + 16 * ch);
+          if (rr < rows && col < cols) st_v4(d + uint64_t(rr) * a.n + col, x);
         }
         __syncwarp();
       }
@@ -866,7 +863,7 @@ mxq_status launch_group(uint32_t smem, uint64_t most, cudaStream_t s, const Args
 
 template <bool SWIGLU, typename OutT>
 mxq_status launch_rows(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
-  return launch_group<mxfp8_rows_kernel<SWIGLU, OutT>, true, kRowThreads>(kRowSmem, most, s, m.b, m.rows, m.sfb, m.sfa, args);
+  return launch_group<mxfp8_rows_kernel<SWIGLU, OutT>, true, kGroupThreads>(kRowSmem, most, s, m.b, m.rows, m.sfb, m.sfa, args);
 }
 
 template <bool PAIR, int BN, typename OutT>

@@ -131,21 +131,36 @@ __device__ __forceinline__ void load_weight(float (&w)[16], const NormArgs& a, u
   }
 }
 
+// (a0 b0, a1 b1) and (a0 b0 + c0, a1 b1 + c1), each rounded once, in one instruction.
+__device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2v(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 // y of 16 elements of a row, their codes, the group's scale (two lanes a
-// group; the lanes of a warp call together) and, where asked for, y itself.
+// group, both or neither of them active; the lanes of a warp call together) and, where asked for, y itself.
 template <typename T>
-__device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, int64_t row, uint32_t c, float rstd,
-                                         bool active) {
+__device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, const float (&w)[16], int64_t row,
+                                         uint32_t c, float rstd, bool active) {
   const uint32_t lane = threadIdx.x & 31;
-  float w[16], y[16];
-  if (active) load_weight(w, a, c);
+  float2 y[8];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    const float2 u = mul2(h.lo(k), h.hi(k), rstd);
-    y[2 * k] = active ? u.x * w[2 * k] : 0.f;
-    y[2 * k + 1] = active ? u.y * w[2 * k + 1] : 0.f;
-    amax = fmaxf(amax, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));   // NaN raises no maximum
+    y[k] = mul2v(mul2(h.lo(k), h.hi(k), rstd), make_float2(w[2 * k], w[2 * k + 1]));
+    amax = fmaxf(amax, fmaxf(fabsf(y[k].x), fabsf(y[k].y)));   // NaN raises no maximum
   }
   amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
   const uint32_t b = mx_scale_byte<8>(amax);
@@ -153,7 +168,7 @@ __device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, in
   uint32_t code[8];
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    const float2 u = mul2(y[2 * k], y[2 * k + 1], mul);
+    const float2 u = mul2(y[k].x, y[k].y, mul);
     code[k] = cvt_e4m3x2(u.x, u.y);
   }
   // a word of the row's next four groups in every eighth lane; groups past N are zeros
@@ -176,8 +191,19 @@ __device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, in
   if (a.normed) {
     In16<T> o;
 #pragma unroll
-    for (int k = 0; k < 8; k++) set_pair(o, k, y[2 * k], y[2 * k + 1]);
+    for (int k = 0; k < 8; k++) set_pair(o, k, y[k].x, y[k].y);
     store16(static_cast<T*>(a.normed) + row * a.N + c, o, a.v8);
+  }
+}
+
+// The scale tiles' rows past M are zeros.
+__device__ __forceinline__ void pad_tiles(const NormArgs& a) {
+  if (!a.swz) return;
+  const uint64_t pad = (uint64_t(a.M + 127) & ~127ull) - uint64_t(a.M);
+  const uint64_t words = pad * a.S4;
+  for (uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += uint64_t(gridDim.x) * blockDim.x) {
+    const uint64_t r = uint64_t(a.M) + i / a.S4;
+    st_u32(a.swz + (((r >> 7) * a.S4 + i % a.S4) << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2), 0);
   }
 }
 
@@ -251,25 +277,26 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
     for (uint32_t c0 = (t & ~31u) * 16; c0 < a.N; c0 += a.row_threads * 16) {   // warps stay together
       const uint32_t c = c0 + lane * 16;
       const bool active = have && c < a.N;
-      if (active) load16(v[0], h + c, a.v8); else v[0].zero();
-      finish16(a, v[0], row, c, rstd, active);
+      float w[16];
+      if (active) {
+        load16(v[0], h + c, a.v8);
+        load_weight(w, a, c);
+      } else {
+        v[0].zero();
+      }
+      finish16(a, v[0], w, row, c, rstd, active);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < C; i++) {
       const uint32_t c = (i * a.row_threads + t) * 16;
-      finish16(a, v[i], row, c, rstd, have && c < a.N);
+      const bool active = have && c < a.N;
+      float w[16];
+      if (active) load_weight(w, a, c);
+      finish16(a, v[i], w, row, c, rstd, active);
     }
   }
-  // the tiles' rows past M are zeros
-  if (a.swz) {
-    const uint64_t pad = (uint64_t(a.M + 127) & ~127ull) - uint64_t(a.M);
-    const uint64_t words = pad * a.S4;
-    for (uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += uint64_t(gridDim.x) * blockDim.x) {
-      const uint64_t r = uint64_t(a.M) + i / a.S4;
-      st_u32(a.swz + (((r >> 7) * a.S4 + i % a.S4) << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2), 0);
-    }
-  }
+  pad_tiles(a);
 }
 
 template <typename T, bool RES, int C, bool LOOP>
@@ -319,145 +346,183 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Eight values of T from 16 (bf16) or 32 bytes.
+// Eight values of T, in pairs, from 16 (bf16) or 32 bytes.
 template <typename T>
 struct Row8 {
-  float f[8];
-  __device__ __forceinline__ void unpack(const uint4& q) {
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+  float2 f[4];
+  __device__ __forceinline__ void load(const uint4* p) { load(p[0], p[sizeof(T) / 2 - 1]); }
+  // from its 16-byte units (bf16: one, b is not used)
+  __device__ __forceinline__ void load(const uint4& a, const uint4& b) {
+    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      f[2 * k] = bf16_lo(u[k]);
-      f[2 * k + 1] = bf16_hi(u[k]);
-    }
-  }
-  __device__ __forceinline__ void load(const uint4* p) {
-    if constexpr (sizeof(T) == 2) {
-      unpack(p[0]);
-    } else {
-      const uint4 a = p[0], b = p[1];
-      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int k = 0; k < 8; k++) f[k] = __uint_as_float(u[k]);
-    }
+    for (int k = 0; k < 4; k++)
+      f[k] = sizeof(T) == 2 ? make_float2(bf16_lo(u[k]), bf16_hi(u[k]))
+                            : make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
   }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (sizeof(T) == 2) {
-      st_v4(p, make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7])));
+      st_v4(p, make_uint4(cvt_bf16x2(f[0].x, f[0].y), cvt_bf16x2(f[1].x, f[1].y), cvt_bf16x2(f[2].x, f[2].y),
+                          cvt_bf16x2(f[3].x, f[3].y)));
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; k += 4)
-        st_v4(p + k, make_uint4(__float_as_uint(f[k]), __float_as_uint(f[k + 1]), __float_as_uint(f[k + 2]), __float_as_uint(f[k + 3])));
+      for (int k = 0; k < 4; k += 2)
+        st_v4(p + 2 * k, make_uint4(__float_as_uint(f[k].x), __float_as_uint(f[k].y), __float_as_uint(f[k + 1].x),
+                                    __float_as_uint(f[k + 1].y)));
     }
   }
 };
 
-__device__ __forceinline__ void weight8(float (&w)[8], const GradArgs& a, uint32_t c) {
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ void weight8(float2 (&w)[4], const GradArgs& a, uint32_t c) {
   if (a.weight_bf16) {
-    Row8<uint16_t> r;
-    r.unpack(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c)));
-#pragma unroll
-    for (int k = 0; k < 8; k++) w[k] = r.f[k];
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c));
+    w[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+    w[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+    w[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z));
+    w[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
   } else {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c);
     const float4 q0 = __ldg(p), q1 = __ldg(p + 1);
-    w[0] = q0.x; w[1] = q0.y; w[2] = q0.z; w[3] = q0.w;
-    w[4] = q1.x; w[5] = q1.y; w[6] = q1.z; w[7] = q1.w;
+    w[0] = make_float2(q0.x, q0.y);
+    w[1] = make_float2(q0.z, q0.w);
+    w[2] = make_float2(q1.x, q1.y);
+    w[3] = make_float2(q1.z, q1.w);
   }
 }
 
-// Sum over the CTA of s; `red` is 32 floats that the next call does not use.
-__device__ __forceinline__ float block_sum(float s, float* red) {
+// Sums over the CTA of s[0 .. ROWS); `red` is 32 ROWS floats that the next call does not use.
+template <int ROWS>
+__device__ __forceinline__ void block_sums(float (&s)[ROWS], float* red) {
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-  if (lane == 0) red[warp] = s;
-  __syncthreads();
-  float r = lane < warps ? red[lane] : 0.f;
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(kFull, r, o);
-  return r;
+    for (int r = 0; r < ROWS; r++) s[r] += __shfl_xor_sync(kFull, s[r], o);
+  if (lane == 0)
+#pragma unroll
+    for (int r = 0; r < ROWS; r++) red[32 * r + warp] = s[r];
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < ROWS; r++) s[r] = lane < warps ? red[32 * r + lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int r = 0; r < ROWS; r++) s[r] += __shfl_xor_sync(kFull, s[r], o);
 }
 
-template <typename T, bool GH, int C, int DEPTH>
-__global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constant__ GradArgs a) {
+template <typename T, bool GH, int C, int ROWS, int DEPTH>
+__global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_constant__ GradArgs a) {
   pdl_enter();
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ float red[2][32];
-  constexpr uint32_t kPiece = 8 * sizeof(T);                       // bytes
+  __shared__ float red[2][32 * ROWS];
+  constexpr uint32_t kUnits = sizeof(T) / 2;                       // 16-byte units of a piece
+  constexpr uint32_t kTensors = GH ? 3 : 2;
   const uint32_t t = threadIdx.x, T0 = blockDim.x;
-  const uint32_t plane = T0 * C * kPiece;                          // one tensor's row in a stage
-  const uint32_t stage = plane * (GH ? 3 : 2);
+  const uint32_t plane = T0 * 16;                                  // a unit of all threads
+  const uint32_t stage = plane * C * kUnits * kTensors * ROWS;
   const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  auto fetch = [&](int64_t row, uint32_t s) {
-    if (row < a.M) {
+  // unit u of piece i of tensor k of row r in a stage
+  auto place = [&](uint32_t s, int r, uint32_t k, int i, uint32_t u) {
+    return s * stage + (((uint32_t(r) * kTensors + k) * C + uint32_t(i)) * kUnits + u) * plane + t * 16;
+  };
+  auto fetch = [&](int64_t row0, uint32_t s) {
 #pragma unroll
-      for (int i = 0; i < C; i++) {
-        const uint32_t c = (i * T0 + t) * 8;
-        if (c < a.N) {
-          const uint32_t dst = ring0 + s * stage + (i * T0 + t) * kPiece;
-          const T* g = static_cast<const T*>(a.g) + row * a.ld_g + c;
-          const T* h = static_cast<const T*>(a.h) + row * a.ld_h + c;
-          const T* gh = static_cast<const T*>(a.gh) + (GH ? row * a.ld_gh + c : 0);
+    for (int r = 0; r < ROWS; r++) {
+      const int64_t row = row0 + r;
+      if (row < a.M) {
 #pragma unroll
-          for (uint32_t b = 0; b < kPiece; b += 16) {
-            copy16(dst + b, reinterpret_cast<const uint8_t*>(g) + b);
-            copy16(dst + plane + b, reinterpret_cast<const uint8_t*>(h) + b);
-            if constexpr (GH) copy16(dst + 2 * plane + b, reinterpret_cast<const uint8_t*>(gh) + b);
+        for (int i = 0; i < C; i++) {
+          const uint32_t c = (i * T0 + t) * 8;
+          if (c < a.N) {
+            const T* g = static_cast<const T*>(a.g) + row * a.ld_g + c;
+            const T* h = static_cast<const T*>(a.h) + row * a.ld_h + c;
+            const T* gh = static_cast<const T*>(a.gh) + (GH ? row * a.ld_gh + c : 0);
+#pragma unroll
+            for (uint32_t u = 0; u < kUnits; u++) {
+              copy16(ring0 + place(s, r, 0, i, u), reinterpret_cast<const uint8_t*>(g) + 16 * u);
+              copy16(ring0 + place(s, r, 1, i, u), reinterpret_cast<const uint8_t*>(h) + 16 * u);
+              if constexpr (GH) copy16(ring0 + place(s, r, 2, i, u), reinterpret_cast<const uint8_t*>(gh) + 16 * u);
+            }
           }
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  auto read = [&](Row8<T>& v, uint32_t s, int r, uint32_t k, int i) {
+    v.load(*reinterpret_cast<const uint4*>(ring + place(s, r, k, i, 0)),
+           *reinterpret_cast<const uint4*>(ring + place(s, r, k, i, kUnits - 1)));
+  };
+  const int64_t stride = int64_t(gridDim.x) * ROWS;
 #pragma unroll
-  for (int s = 0; s < DEPTH - 1; s++) fetch(int64_t(blockIdx.x) + int64_t(s) * gridDim.x, s);
+  for (int s = 0; s < DEPTH - 1; s++) fetch(int64_t(blockIdx.x) * ROWS + s * stride, s);
 
-  float w[C][8], dw[C][8];
+  float2 w[C][4], dw[C][4];
 #pragma unroll
   for (int i = 0; i < C; i++) {
     const uint32_t c = (i * T0 + t) * 8;
     if (c < a.N) weight8(w[i], a, c);
 #pragma unroll
-    for (int k = 0; k < 8; k++) dw[i][k] = 0.f;
+    for (int k = 0; k < 4; k++) dw[i][k] = twice(0.f);
   }
   const float inv_n = 1.f / float(a.N);
   uint32_t s = 0, par = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, par ^= 1) {
+  float next[ROWS];                                                // 1 / rms of the rows to come
+  auto ask = [&](int64_t row) {
+#pragma unroll
+    for (int r = 0; r < ROWS; r++) next[r] = row + r < a.M ? __ldg(a.rstd + row + r) : 0.f;
+  };
+  ask(int64_t(blockIdx.x) * ROWS);
+  for (int64_t row = int64_t(blockIdx.x) * ROWS; row < a.M; row += stride, par ^= 1) {
     // the stage that was read last is filled again (each thread's own pieces)
-    fetch(row + int64_t(DEPTH - 1) * gridDim.x, s == 0 ? DEPTH - 1 : s - 1);
+    fetch(row + (DEPTH - 1) * stride, s == 0 ? DEPTH - 1 : s - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
-    const float rstd = __ldg(a.rstd + row);
-    const uint8_t* at = ring + s * stage;
-    Row8<T> gw[C], xh[C];
-    float sum = 0.f;
+    float rstd[ROWS], mean[ROWS];
 #pragma unroll
-    for (int i = 0; i < C; i++) {
-      if ((i * T0 + t) * 8 < a.N) {
-        gw[i].load(reinterpret_cast<const uint4*>(at + (i * T0 + t) * kPiece));
-        xh[i].load(reinterpret_cast<const uint4*>(at + plane + (i * T0 + t) * kPiece));
+    for (int r = 0; r < ROWS; r++) rstd[r] = next[r];
+    ask(row + stride);
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-          xh[i].f[k] *= rstd;
-          dw[i][k] = fmaf(gw[i].f[k], xh[i].f[k], dw[i][k]);
-          gw[i].f[k] *= w[i][k];
-          sum = fmaf(gw[i].f[k], xh[i].f[k], sum);
+    for (int r = 0; r < ROWS; r++) {
+      mean[r] = 0.f;
+      if (ROWS > 1 && row + r >= a.M) continue;
+      float2 sum = twice(0.f);
+#pragma unroll
+      for (int i = 0; i < C; i++) {
+        if ((i * T0 + t) * 8 < a.N) {
+          Row8<T> g, h;
+          read(g, s, r, 0, i);
+          read(h, s, r, 1, i);
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const float2 xh = mul2v(h.f[k], twice(rstd[r]));
+            dw[i][k] = fma2v(g.f[k], xh, dw[i][k]);
+            sum = fma2v(mul2v(g.f[k], w[i][k]), xh, sum);
+          }
         }
       }
+      mean[r] = sum.x + sum.y;
     }
-    const float mean = block_sum(sum, red[par]) * inv_n;
+    block_sums<ROWS>(mean, red[par]);
 #pragma unroll
-    for (int i = 0; i < C; i++) {
-      const uint32_t c = (i * T0 + t) * 8;
-      if (c < a.N) {
-        Row8<T> o;
-        if constexpr (GH) o.load(reinterpret_cast<const uint4*>(at + 2 * plane + (i * T0 + t) * kPiece));
+    for (int r = 0; r < ROWS; r++) {
+      if (ROWS > 1 && row + r >= a.M) continue;
+      mean[r] *= inv_n;
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const float d = fmaf(-xh[i].f[k], mean, gw[i].f[k]);
-          o.f[k] = GH ? fmaf(rstd, d, o.f[k]) : rstd * d;
+      for (int i = 0; i < C; i++) {
+        const uint32_t c = (i * T0 + t) * 8;
+        if (c < a.N) {
+          Row8<T> g, h, o;
+          read(g, s, r, 0, i);
+          read(h, s, r, 1, i);
+          if constexpr (GH) read(o, s, r, 2, i);
+#pragma unroll
+          for (int k = 0; k < 4; k++) {
+            const float2 d = fma2v(mul2v(h.f[k], twice(rstd[r])), twice(-mean[r]), mul2v(g.f[k], w[i][k]));
+            o.f[k] = GH ? fma2v(d, twice(rstd[r]), o.f[k]) : mul2v(d, twice(rstd[r]));
+          }
+          o.store(static_cast<T*>(a.dx) + (row + r) * int64_t(a.N) + c);
         }
-        o.store(static_cast<T*>(a.dx) + row * int64_t(a.N) + c);
       }
     }
     if (++s == DEPTH) s = 0;
@@ -469,8 +534,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_kernel(const __grid_constan
       if (c < a.N) {
         float* p = a.part + uint64_t(blockIdx.x) * a.N + c;
 #pragma unroll
-        for (int k = 0; k < 8; k += 4)
-          st_v4(p + k, make_uint4(__float_as_uint(dw[i][k]), __float_as_uint(dw[i][k + 1]), __float_as_uint(dw[i][k + 2]), __float_as_uint(dw[i][k + 3])));
+        for (int k = 0; k < 4; k += 2)
+          st_v4(p + 2 * k, make_uint4(__float_as_uint(dw[i][k].x), __float_as_uint(dw[i][k].y),
+                                      __float_as_uint(dw[i][k + 1].x), __float_as_uint(dw[i][k + 1].y)));
       }
     }
   }
@@ -487,26 +553,28 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_long_kernel(const __grid_co
     const float rstd = __ldg(a.rstd + row);
     const T* g = static_cast<const T*>(a.g) + row * a.ld_g;
     const T* h = static_cast<const T*>(a.h) + row * a.ld_h;
-    float sum = 0.f, w[8];
-    Row8<T> gw, xh;
+    float2 two = twice(0.f), w[4];
+    Row8<T> g8, h8;
     for (uint32_t c = threadIdx.x * 8; c < a.N; c += blockDim.x * 8) {
-      gw.load(reinterpret_cast<const uint4*>(g + c));
-      xh.load(reinterpret_cast<const uint4*>(h + c));
+      g8.load(reinterpret_cast<const uint4*>(g + c));
+      h8.load(reinterpret_cast<const uint4*>(h + c));
       weight8(w, a, c);
 #pragma unroll
-      for (int k = 0; k < 8; k++) sum = fmaf(gw.f[k] * w[k], xh.f[k] * rstd, sum);
+      for (int k = 0; k < 4; k++) two = fma2v(mul2v(g8.f[k], w[k]), mul2v(h8.f[k], twice(rstd)), two);
     }
-    const float mean = block_sum(sum, red[par]) * inv_n;
+    float sum[1] = {two.x + two.y};
+    block_sums<1>(sum, red[par]);
+    const float mean = sum[0] * inv_n;
     for (uint32_t c = threadIdx.x * 8; c < a.N; c += blockDim.x * 8) {
-      gw.load(reinterpret_cast<const uint4*>(g + c));
-      xh.load(reinterpret_cast<const uint4*>(h + c));
+      g8.load(reinterpret_cast<const uint4*>(g + c));
+      h8.load(reinterpret_cast<const uint4*>(h + c));
       weight8(w, a, c);
       Row8<T> o;
       if constexpr (GH) o.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.gh) + row * a.ld_gh + c));
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        const float d = fmaf(-(xh.f[k] * rstd), mean, gw.f[k] * w[k]);
-        o.f[k] = GH ? fmaf(rstd, d, o.f[k]) : rstd * d;
+      for (int k = 0; k < 4; k++) {
+        const float2 d = fma2v(mul2v(h8.f[k], twice(rstd)), twice(-mean), mul2v(g8.f[k], w[k]));
+        o.f[k] = GH ? fma2v(d, twice(rstd), o.f[k]) : mul2v(d, twice(rstd));
       }
       o.store(static_cast<T*>(a.dx) + row * int64_t(a.N) + c);
     }
@@ -519,18 +587,21 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_dweight_kernel(const __grid_
   pdl_enter();
   const uint32_t c = (blockIdx.x * kThreads + threadIdx.x) * 8;
   if (c >= a.N) return;
-  float dw[8] = {};
+  float2 dw[4] = {};
   for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
     const float rstd = __ldg(a.rstd + row);
     Row8<T> g, h;
     g.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.g) + row * a.ld_g + c));
     h.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.h) + row * a.ld_h + c));
 #pragma unroll
-    for (int k = 0; k < 8; k++) dw[k] = fmaf(g.f[k], h.f[k] * rstd, dw[k]);
+    for (int k = 0; k < 4; k++) dw[k] = fma2v(g.f[k], mul2v(h.f[k], twice(rstd)), dw[k]);
   }
   float* p = a.part + uint64_t(blockIdx.y) * a.N + c;
 #pragma unroll
-  for (int k = 0; k < 8; k++) p[k] = dw[k];
+  for (int k = 0; k < 4; k++) {
+    p[2 * k] = dw[k].x;
+    p[2 * k + 1] = dw[k].y;
+  }
 }
 
 // dweight[c] = the sum of `parts` partial sums, 32 columns a CTA, eight shares
@@ -562,28 +633,29 @@ constexpr uint32_t kRingBytes = 200 * 1024;
 // CTAs of the gradient, rows of the workspace: short rows need more CTAs on a
 // multiprocessor for as many bytes in flight.
 uint32_t grad_parts(int64_t M, int64_t N) {
-  const uint32_t per = N > 4096 ? 1 : N > 2048 ? 2 : N > 1024 ? 4 : 8;
+  const uint32_t per = N > 4096 ? 1 : N > 2048 ? 2 : 4;
   return uint32_t(std::min<int64_t>(M, int64_t(kSms) * per));
 }
 
-template <typename T, bool GH, int C, int DEPTH>
+template <typename T, bool GH, int C, int ROWS, int DEPTH>
 mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaStream_t s) {
-  const uint32_t smem = DEPTH * threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
-  const cudaError_t e = ensure_smem_limit<rmsnorm_grad_kernel<T, GH, C, DEPTH>>(int(kRingBytes));
+  const uint32_t smem = ROWS * DEPTH * threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
+  const cudaError_t e = ensure_smem_limit<rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>>(int(kRingBytes));
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return MXQ_ERR_CUDA;
   }
-  return launched(launch_pdl_ex(rmsnorm_grad_kernel<T, GH, C, DEPTH>, grid, threads, smem, s, a));
+  return launched(launch_pdl_ex(rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>, grid, threads, smem, s, a));
 }
 
+// Two rows at a time where two stages of them fit: one barrier for both.
 template <typename T, bool GH, int C>
 mxq_status grad_depth(const GradArgs& a, uint32_t grid, uint32_t per, uint32_t threads, cudaStream_t s) {
-  const uint32_t stage = threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
+  const uint32_t row = threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
   const uint32_t room = kRingBytes / per;
-  if (stage * 4 <= room) return launch_grad<T, GH, C, 4>(a, grid, threads, s);
-  if (stage * 2 <= room) return launch_grad<T, GH, C, 2>(a, grid, threads, s);
-  return launch_grad<T, GH, C, 1>(a, grid, threads, s);
+  if (row * 4 <= room) return launch_grad<T, GH, C, 2, 2>(a, grid, threads, s);
+  if (row * 2 <= room) return launch_grad<T, GH, C, 1, 2>(a, grid, threads, s);
+  return launch_grad<T, GH, C, 1, 1>(a, grid, threads, s);
 }
 
 template <typename T, bool GH>
@@ -604,8 +676,9 @@ mxq_status grad_dispatch(const GradArgs& a, uint32_t grid, cudaStream_t s) {
     return launched(cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel<T>, a));
   }
   const uint32_t per = (grid + kSms - 1) / kSms;
-  if (pieces <= 512) return grad_depth<T, GH, 1>(a, grid, per, (pieces + 31) / 32 * 32, s);
-  return grad_depth<T, GH, 2>(a, grid, per, ((pieces + 1) / 2 + 31) / 32 * 32, s);
+  if (pieces <= 128) return grad_depth<T, GH, 1>(a, grid, per, (pieces + 31) / 32 * 32, s);
+  if (pieces <= 1024) return grad_depth<T, GH, 2>(a, grid, per, ((pieces + 1) / 2 + 31) / 32 * 32, s);
+  return grad_depth<T, GH, 4>(a, grid, per, ((pieces + 3) / 4 + 31) / 32 * 32, s);
 }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
