@@ -240,6 +240,13 @@ def _empty_like(x: torch.Tensor, shape, dtype: torch.dtype) -> torch.Tensor:
     return _empty(shape, dtype, x.device)
 
 
+def _empty_as(x: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """:func:`_empty_like` with the shape of ``x`` (contiguous)."""
+    if _output_allocator is None and x.is_contiguous():
+        return torch.empty_like(x, dtype=dtype)                  # half a microsecond less than new_empty
+    return _empty_like(x, x.shape, dtype)
+
+
 def _zeros(shape, dtype: torch.dtype, device) -> torch.Tensor:
     return _empty(shape, dtype, device).zero_()
 
@@ -1036,12 +1043,12 @@ def mxfp8_rmsnorm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
         if residual.shape != shape or residual.dtype is not dtype:
             raise ValueError("residual must have x's shape and dtype")
         ld_res = _rows_view(residual)[2]
-        hidden = _empty_like(x, shape, dtype)
+        hidden = _empty_as(x, dtype)
         res, out = residual.data_ptr(), hidden.data_ptr()
-    q = _empty_like(x, shape, torch.uint8)
+    q = _empty_as(x, torch.uint8)
     s = _empty_like(x, (*lead, N // 32), torch.uint8)
     swz = _empty_like(x, ((M + 127) // 128 * 128 * ((N + 127) // 128 * 4),), torch.uint8) if swizzled else None
-    y = _empty_like(x, shape, dtype) if normed else None
+    y = _empty_as(x, dtype) if normed else None
     rstd = _empty_like(x, lead, torch.float32)
     if N == 0:
         rstd.fill_(float(eps) ** -0.5 if eps > 0 else math.inf)      # the mean of nothing is 0
@@ -1082,7 +1089,7 @@ def rmsnorm_backward(grad: torch.Tensor, hidden: torch.Tensor, weight: torch.Ten
         if grad_hidden.shape != shape or grad_hidden.dtype is not dtype:
             raise ValueError("the gradients must have hidden's shape and dtype")
         gh, ld_gh = grad_hidden.data_ptr(), _rows_view(grad_hidden)[2]
-    dx = _empty_like(hidden, shape, dtype)
+    dx = _empty_as(hidden, dtype)
     dw = _empty_like(hidden, (N,), weight.dtype)
     n = lib.mxq_rmsnorm_backward_workspace_bytes(M, N)
     work = _empty_like(hidden, (n,), torch.uint8)

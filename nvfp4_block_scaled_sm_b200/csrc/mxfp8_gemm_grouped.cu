@@ -132,6 +132,8 @@ struct ExpertCursor {
   }
 };
 
+constexpr uint32_t kBand = 8;  // row tiles of a band
+
 // An output tile's place: all lanes of a warp hold the same.
 struct Place {
   uint32_t expert;
@@ -153,9 +155,12 @@ __device__ __forceinline__ bool find_rows(const GroupArgs& a, ExpertCursor& c, u
                      off1 = __shfl_sync(kFull, c.off1, j), blocks = __shfl_sync(kFull, c.blocks, j);
       const uint32_t n = off1 - off0, tm = (n + c.unit - 1) / c.unit;
       const uint32_t local = t - (incl - tm) * a.tiles_n;
-      // row tiles first: neighbouring pairs read the same rows of B
-      p.n_blk = local / tm;
-      const uint32_t m0 = (local - p.n_blk * tm) * c.unit;
+      // bands of kBand row tiles, row tiles first in a band: neighbouring pairs
+      // read the same rows of B, and what the pairs read at one time stays in L2
+      const uint32_t band = local / (kBand * a.tiles_n), in_band = local - band * kBand * a.tiles_n;
+      const uint32_t rows = min(kBand, tm - band * kBand);
+      p.n_blk = in_band / rows;
+      const uint32_t m0 = (band * kBand + in_band - p.n_blk * rows) * c.unit;
       p.expert = c.first + j;
       p.row = off0 + m0;
       p.block = blocks - (n + 127) / 128 + m0 / 128;
