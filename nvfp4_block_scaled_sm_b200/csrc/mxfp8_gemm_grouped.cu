@@ -33,9 +33,9 @@ namespace {
 
 constexpr int kEpiWarps = 8;
 constexpr int kGroupThreads = 32 * (4 + kEpiWarps);   // warps: 0, 10, 11 load, 1 issues the MMAs, 2-9 are the epilogue
-// staging of a warp's stores: 32 rows x 64 bytes, pitch 80
-constexpr uint32_t kSlicePitch = 80;
-constexpr uint32_t kSliceBytes = 32 * kSlicePitch;
+// staging of a warp's stores: 16 rows x 128 bytes, pitch 144
+constexpr uint32_t kSlicePitch = 144;
+constexpr uint32_t kSliceBytes = 16 * kSlicePitch;
 constexpr uint32_t kBarrierBytes = 256;
 
 // Tiles of the weights' gradients.
@@ -554,7 +554,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
 // most 128: every expert has the same tiles, with as many K blocks as its rows
 // come to, and none for an expert without rows (zeros are written). Warps as
 // above; the accumulator has a row of D per lane, a warp's columns go through
-// 32 staging rows of its own.
+// staging rows of its own.
 
 template <bool PAIR, int BN, typename OutT>
 __global__ void __launch_bounds__(kGroupThreads, 1)
@@ -759,35 +759,41 @@ mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
       if (col0 >= a.n) continue;
       const uint32_t cols = min(uint32_t(kCols), a.n - col0);         // a multiple of 16
       OutT* d = static_cast<OutT*>(a.d) + (uint64_t(p.expert) * a.rows_a + row0) * a.n + col0;
-      // slices of 64 bytes a row (32 bf16 columns or 16 fp32) through the warp's
-      // staging rows, so that a store instruction writes 64 bytes of each of
-      // eight rows
-      constexpr uint32_t kSlice = 64 / sizeof(OutT);
-      const uint32_t rsub = lane >> 2, ch = lane & 3;
+      // slices of 128 bytes a row (64 bf16 columns or 32 fp32), 16 rows at a
+      // time, through the warp's staging rows, so that a store instruction
+      // writes whole 128-byte lines (with lines in halves the writes took 1.3
+      // times as long)
+      constexpr uint32_t kSlice = 128 / sizeof(OutT);
+      const uint32_t rsub = lane >> 3, ch = lane & 7;
 #pragma unroll
       for (uint32_t c0 = 0; c0 < uint32_t(kCols); c0 += kSlice) {
         if (c0 >= cols) break;
+        const uint32_t col = c0 + kSlice / 8 * ch;
 #pragma unroll
-        for (uint32_t q = 0; q < 4; q++) {
-          uint32_t w[4];
+        for (uint32_t h = 0; h < 2; h++) {
+          if (lane >> 4 == h) {
 #pragma unroll
-          for (uint32_t i = 0; i < 4; i++) {
-            if constexpr (sizeof(OutT) == 2)
-              w[i] = cvt_bf16x2(__uint_as_float(v[c0 + 8 * q + 2 * i]), __uint_as_float(v[c0 + 8 * q + 2 * i + 1]));
-            else
-              w[i] = v[c0 + 4 * q + i];
+            for (uint32_t q = 0; q < 8; q++) {
+              uint32_t w[4];
+#pragma unroll
+              for (uint32_t i = 0; i < 4; i++) {
+                if constexpr (sizeof(OutT) == 2)
+                  w[i] = cvt_bf16x2(__uint_as_float(v[c0 + 8 * q + 2 * i]), __uint_as_float(v[c0 + 8 * q + 2 * i + 1]));
+                else
+                  w[i] = v[c0 + 4 * q + i];
+              }
+              sts128_u32(slice + (lane & 15) * kSlicePitch + 16 * q, make_uint4(w[0], w[1], w[2], w[3]));
+            }
           }
-          sts128_u32(slice + lane * kSlicePitch + 16 * q, make_uint4(w[0], w[1], w[2], w[3]));
-        }
-        __syncwarp();
-        const uint32_t col = c0 + kSlice / 4 * ch;
+          __syncwarp();
 #pragma unroll
-        for (uint32_t j = 0; j < 4; j++) {
-          const uint32_t rr = 8 * j + rsub;
-          const uint4 x = lds128_u32(slice + rr * kSlicePitch + 16 * ch);
-          if (rr < rows && col < cols) st_v4(d + uint64_t(rr) * a.n + col, x);
+          for (uint32_t j = 0; j < 4; j++) {
+            const uint32_t rr = 4 * j + rsub;
+            const uint4 x = lds128_u32(slice + rr * kSlicePitch + 16 * ch);
+            if (16 * h + rr < rows && col < cols) st_v4(d + uint64_t(16 * h + rr) * a.n + col, x);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
   }
