@@ -323,9 +323,9 @@ mxq_status norm_dispatch(NormArgs& a, cudaStream_t s) {
 //
 // HBM-bound: per bf16 element 4 bytes read (6 with grad_hidden), 2 written.
 // Persistent CTAs take rows blockIdx.x, + grid, ...: a thread owns the same C
-// pieces of 8 columns in every row, so that the weight's gradient stays in its
+// 16-byte units of every row, so that the weight's gradient stays in its
 // registers until the end. Rows are copied into a ring of DEPTH rows in shared
-// memory with cp.async, each thread its own pieces: no thread waits for
+// memory with cp.async, each thread its own units: no thread waits for
 // another's copies, and the only barrier of a row is that of the sum
 // mean(g w xh). The CTAs' sums of dweight go to the workspace [grid, N] and a
 // second kernel adds them up in a fixed order. Rows of more than 16384
@@ -346,48 +346,56 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Eight values of T, in pairs, from 16 (bf16) or 32 bytes.
+// (plain: dx may be grad_hidden itself)
+__device__ __forceinline__ uint4 load_plain(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// The values of T in 16 bytes, in pairs.
 template <typename T>
-struct Row8 {
-  float2 f[4];
-  __device__ __forceinline__ void load(const uint4* p) { load(p[0], p[sizeof(T) / 2 - 1]); }
-  // from its 16-byte units (bf16: one, b is not used)
-  __device__ __forceinline__ void load(const uint4& a, const uint4& b) {
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+struct Unit {
+  static constexpr int kPairs = 8 / sizeof(T);
+  float2 f[kPairs];
+  __device__ __forceinline__ void load(const uint4& a) {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int k = 0; k < 4; k++)
+    for (int k = 0; k < kPairs; k++)
       f[k] = sizeof(T) == 2 ? make_float2(bf16_lo(u[k]), bf16_hi(u[k]))
-                            : make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
+                            : make_float2(__uint_as_float(u[2 * k % 4]), __uint_as_float(u[(2 * k + 1) % 4]));
   }
   __device__ __forceinline__ void store(T* p) const {
-    if constexpr (sizeof(T) == 2) {
+    if constexpr (sizeof(T) == 2)
       st_v4(p, make_uint4(cvt_bf16x2(f[0].x, f[0].y), cvt_bf16x2(f[1].x, f[1].y), cvt_bf16x2(f[2].x, f[2].y),
                           cvt_bf16x2(f[3].x, f[3].y)));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; k += 2)
-        st_v4(p + 2 * k, make_uint4(__float_as_uint(f[k].x), __float_as_uint(f[k].y), __float_as_uint(f[k + 1].x),
-                                    __float_as_uint(f[k + 1].y)));
-    }
+    else
+      st_v4(p, make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x),
+                          __float_as_uint(f[1].y)));
   }
 };
 
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
-__device__ __forceinline__ void weight8(float2 (&w)[4], const GradArgs& a, uint32_t c) {
+// The weights of P pairs of columns from c on (a multiple of 2 P).
+template <int P>
+__device__ __forceinline__ void weights_at(float2 (&w)[P], const GradArgs& a, uint32_t c) {
   if (a.weight_bf16) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c));
-    w[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
-    w[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
-    w[2] = make_float2(bf16_lo(q.z), bf16_hi(q.z));
-    w[3] = make_float2(bf16_lo(q.w), bf16_hi(q.w));
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.weight) + c);
+#pragma unroll
+    for (int k = 0; k < P; k += 2) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p + k));
+      w[k] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+      w[k + 1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
+    }
   } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c);
-    const float4 q0 = __ldg(p), q1 = __ldg(p + 1);
-    w[0] = make_float2(q0.x, q0.y);
-    w[1] = make_float2(q0.z, q0.w);
-    w[2] = make_float2(q1.x, q1.y);
-    w[3] = make_float2(q1.z, q1.w);
+    const float* p = static_cast<const float*>(a.weight) + c;
+#pragma unroll
+    for (int k = 0; k < P; k += 2) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(p + 2 * k));
+      w[k] = make_float2(q.x, q.y);
+      w[k + 1] = make_float2(q.z, q.w);
+    }
   }
 }
 
@@ -416,55 +424,53 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
   pdl_enter();
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][32 * ROWS];
-  constexpr uint32_t kUnits = sizeof(T) / 2;                       // 16-byte units of a piece
-  constexpr uint32_t kTensors = GH ? 3 : 2;
+  constexpr uint32_t kVec = 16 / sizeof(T);                        // columns of a unit
+  constexpr int kPairs = Unit<T>::kPairs;
+  constexpr bool kGhRing = GH && sizeof(T) == 2;                   // else grad_hidden goes through registers
+  constexpr uint32_t kTensors = kGhRing ? 3 : 2;
   const uint32_t t = threadIdx.x, T0 = blockDim.x;
   const uint32_t plane = T0 * 16;                                  // a unit of all threads
-  const uint32_t stage = plane * C * kUnits * kTensors * ROWS;
+  const uint32_t stage = plane * C * kTensors * ROWS;
   const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-  // unit u of piece i of tensor k of row r in a stage
-  auto place = [&](uint32_t s, int r, uint32_t k, int i, uint32_t u) {
-    return s * stage + (((uint32_t(r) * kTensors + k) * C + uint32_t(i)) * kUnits + u) * plane + t * 16;
+  auto column = [&](int i) { return (uint32_t(i) * T0 + t) * kVec; };
+  // unit i of tensor k of row r in a stage
+  auto place = [&](uint32_t s, int r, uint32_t k, int i) {
+    return s * stage + ((uint32_t(r) * kTensors + k) * C + uint32_t(i)) * plane + t * 16;
   };
   auto fetch = [&](int64_t row0, uint32_t s) {
 #pragma unroll
     for (int r = 0; r < ROWS; r++) {
       const int64_t row = row0 + r;
       if (row < a.M) {
+        const T* g = static_cast<const T*>(a.g) + row * a.ld_g;
+        const T* h = static_cast<const T*>(a.h) + row * a.ld_h;
+        const T* gh = static_cast<const T*>(a.gh) + (kGhRing ? row * a.ld_gh : 0);
 #pragma unroll
         for (int i = 0; i < C; i++) {
-          const uint32_t c = (i * T0 + t) * 8;
+          const uint32_t c = column(i);
           if (c < a.N) {
-            const T* g = static_cast<const T*>(a.g) + row * a.ld_g + c;
-            const T* h = static_cast<const T*>(a.h) + row * a.ld_h + c;
-            const T* gh = static_cast<const T*>(a.gh) + (GH ? row * a.ld_gh + c : 0);
-#pragma unroll
-            for (uint32_t u = 0; u < kUnits; u++) {
-              copy16(ring0 + place(s, r, 0, i, u), reinterpret_cast<const uint8_t*>(g) + 16 * u);
-              copy16(ring0 + place(s, r, 1, i, u), reinterpret_cast<const uint8_t*>(h) + 16 * u);
-              if constexpr (GH) copy16(ring0 + place(s, r, 2, i, u), reinterpret_cast<const uint8_t*>(gh) + 16 * u);
-            }
+            copy16(ring0 + place(s, r, 0, i), g + c);
+            copy16(ring0 + place(s, r, 1, i), h + c);
+            if constexpr (kGhRing) copy16(ring0 + place(s, r, 2, i), gh + c);
           }
         }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto read = [&](Row8<T>& v, uint32_t s, int r, uint32_t k, int i) {
-    v.load(*reinterpret_cast<const uint4*>(ring + place(s, r, k, i, 0)),
-           *reinterpret_cast<const uint4*>(ring + place(s, r, k, i, kUnits - 1)));
+  auto read = [&](Unit<T>& v, uint32_t s, int r, uint32_t k, int i) {
+    v.load(*reinterpret_cast<const uint4*>(ring + place(s, r, k, i)));
   };
   const int64_t stride = int64_t(gridDim.x) * ROWS;
 #pragma unroll
   for (int s = 0; s < DEPTH - 1; s++) fetch(int64_t(blockIdx.x) * ROWS + s * stride, s);
 
-  float2 w[C][4], dw[C][4];
+  float2 w[C][kPairs], dw[C][kPairs];
 #pragma unroll
   for (int i = 0; i < C; i++) {
-    const uint32_t c = (i * T0 + t) * 8;
-    if (c < a.N) weight8(w[i], a, c);
+    if (column(i) < a.N) weights_at(w[i], a, column(i));
 #pragma unroll
-    for (int k = 0; k < 4; k++) dw[i][k] = twice(0.f);
+    for (int k = 0; k < kPairs; k++) dw[i][k] = twice(0.f);
   }
   const float inv_n = 1.f / float(a.N);
   uint32_t s = 0, par = 0;
@@ -475,13 +481,22 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
   };
   ask(int64_t(blockIdx.x) * ROWS);
   for (int64_t row = int64_t(blockIdx.x) * ROWS; row < a.M; row += stride, par ^= 1) {
-    // the stage that was read last is filled again (each thread's own pieces)
+    // the stage that was read last is filled again (each thread's own units)
     fetch(row + (DEPTH - 1) * stride, s == 0 ? DEPTH - 1 : s - 1);
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
     float rstd[ROWS], mean[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; r++) rstd[r] = next[r];
     ask(row + stride);
+    uint4 gh[GH && !kGhRing ? ROWS * C : 1];
+    if constexpr (GH && !kGhRing) {
+#pragma unroll
+      for (int r = 0; r < ROWS; r++)
+#pragma unroll
+        for (int i = 0; i < C; i++)
+          if (column(i) < a.N && (ROWS == 1 || row + r < a.M))
+            gh[r * C + i] = load_plain(static_cast<const T*>(a.gh) + (row + r) * a.ld_gh + column(i));
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; r++) {
       mean[r] = 0.f;
@@ -489,12 +504,12 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
       float2 sum = twice(0.f);
 #pragma unroll
       for (int i = 0; i < C; i++) {
-        if ((i * T0 + t) * 8 < a.N) {
-          Row8<T> g, h;
+        if (column(i) < a.N) {
+          Unit<T> g, h;
           read(g, s, r, 0, i);
           read(h, s, r, 1, i);
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
+          for (int k = 0; k < kPairs; k++) {
             const float2 xh = mul2v(h.f[k], twice(rstd[r]));
             dw[i][k] = fma2v(g.f[k], xh, dw[i][k]);
             sum = fma2v(mul2v(g.f[k], w[i][k]), xh, sum);
@@ -508,20 +523,21 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
     for (int r = 0; r < ROWS; r++) {
       if (ROWS > 1 && row + r >= a.M) continue;
       mean[r] *= inv_n;
+      T* dx = static_cast<T*>(a.dx) + (row + r) * int64_t(a.N);
 #pragma unroll
       for (int i = 0; i < C; i++) {
-        const uint32_t c = (i * T0 + t) * 8;
-        if (c < a.N) {
-          Row8<T> g, h, o;
+        if (column(i) < a.N) {
+          Unit<T> g, h, o;
           read(g, s, r, 0, i);
           read(h, s, r, 1, i);
-          if constexpr (GH) read(o, s, r, 2, i);
+          if constexpr (kGhRing) read(o, s, r, 2, i);
+          if constexpr (GH && !kGhRing) o.load(gh[r * C + i]);
 #pragma unroll
-          for (int k = 0; k < 4; k++) {
+          for (int k = 0; k < kPairs; k++) {
             const float2 d = fma2v(mul2v(h.f[k], twice(rstd[r])), twice(-mean[r]), mul2v(g.f[k], w[i][k]));
             o.f[k] = GH ? fma2v(d, twice(rstd[r]), o.f[k]) : mul2v(d, twice(rstd[r]));
           }
-          o.store(static_cast<T*>(a.dx) + (row + r) * int64_t(a.N) + c);
+          o.store(dx + column(i));
         }
       }
     }
@@ -530,11 +546,10 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
   if (a.part) {
 #pragma unroll
     for (int i = 0; i < C; i++) {
-      const uint32_t c = (i * T0 + t) * 8;
-      if (c < a.N) {
-        float* p = a.part + uint64_t(blockIdx.x) * a.N + c;
+      if (column(i) < a.N) {
+        float* p = a.part + uint64_t(blockIdx.x) * a.N + column(i);
 #pragma unroll
-        for (int k = 0; k < 4; k += 2)
+        for (int k = 0; k < kPairs; k += 2)
           st_v4(p + 2 * k, make_uint4(__float_as_uint(dw[i][k].x), __float_as_uint(dw[i][k].y),
                                       __float_as_uint(dw[i][k + 1].x), __float_as_uint(dw[i][k + 1].y)));
       }
@@ -553,26 +568,27 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_long_kernel(const __grid_co
     const float rstd = __ldg(a.rstd + row);
     const T* g = static_cast<const T*>(a.g) + row * a.ld_g;
     const T* h = static_cast<const T*>(a.h) + row * a.ld_h;
-    float2 two = twice(0.f), w[4];
-    Row8<T> g8, h8;
-    for (uint32_t c = threadIdx.x * 8; c < a.N; c += blockDim.x * 8) {
-      g8.load(reinterpret_cast<const uint4*>(g + c));
-      h8.load(reinterpret_cast<const uint4*>(h + c));
-      weight8(w, a, c);
+    constexpr uint32_t kVec = 16 / sizeof(T);
+    float2 two = twice(0.f), w[Unit<T>::kPairs];
+    Unit<T> g8, h8;
+    for (uint32_t c = threadIdx.x * kVec; c < a.N; c += blockDim.x * kVec) {
+      g8.load(load_plain(g + c));
+      h8.load(load_plain(h + c));
+      weights_at(w, a, c);
 #pragma unroll
-      for (int k = 0; k < 4; k++) two = fma2v(mul2v(g8.f[k], w[k]), mul2v(h8.f[k], twice(rstd)), two);
+      for (int k = 0; k < Unit<T>::kPairs; k++) two = fma2v(mul2v(g8.f[k], w[k]), mul2v(h8.f[k], twice(rstd)), two);
     }
     float sum[1] = {two.x + two.y};
     block_sums<1>(sum, red[par]);
     const float mean = sum[0] * inv_n;
-    for (uint32_t c = threadIdx.x * 8; c < a.N; c += blockDim.x * 8) {
-      g8.load(reinterpret_cast<const uint4*>(g + c));
-      h8.load(reinterpret_cast<const uint4*>(h + c));
-      weight8(w, a, c);
-      Row8<T> o;
-      if constexpr (GH) o.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.gh) + row * a.ld_gh + c));
+    for (uint32_t c = threadIdx.x * kVec; c < a.N; c += blockDim.x * kVec) {
+      g8.load(load_plain(g + c));
+      h8.load(load_plain(h + c));
+      weights_at(w, a, c);
+      Unit<T> o;
+      if constexpr (GH) o.load(load_plain(static_cast<const T*>(a.gh) + row * a.ld_gh + c));
 #pragma unroll
-      for (int k = 0; k < 4; k++) {
+      for (int k = 0; k < Unit<T>::kPairs; k++) {
         const float2 d = fma2v(mul2v(h8.f[k], twice(rstd)), twice(-mean), mul2v(g8.f[k], w[k]));
         o.f[k] = GH ? fma2v(d, twice(rstd), o.f[k]) : mul2v(d, twice(rstd));
       }
@@ -581,24 +597,25 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_long_kernel(const __grid_co
   }
 }
 
-// dweight's partial sums of long rows: CTA (column block, share of the rows).
+// dweight's partial sums of long rows, before dx may overwrite an input: CTA
+// (column block, share of the rows).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rmsnorm_dweight_kernel(const __grid_constant__ GradArgs a) {
   pdl_enter();
-  const uint32_t c = (blockIdx.x * kThreads + threadIdx.x) * 8;
+  const uint32_t c = (blockIdx.x * kThreads + threadIdx.x) * (16 / sizeof(T));
   if (c >= a.N) return;
-  float2 dw[4] = {};
+  float2 dw[Unit<T>::kPairs] = {};
   for (int64_t row = blockIdx.y; row < a.M; row += gridDim.y) {
     const float rstd = __ldg(a.rstd + row);
-    Row8<T> g, h;
-    g.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.g) + row * a.ld_g + c));
-    h.load(reinterpret_cast<const uint4*>(static_cast<const T*>(a.h) + row * a.ld_h + c));
+    Unit<T> g, h;
+    g.load(load_plain(static_cast<const T*>(a.g) + row * a.ld_g + c));
+    h.load(load_plain(static_cast<const T*>(a.h) + row * a.ld_h + c));
 #pragma unroll
-    for (int k = 0; k < 4; k++) dw[k] = fma2v(g.f[k], mul2v(h.f[k], twice(rstd)), dw[k]);
+    for (int k = 0; k < Unit<T>::kPairs; k++) dw[k] = fma2v(g.f[k], mul2v(h.f[k], twice(rstd)), dw[k]);
   }
   float* p = a.part + uint64_t(blockIdx.y) * a.N + c;
 #pragma unroll
-  for (int k = 0; k < 4; k++) {
+  for (int k = 0; k < Unit<T>::kPairs; k++) {
     p[2 * k] = dw[k].x;
     p[2 * k + 1] = dw[k].y;
   }
@@ -628,18 +645,19 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_join_kernel(const float* __r
 
 constexpr uint32_t kLongRow = 16384;     // elements
 constexpr uint32_t kSms = 148;
-constexpr uint32_t kRingBytes = 200 * 1024;
+constexpr uint32_t kRingBytes = 225 * 1024;
 
-// CTAs of the gradient, rows of the workspace: short rows need more CTAs on a
-// multiprocessor for as many bytes in flight.
-uint32_t grad_parts(int64_t M, int64_t N) {
-  const uint32_t per = N > 4096 ? 1 : N > 2048 ? 2 : 4;
+// CTAs of the gradient: short rows need more of them on a multiprocessor for as
+// many bytes in flight (65536 x 1024 bf16: 75 us with four, 93 with eight;
+// 16384 x 4096: 68 with two of 256 threads, 82 with two of 512).
+uint32_t grad_ctas(int64_t M, int64_t row_bytes) {
+  const uint32_t per = row_bytes > 8192 ? 1 : row_bytes > 4096 ? 2 : 4;
   return uint32_t(std::min<int64_t>(M, int64_t(kSms) * per));
 }
 
 template <typename T, bool GH, int C, int ROWS, int DEPTH>
 mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaStream_t s) {
-  const uint32_t smem = ROWS * DEPTH * threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
+  const uint32_t smem = ROWS * DEPTH * threads * C * 16 * (GH && sizeof(T) == 2 ? 3 : 2);
   const cudaError_t e = ensure_smem_limit<rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>>(int(kRingBytes));
   if (e != cudaSuccess) {
     record_cuda_error(e);
@@ -648,37 +666,49 @@ mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaS
   return launched(launch_pdl_ex(rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>, grid, threads, smem, s, a));
 }
 
-// Two rows at a time where two stages of them fit: one barrier for both.
+// Two rows at a time, and one barrier for both, where two stages of them fit
+// (16384 x 7168 bf16: 109 us, one row at a time in four stages 131); rows of up
+// to two units a thread always do, with the CTAs that share a multiprocessor.
 template <typename T, bool GH, int C>
-mxq_status grad_depth(const GradArgs& a, uint32_t grid, uint32_t per, uint32_t threads, cudaStream_t s) {
-  const uint32_t row = threads * C * 8 * uint32_t(sizeof(T)) * (GH ? 3 : 2);
-  const uint32_t room = kRingBytes / per;
-  if (row * 4 <= room) return launch_grad<T, GH, C, 2, 2>(a, grid, threads, s);
-  if (row * 2 <= room) return launch_grad<T, GH, C, 1, 2>(a, grid, threads, s);
-  return launch_grad<T, GH, C, 1, 1>(a, grid, threads, s);
+mxq_status grad_depth(const GradArgs& a, uint32_t grid, uint32_t threads, cudaStream_t s) {
+  const uint32_t row = threads * C * 16 * (GH && sizeof(T) == 2 ? 3 : 2);
+  if constexpr (C <= 2)
+    return launch_grad<T, GH, C, 2, 2>(a, grid, threads, s);
+  else if constexpr (C == 4)
+    return row * 4 <= kRingBytes ? launch_grad<T, GH, C, 2, 2>(a, grid, threads, s)
+                                 : launch_grad<T, GH, C, 1, 2>(a, grid, threads, s);
+  else
+    return row * 2 <= kRingBytes ? launch_grad<T, GH, C, 1, 2>(a, grid, threads, s)
+                                 : launch_grad<T, GH, C, 1, 1>(a, grid, threads, s);
 }
 
 template <typename T, bool GH>
 mxq_status grad_dispatch(const GradArgs& a, uint32_t grid, cudaStream_t s) {
-  const uint32_t pieces = a.N / 8;
+  constexpr uint32_t kVec = 16 / sizeof(T);
+  const uint32_t units = (a.N + kVec - 1) / kVec;
   if (a.N > kLongRow) {
-    const mxq_status st = launched(launch_pdl_ex(rmsnorm_grad_long_kernel<T, GH>, grid, 1024, 0, s, a));
-    if (st != MXQ_OK || !a.part) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((pieces + kThreads - 1) / kThreads, grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return launched(cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel<T>, a));
+    if (a.part) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((units + kThreads - 1) / kThreads, grid);
+      cfg.blockDim = dim3(kThreads);
+      cfg.stream = s;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      const mxq_status st = launched(cudaLaunchKernelEx(&cfg, rmsnorm_dweight_kernel<T>, a));
+      if (st != MXQ_OK) return st;
+    }
+    return launched(launch_pdl_ex(rmsnorm_grad_long_kernel<T, GH>, grid, 1024, 0, s, a));
   }
-  const uint32_t per = (grid + kSms - 1) / kSms;
-  if (pieces <= 128) return grad_depth<T, GH, 1>(a, grid, per, (pieces + 31) / 32 * 32, s);
-  if (pieces <= 1024) return grad_depth<T, GH, 2>(a, grid, per, ((pieces + 1) / 2 + 31) / 32 * 32, s);
-  return grad_depth<T, GH, 4>(a, grid, per, ((pieces + 3) / 4 + 31) / 32 * 32, s);
+  // units of a thread: one for short rows, two up to 512 threads, and as many
+  // as it takes beyond
+  auto threads = [&](uint32_t c) { return ((units + c - 1) / c + 31) / 32 * 32; };
+  if (units <= 128) return grad_depth<T, GH, 1>(a, grid, threads(1), s);
+  if (units <= 1024) return grad_depth<T, GH, 2>(a, grid, threads(2), s);
+  if (sizeof(T) == 2 || units <= 2048) return grad_depth<T, GH, 4>(a, grid, threads(4), s);
+  return grad_depth<T, GH, sizeof(T) == 2 ? 4 : 8>(a, grid, threads(8), s);
 }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
@@ -734,7 +764,7 @@ mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld
 
 size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
   if (M <= 0 || N <= 0) return 0;
-  return size_t(mxq::grad_parts(M, N)) * size_t(N) * sizeof(float);
+  return size_t(mxq::grad_ctas(M, 2 * N)) * size_t(N) * sizeof(float);   // (fp32 rows take no more)
 }
 
 mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, int64_t ld_g, const void* hidden,
@@ -781,7 +811,7 @@ mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, 
   a.M = M;
   a.N = uint32_t(N);
   a.weight_bf16 = weight_dt == MXQ_BF16;
-  const uint32_t parts = grad_parts(M, N);
+  const uint32_t parts = grad_ctas(M, N * es);
   mxq_status st;
   if (dt == MXQ_BF16)
     st = grad_hidden ? grad_dispatch<uint16_t, true>(a, parts, s) : grad_dispatch<uint16_t, false>(a, parts, s);

@@ -125,14 +125,16 @@ def test_hidden_in_place_of_an_input(dtype, N, into):
 @pytest.mark.parametrize("into", ["grad", "grad_hidden"])
 def test_gradient_in_place_of_an_input(dtype, N, into):
     M, code = 300, 0 if dtype == BF16 else 1
-    g, h, gh, w = (normal(i, M, N, dtype=dtype) for i in (1, 2, 3)), None, None, normal(4, N)
-    g, h, gh = g
+    g, h, gh = (normal(i, M, N, dtype=dtype) for i in (1, 2, 3))
+    w = normal(4, N)
     rstd = torch.rsqrt(h.double().square().mean(1) + 1e-6).float()
-    want, _ = mxq.rmsnorm_backward(g, h, w, rstd, grad_hidden=gh)
-    out = g if into == "grad" else gh
+    want, want_w = mxq.rmsnorm_backward(g, h, w, rstd, grad_hidden=gh)
+    out, dw = g if into == "grad" else gh, torch.empty_like(w)
+    n = mxq.lib.mxq_rmsnorm_backward_workspace_bytes(M, N)
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
     st = torch.cuda.current_stream().cuda_stream
-    assert mxq.lib.mxq_rmsnorm_backward(ptr(g), code, M, N, N, ptr(h), N, ptr(w), 0, ptr(rstd), ptr(gh), N, ptr(out), None, None, 0, st) == 0
-    assert torch.equal(out, want)
+    assert mxq.lib.mxq_rmsnorm_backward(ptr(g), code, M, N, N, ptr(h), N, ptr(w), 0, ptr(rstd), ptr(gh), N, ptr(out), ptr(dw), ptr(work), n, st) == 0
+    assert torch.equal(out, want) and torch.equal(dw, want_w)
 
 
 def test_without_a_weight_gradient_no_workspace_is_touched():

@@ -101,7 +101,7 @@ def test_empty_rows_and_columns():
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("M,N", [(1, 8), (3, 96), (400, 136), (61, 1056), (300, 2048), (500, 4096), (150, 4104), (333, 7168),
-                                 (5, 16384), (9, 16392), (160, 20480)])
+                                 (301, 8192), (300, 9216), (5, 16384), (9, 16392), (160, 20480)])
 def test_gradient(M, N, dtype):
     for wd, with_hidden in ((dtype, True), (FP32, False)):
         g, h, w = rows(M, M, N, dtype, 0.1), rows(N, M, N, dtype), weights(7, N, wd)
