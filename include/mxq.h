@@ -350,11 +350,9 @@ mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
  *  error_flag  as for mxfp8_gemm.
  * K % 32 == 0; N % 16 == 0, with swiglu N % 256 == 0 (each half is whole scale
  * tiles); pointers 16-byte aligned. K == 0 writes zeros into the experts' rows.
- * M, N, K and E * N are below 2^31 - 256, and the scales of either side below
- * 2^38 bytes. One launch of persistent CTAs of 320 threads: pairs over 256 x
- * 256 output tiles when the experts have more than 128 rows on average, single
- * CTAs over 128 x 256 tiles otherwise (128 x 128 when those are too few for
- * the multiprocessors). */
+ * M, N and E * N are below 2^31 - 256, K at most 2^26, and the scales of either
+ * side below 2^38 bytes. One launch of persistent pairs of CTAs (384 threads and about
+ * 218 KB of shared memory each) over tiles of up to 256 rows x 256 columns. */
 mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t sa_bytes,
                               const uint8_t* qb, const uint8_t* sb_swz, int32_t E,
                               const int64_t* row_offsets, int64_t M, int64_t N, int64_t K, int swiglu,
@@ -399,11 +397,12 @@ mxq_status mxfp8_quantize_columnwise_stacked(const void* x, int dt, int32_t E, i
  * exact, fp32 sums).
  *  qa_t [Na, P], sa_swz its scales; qb_t [Nb, P], sb_swz its scales;
  *  P % 128 == 0 (mxq_grouped_padded_rows), Nb % 16 == 0.
- *  row_offsets  as above; columns from P on are not read, whatever the offsets.
+ *  row_offsets  the same, within the rows that were quantized (no column from P
+ *          on is read, whatever they hold).
  *  d       [E, Na, Nb] row-major, bf16 or fp32; experts without rows get zeros.
  *  error_flag  as for mxfp8_gemm.
- * Limits and launch as for mxfp8_gemm_grouped (pairs of CTAs when Na > 128 and
- * Nb > 128, otherwise 128 x 128 tiles). */
+ * Na, Nb and P are limited as N and K are in mxfp8_gemm_grouped. One launch: pairs of CTAs over 256 x 256
+ * tiles when Na > 128 and Nb > 128, otherwise CTAs over 128 x 128 tiles. */
 mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, const uint8_t* qb_t,
                                     const uint8_t* sb_swz, int32_t E, const int64_t* row_offsets,
                                     int64_t P, int64_t Na, int64_t Nb, void* d, int out_dt,

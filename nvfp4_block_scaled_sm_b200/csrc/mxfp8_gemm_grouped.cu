@@ -37,15 +37,16 @@ constexpr int kGroupThreads = 32 * (4 + kEpiWarps);   // warps: 0, 10, 11 load, 
 constexpr uint32_t kSlicePitch = 144;
 constexpr uint32_t kSliceBytes = 16 * kSlicePitch;
 constexpr uint32_t kBarrierBytes = 256;
+constexpr int64_t kMostSum = int64_t(1) << 26;  // terms of a sum: a tile takes less than the waits' limit
 
 // Tiles of the weights' gradients.
-template <bool PAIR, int BN>
+template <bool PAIR>
 struct TileCfg {
+  static constexpr int BN = PAIR ? 256 : 128;
   static constexpr uint32_t kRows = PAIR ? 256 : 128;                  // output rows of a tile
-  static constexpr uint32_t kBRows = PAIR ? 128 : BN;                  // rows of B that a CTA loads
-  static constexpr int kStages = PAIR || BN == 128 ? 6 : 4;
-  static constexpr uint32_t kTileA = 128 * kBK, kTileB = kBRows * kBK;
-  static constexpr uint32_t kOperands = kTileA + kTileB;               // a multiple of 1 KiB
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kTileA = 128 * kBK;                        // and as much of B
+  static constexpr uint32_t kOperands = 2 * kTileA;                    // a multiple of 1 KiB
   static constexpr uint32_t kSfbTiles = BN / 128;
   static constexpr uint32_t kScales = kSfTile * (1 + kSfbTiles);
   static constexpr uint32_t kStageTx = kOperands + kScales;            // bytes that one CTA loads a stage
@@ -71,9 +72,6 @@ struct GroupArgs {
   uint32_t nb128;           // rows: 128-row blocks of an expert's B scales
   uint32_t tiles_m;         // wgrad: output tiles along Na
   uint32_t tiles_n;         // output tiles along the columns
-  uint32_t k;               // rows: K
-  const uint8_t* w;         // rows: the weights' codes and scales
-  const uint8_t* sfw;
 };
 
 // Walks the experts in order, 32 at a time in the lanes of a converged warp.
@@ -210,29 +208,44 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // holds 256 rows of the weight as the MMA's M side, and up to 256 of the
 // expert's rows as its N side, in steps of 32. The ragged side is so the one
 // whose size an MMA may choose: a tile of 20 rows costs an eighth of one of
-// 256, where rows on the M side would fill 128 or 256 whatever they are (the
-// first version's form: 32768 rows of 64 experts, 512 on average, padded by a
-// quarter).
+// 256, where rows on the M side fill 128 or 256 whatever they are. Measured
+// against that form (256 x 256 over pairs, 128 x 256 in single CTAs for few
+// rows), with 64 weights of 4096 x 7168 and rows spread over them like e^(0.7
+// normal): 16384 rows 475 us against 658, 8192 rows 352 against 411, 8 rows
+// 46 against 56.
 //
 // Per K block of 128 each CTA loads its 128 rows of the weight (16 KiB), its
-// half of the tile's rows (up to 16 KiB: one box of 128 rows for whole tiles,
-// else boxes of 16), and the scale tiles of both; six stages. The accumulator
-// has a weight row per lane and a row of the experts' per column.
+// half of the tile's rows (up to 16 KiB, in at most three boxes of 128, 64, 32
+// and 16 rows), and the scale tiles of both; six stages. The accumulator has a
+// weight row per lane and a row of the experts' per column.
 //
-// Warps: 0 loads, 1 (of the even CTA) issues the MMAs, 2-9 are the epilogue:
-// two a quarter of the lanes, each with half of the columns. Each takes its
-// columns into registers in one go (at most 128 fp32), hands the accumulator
-// back, and does everything else while the next tile's MMAs run: tensor memory
-// has no room for a second accumulator beside the scales. A column of 32 lanes
-// is 32 neighbouring outputs of a row, stored as 64 (bf16, lanes exchanging
-// halves of column pairs) or 128 bytes.
+// Warps: 0, 10 and 11 load, 1 (of the even CTA) issues the MMAs, 2-9 are the
+// epilogue. The issue of TMA loads is what bound the first version: a lone lane
+// took 165 cycles a load, five or more a K block of 512 MMA cycles (32768
+// rows, 1156 us). Converged warps whose elected lane issues take about 105, and
+// three of them side by side (weight and its scales, rows, their scales) leave
+// the MMA issue as the longest (835 us). Prefetches into L2, by TMA or by
+// loads of another warp, made it slower: they take from the same queues.
+//
+// The epilogue has two warps a quarter of the lanes, each with half of the
+// columns. Each takes its columns into registers in one go (at most 128 fp32),
+// hands the accumulator back, and does everything else while the next tile's
+// MMAs run: tensor memory has no room for a second accumulator beside the
+// scales. A column of 32 lanes is 32 neighbouring outputs of a row, stored as
+// 64 (bf16, lanes exchanging halves of column pairs) or 128 bytes.
 //
 // SWIGLU: the even CTA holds 128 rows of the gate, the odd one the same rows of
 // the up half, so a pair of factors meets across the CTAs: of every 16 columns
 // the even CTA finishes the first eight and the odd one the last, and each
 // warp sends the other eight to its like in the peer's shared memory (st.async,
 // two slots of 1 KiB a warp, counted on a barrier of the receiver). The halves
-// are never written to memory.
+// are never written to memory. 4 % more time than the product alone.
+//
+// What bounds it: with few rows a weight, HBM (512 rows 297 us for weights of
+// 1.9 GB; 6.4 TB/s). With many, the power limit: 32768 rows of one expert take
+// 671 us, as the single product does (2.87 PFLOP/s); of 64 experts, with the
+// weights from HBM, 750 to 835 us, and 985 us once the clock has settled at
+// 1.2 GHz under load.
 
 constexpr uint32_t kRowTile = 256;                          // most rows of a tile
 constexpr int kRowStages = 6;
@@ -494,7 +507,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
         left -= int32_t(8 * rank);
         auto send = [&](const uint32_t* x) {
           const uint32_t slot = sends & 1u;
-          if (sends >= 2 && !__all_sync(kFull, mbar_wait(free0 + 16u * w + 8u * slot, ((sends >> 1) - 1) & 1u, kWaitNs)))
+          if (sends >= 2 && !__all_sync(kFull, mbar_wait<true>(free0 + 16u * w + 8u * slot, ((sends >> 1) - 1) & 1u, kWaitNs)))
             return false;
           if (lane == 0) mbar_expect_tx(sent0 + 16u * w + 8u * slot, kSendBytes);   // what the peer sends to this slot
           const uint32_t dst = peer_slots + slot * kSendBytes + lane * 16, bar = peer_sent + 8u * slot;
@@ -512,7 +525,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
             if (!ok) break;
           }
           const uint32_t slot = takes & 1u;
-          ok = __all_sync(kFull, mbar_wait(sent0 + 16u * w + 8u * slot, (takes >> 1) & 1u, kWaitNs));
+          ok = __all_sync(kFull, mbar_wait<true>(sent0 + 16u * w + 8u * slot, (takes >> 1) & 1u, kWaitNs));
           if (!ok) break;
           const uint32_t src = slots + (2 * w + slot) * kSendBytes + lane * 16;
           const uint4 q0 = lds128_u32(src), q1 = lds128_u32(src + 512);
@@ -556,12 +569,13 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
 // above; the accumulator has a row of D per lane, a warp's columns go through
 // staging rows of its own.
 
-template <bool PAIR, int BN, typename OutT>
+template <bool PAIR, typename OutT>
 __global__ void __launch_bounds__(kGroupThreads, 1)
 mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
                    const __grid_constant__ CUtensorMap tma_sfa,
                    const __grid_constant__ CUtensorMap tma_sfb, const __grid_constant__ GroupArgs a) {
-  using C = TileCfg<PAIR, BN>;
+  using C = TileCfg<PAIR>;
+  constexpr int BN = C::BN;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -823,7 +837,7 @@ struct GroupMaps {
 };
 
 template <auto Kernel>
-uint32_t max_group_clusters(int threads, size_t smem) {
+uint32_t max_group_clusters(size_t smem) {
   static std::atomic<int> cached[256];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 256) dev = 0;
@@ -831,7 +845,7 @@ uint32_t max_group_clusters(int threads, size_t smem) {
   if (n > 0) return uint32_t(n);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 256);
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(kGroupThreads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -849,17 +863,17 @@ uint32_t max_group_clusters(int threads, size_t smem) {
 }
 
 // Launches a persistent kernel of pairs (or of single CTAs) for at most `most` output tiles.
-template <auto Kernel, bool PAIR, int THREADS, typename... Args>
+template <auto Kernel, bool PAIR, typename... Args>
 mxq_status launch_group(uint32_t smem, uint64_t most, cudaStream_t s, const Args&... args) {
   const cudaError_t attr_err = ensure_smem_limit<Kernel>(int(smem));
   if (attr_err != cudaSuccess) {
     record_cuda_error(attr_err);
     return MXQ_ERR_CUDA;
   }
-  const uint64_t resident = PAIR ? max_group_clusters<Kernel>(THREADS, smem) : uint64_t(sm_count());
+  const uint64_t resident = PAIR ? max_group_clusters<Kernel>(smem) : uint64_t(sm_count());
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(uint32_t(std::min(most, resident)) * (PAIR ? 2 : 1));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(kGroupThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -874,13 +888,12 @@ mxq_status launch_group(uint32_t smem, uint64_t most, cudaStream_t s, const Args
 
 template <bool SWIGLU, typename OutT>
 mxq_status launch_rows(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
-  return launch_group<mxfp8_rows_kernel<SWIGLU, OutT>, true, kGroupThreads>(kRowSmem, most, s, m.b, m.rows, m.sfb, m.sfa, args);
+  return launch_group<mxfp8_rows_kernel<SWIGLU, OutT>, true>(kRowSmem, most, s, m.b, m.rows, m.sfb, m.sfa, args);
 }
 
-template <bool PAIR, int BN, typename OutT>
+template <bool PAIR, typename OutT>
 mxq_status launch_wgrad(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
-  return launch_group<mxfp8_wgrad_kernel<PAIR, BN, OutT>, PAIR, kGroupThreads>(TileCfg<PAIR, BN>::kSmem, most, s, m.a, m.b, m.sfa,
-                                                                m.sfb, args);
+  return launch_group<mxfp8_wgrad_kernel<PAIR, OutT>, PAIR>(TileCfg<PAIR>::kSmem, most, s, m.a, m.b, m.sfa, m.sfb, args);
 }
 
 }  // namespace
@@ -905,7 +918,7 @@ mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t 
     return MXQ_ERR_SHAPE;
   // coordinates of the loads and the list of tiles are counted in 32 bits
   constexpr int64_t kMost = 0x7fffff00ll;
-  if (M > kMost || N > kMost || K > kMost || N * E > kMost) return MXQ_ERR_SHAPE;
+  if (M > kMost || N > kMost || K > kMostSum || N * E > kMost) return MXQ_ERR_SHAPE;
   const int64_t kp4 = (K + 127) / 128, nb128 = (N + 127) / 128;
   if ((M / 128 + E + 1) * kp4 > kMost / 4 || nb128 * E * kp4 > kMost / 4) return MXQ_ERR_SHAPE;
   if ((M / 128 + E) * ((N + 127) / 128) > kMost) return MXQ_ERR_SHAPE;
@@ -924,9 +937,6 @@ mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t 
   args.b_rows = uint32_t(N);
   args.nk = args.kp4 = uint32_t(kp4);
   args.nb128 = uint32_t(nb128);
-  args.k = uint32_t(K);
-  args.w = qb;
-  args.sfw = sb_swz;
   // experts that can have rows, and the tiles that they can have
   const uint64_t active = uint64_t(std::min<int64_t>(E, M));
   if (K > 0) {
@@ -958,7 +968,7 @@ mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, 
   if (E < 1 || E > MXQ_GROUPED_MAX_EXPERTS) return MXQ_ERR_SHAPE;
   if (P < 0 || Na < 0 || Nb < 0 || P % 128 != 0 || Nb % 16 != 0) return MXQ_ERR_SHAPE;
   constexpr int64_t kMost = 0x7fffff00ll;
-  if (P > kMost || Na > kMost || Nb > kMost) return MXQ_ERR_SHAPE;
+  if (P > kMostSum || Na > kMost || Nb > kMost) return MXQ_ERR_SHAPE;
   const int64_t kp4 = P / 128;
   if ((Na + 127) / 128 * kp4 > kMost / 4 || (Nb + 127) / 128 * kp4 > kMost / 4) return MXQ_ERR_SHAPE;
   const bool pair = Na > 128 && Nb > 128;
@@ -993,8 +1003,8 @@ mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, 
   const uint64_t most = uint64_t(tiles_m) * uint64_t(tiles_n) * uint64_t(E);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (out_dt == MXQ_BF16)
-    return pair ? launch_wgrad<true, 256, uint16_t>(maps, args, most, s) : launch_wgrad<false, 128, uint16_t>(maps, args, most, s);
-  return pair ? launch_wgrad<true, 256, float>(maps, args, most, s) : launch_wgrad<false, 128, float>(maps, args, most, s);
+    return pair ? launch_wgrad<true, uint16_t>(maps, args, most, s) : launch_wgrad<false, uint16_t>(maps, args, most, s);
+  return pair ? launch_wgrad<true, float>(maps, args, most, s) : launch_wgrad<false, float>(maps, args, most, s);
 }
 
 }  // extern "C"

@@ -37,17 +37,26 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 // soon as the phase completes, so waiting warps do not spin: a poll that
 // returned at once cost the GEMM about 10 % of its time (waiting warps share
 // the issue slots of the MMA and producer warps, and burn power under the cap).
+// CLUSTER: the phase is completed by, and orders accesses of, another CTA of the cluster.
 constexpr uint32_t kPollSuspendNs = 20000;
 
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
   uint64_t deadline = 0;
   for (uint32_t it = 0; it < (1u << 30); ++it) {
     uint32_t done;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "n"(kPollSuspendNs)
-        : "memory");
+    if constexpr (CLUSTER)
+      asm volatile(
+          "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+          : "=r"(done)
+          : "r"(bar), "r"(parity), "n"(kPollSuspendNs)
+          : "memory");
+    else
+      asm volatile(
+          "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+          : "=r"(done)
+          : "r"(bar), "r"(parity), "n"(kPollSuspendNs)
+          : "memory");
     if (done) return true;
     if ((it & 15u) == 15u) {
       const uint64_t now = globaltimer();

@@ -24,8 +24,9 @@ def test_gemm_grouped():
     assert f(*edit(base, out=2)) == DTYPE
     assert f(*edit(base, sw=2)) == ARG
     for bad in (dict(E=0), dict(E=1025), dict(M=-1), dict(N=-16), dict(K=-32), dict(K=48), dict(N=24), dict(sw=1, N=128), dict(sab=-1),
-                dict(sab=0), dict(sab=600), dict(M=600), dict(M=1 << 31), dict(N=1 << 31), dict(K=1 << 31), dict(N=1 << 30),
-                dict(N=(1 << 29), K=1 << 20)):
+                dict(sab=0), dict(sab=600), dict(M=600), dict(M=1 << 31), dict(N=1 << 31), dict(K=(1 << 26) + 32), dict(N=1 << 30),
+                dict(N=(1 << 29), K=1 << 20),
+                dict(K=1 << 31)):
         assert f(*edit(base, **bad)) == SHAPE, bad
     for p in ("qa", "sa", "qb", "sb", "d", "off"):
         assert f(*edit(base, **{p: None})) == NULL
@@ -40,7 +41,7 @@ def test_wgrad():
     base = dict(qa=A, sa=A, qb=A, sb=A, E=3, off=A, P=384, Na=16, Nb=32, d=A, out=1, err=None, stream=None)
     assert f(*edit(base)) == CUDA
     assert f(*edit(base, out=-1)) == DTYPE
-    for bad in (dict(E=0), dict(E=1025), dict(P=64), dict(P=-128), dict(Na=-1), dict(Nb=8), dict(Nb=-16), dict(P=1 << 31), dict(Na=1 << 31),
+    for bad in (dict(E=0), dict(E=1025), dict(P=64), dict(P=-128), dict(Na=-1), dict(Nb=8), dict(Nb=-16), dict(P=(1 << 26) + 128), dict(Na=1 << 31),
                 dict(Nb=1 << 31), dict(Na=1 << 30, Nb=1 << 30), dict(Na=1 << 30, P=1 << 20)):
         assert f(*edit(base, **bad)) == SHAPE, bad
     for p in ("qa", "sa", "qb", "sb", "d", "off"):
