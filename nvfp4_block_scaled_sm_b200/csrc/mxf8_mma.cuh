@@ -242,6 +242,39 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
+// A K block of the pair for a converged warp, issued by one lane: the scale
+// copies (A's at sfa, B's one or two tiles at sfb, sfb + 4), four MMAs of K =
+// 32 and the commit on `bar`. One elect.sync for all.
+__device__ __forceinline__ void mma_block_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                               uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t sc_lo,
+                                               uint32_t sc_hi, uint32_t two, uint32_t accumulate, uint32_t bar) {
+  asm volatile(
+      "{ .reg .pred e, t, p; .reg .b64 da, db, sc; .reg .b32 al, bl, sl, id, ta, tb;\n\t"
+      "elect.sync _|e, 0xffffffff; setp.ne.and.b32 t, %9, 0, e; setp.ne.b32 p, %10, 0;\n\t"
+      "add.u32 sl, %7, 32; mov.b64 sc, {sl, %8};\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], sc;\n\t"
+      "add.u32 sl, %7, 64; add.u32 tb, %6, 4; mov.b64 sc, {sl, %8};\n\t"
+      "@t tcgen05.cp.cta_group::2.32x128b.warpx4 [tb], sc;\n\t"
+      "mov.b64 sc, {%7, %8};\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], sc;\n\t"
+      "mov.b64 da, {%1, %3}; mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], da, db, %4, [%5], [%6], p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.u32 al, %1, 2; add.u32 bl, %2, 2; mov.b64 da, {al, %3}; mov.b64 db, {bl, %3};\n\t"
+      "or.b32 id, %4, 0x20000010; or.b32 ta, %5, 0x40000000; or.b32 tb, %6, 0x40000000;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], da, db, id, [ta], [tb], p;\n\t"
+      "add.u32 al, %1, 4; add.u32 bl, %2, 4; mov.b64 da, {al, %3}; mov.b64 db, {bl, %3};\n\t"
+      "or.b32 id, %4, 0x40000020; or.b32 ta, %5, 0x80000000; or.b32 tb, %6, 0x80000000;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], da, db, id, [ta], [tb], p;\n\t"
+      "add.u32 al, %1, 6; add.u32 bl, %2, 6; mov.b64 da, {al, %3}; mov.b64 db, {bl, %3};\n\t"
+      "or.b32 id, %4, 0x60000030; or.b32 ta, %5, 0xc0000000; or.b32 tb, %6, 0xc0000000;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], da, db, id, [ta], [tb], p;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12; }"
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(sc_lo), "r"(sc_hi),
+        "r"(two), "r"(accumulate), "r"(bar), "h"(uint16_t(3))
+      : "memory");
+}
+
 // Instruction descriptor as instr_desc<256> but for the pair's M = 256.
 __device__ __forceinline__ uint32_t instr_desc_pair(uint32_t k) {
   return (k << 4) | (uint32_t(256 >> 3) << 17) | (1u << 23) | (uint32_t(256 >> 4) << 24) | (k << 29);

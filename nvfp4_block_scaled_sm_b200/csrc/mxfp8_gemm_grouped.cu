@@ -416,7 +416,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       const uint32_t op_lo = uint32_t(op0), op_hi = uint32_t(op0 >> 32);
       const uint32_t sc_lo = uint32_t(sc0), sc_hi = uint32_t(sc0 >> 32);
       constexpr uint32_t kStageW = kRowStage >> 4, kTileW = kWeightTile >> 4;
-      constexpr uint32_t kScaleW = kRowScales >> 4, kSfW = kSfTile >> 4;
+      constexpr uint32_t kScaleW = kRowScales >> 4;
       uint32_t s = 0, phase = 0, done = 0;
       for (; find_rows(a, cursor, tile, lane, p); tile += step, done++) {
         const uint32_t n = columns(), idesc = instr_desc_n(n);
@@ -436,14 +436,8 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
           tc_fence_after();
           const uint32_t so = s * kStageW, sc = sc_lo + s * kScaleW;
           const uint32_t sfw_t = tmem + 256 + kRowSfCols * s, sfx_t = sfw_t + 4u;
-          tmem_copy_scales_pair(sfx_t, sc + kSfW, sc_hi);
-          if (n > 128) tmem_copy_scales_pair(sfx_t + 4u, sc + 2 * kSfW, sc_hi);
-          tmem_copy_scales_pair(sfw_t, sc, sc_hi);
-#pragma unroll
-          for (uint32_t k = 0; k < 4; k++)
-            mma_mxf8_pair(tmem, op_lo + so + 2 * k, op_lo + so + kTileW + 2 * k, op_hi, idesc | (k << 4) | (k << 29),
-                          sfw_t | (k << 30), sfx_t | (k << 30), (kb | k) != 0u);
-          mma_commit_pair(empty_bar(s));
+          mma_block_pair(tmem, op_lo + so, op_lo + so + kTileW, op_hi, idesc, sfw_t, sfx_t, sc, sc_hi, n > 128, kb,
+                         empty_bar(s));
           if (++s == kRowStages) {
             s = 0;
             phase ^= 1u;
@@ -694,27 +688,18 @@ mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
           tc_fence_after();
           const uint32_t so = s * kStageW, sc = sc_lo + s * kScaleW;
           const uint32_t sfa_t = tmem + BN + C::kSfCols * s, sfb_t = sfa_t + 4u;
+          if constexpr (PAIR) {
+            mma_block_pair(tmem, op_lo + so, op_lo + so + kTileAW, op_hi, instr_desc_n(BN), sfa_t, sfb_t, sc, sc_hi, 1u, i,
+                           empty_bar(s));
+          } else {
+            tmem_copy_scales(sfb_t, sc + kSfW, sc_hi);
+            tmem_copy_scales(sfa_t, sc, sc_hi);
 #pragma unroll
-          for (uint32_t j = 0; j <= C::kSfbTiles; j++) {   // B's tiles first, then A's
-            const uint32_t w = j == C::kSfbTiles ? 0 : j + 1;
-            if constexpr (PAIR)
-              tmem_copy_scales_pair(sfa_t + 4u * w, sc + kSfW * w, sc_hi);
-            else
-              tmem_copy_scales(sfa_t + 4u * w, sc + kSfW * w, sc_hi);
-          }
-#pragma unroll
-          for (uint32_t k = 0; k < 4; k++) {
-            if constexpr (PAIR)
-              mma_mxf8_pair(tmem, op_lo + so + 2 * k, op_lo + so + kTileAW + 2 * k, op_hi, instr_desc_pair(k),
-                            sfa_t | (k << 30), sfb_t | (k << 30), (i | k) != 0u);
-            else
+            for (uint32_t k = 0; k < 4; k++)
               mma_mxf8(tmem, op_lo + so + 2 * k, op_lo + so + kTileAW + 2 * k, op_hi, instr_desc<BN>(k),
                        sfa_t | (k << 30), sfb_t | (k << 30), (i | k) != 0u);
-          }
-          if constexpr (PAIR)
-            mma_commit_pair(empty_bar(s));
-          else
             mma_commit(empty_bar(s));
+          }
           if (++s == kStages) {
             s = 0;
             phase ^= 1u;
