@@ -629,8 +629,17 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_join_kernel(const float* __r
   __shared__ float red[8][33];
   const uint32_t lane = threadIdx.x & 31, share = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < N)
-    for (uint32_t p = share; p < parts; p += 8) s += part[uint64_t(p) * N + c];
+  if (c < N) {
+    uint32_t p = share;
+    for (; p + 56 < parts; p += 64) {                  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (uint32_t i = 0; i < 8; i++) v[i] = part[uint64_t(p + 8 * i) * N + c];
+#pragma unroll
+      for (uint32_t i = 0; i < 8; i++) s += v[i];
+    }
+    for (; p < parts; p += 8) s += part[uint64_t(p) * N + c];
+  }
   red[share][lane] = s;
   __syncthreads();
   if (share != 0 || c >= N) return;
