@@ -348,6 +348,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
   cluster_sync();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_enter();  // (all of the above overlaps the end of the grid before)
 
   ExpertCursor cursor;
   cursor.start(a.offsets, a.E, a.rows, kRowTile, lane);
@@ -614,6 +615,7 @@ mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
   if constexpr (PAIR) cluster_sync();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_enter();  // (all of the above overlaps the end of the grid before)
 
   ExpertCursor cursor;
   // (rows are clamped by K blocks, in find_wgrad)
@@ -861,13 +863,15 @@ mxq_status launch_group(uint32_t smem, uint64_t most, cudaStream_t s, const Args
   cfg.blockDim = dim3(kGroupThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = PAIR ? 2 : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return launched(cudaLaunchKernelEx(&cfg, Kernel, args...));
 }
 
