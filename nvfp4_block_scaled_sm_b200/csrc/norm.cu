@@ -42,6 +42,7 @@ struct NormArgs {
   uint32_t N;
   uint32_t S4;            // ceil(N / 128)
   uint32_t row_threads;   // threads of a row, a multiple of 32
+  uint32_t row_ctas;      // CTAs with rows
   double eps;
   int weight_bf16;
   bool v8;                // x, residual, hidden and normed: rows on 32-byte boundaries
@@ -196,20 +197,18 @@ __device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, co
   }
 }
 
-// The scale tiles' rows past M are zeros.
-__device__ __forceinline__ void pad_tiles(const NormArgs& a) {
-  if (!a.swz) return;
-  const uint64_t pad = (uint64_t(a.M + 127) & ~127ull) - uint64_t(a.M);
-  const uint64_t words = pad * a.S4;
-  for (uint64_t i = uint64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < words; i += uint64_t(gridDim.x) * blockDim.x) {
-    const uint64_t r = uint64_t(a.M) + i / a.S4;
-    st_u32(a.swz + (((r >> 7) * a.S4 + i % a.S4) << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2), 0);
-  }
+// The scale tiles' rows past M are zeros: a warp a row, of CTAs behind those of the rows.
+__device__ __forceinline__ void pad_tiles(const NormArgs& a, uint32_t cta) {
+  const int64_t r = a.M + int64_t(cta) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (r >= ((a.M + 127) & ~int64_t(127))) return;
+  uint8_t* p = a.swz + ((uint64_t(r) >> 7) * a.S4 << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2);
+  for (uint32_t j = threadIdx.x & 31; j < a.S4; j += 32) st_u32(p + (uint64_t(j) << 9), 0);
 }
 
 template <typename T, bool RES, int C, bool LOOP>
 __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   pdl_enter();
+  if (blockIdx.x >= a.row_ctas) return pad_tiles(a, blockIdx.x - a.row_ctas);
   __shared__ double sums[32];
   __shared__ float rstds[32];
   const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -296,14 +295,16 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
       finish16(a, v[i], w, row, c, rstd, active);
     }
   }
-  pad_tiles(a);
 }
 
 template <typename T, bool RES, int C, bool LOOP>
-mxq_status launch_norm(const NormArgs& a, uint32_t rows, cudaStream_t s) {
-  const uint64_t grid = (uint64_t(a.M) + rows - 1) / rows;
+mxq_status launch_norm(NormArgs& a, uint32_t rows, cudaStream_t s) {
+  const uint32_t threads = a.row_threads * rows;
+  a.row_ctas = uint32_t((uint64_t(a.M) + rows - 1) / rows);
+  const uint32_t pad = a.swz ? uint32_t(-a.M & 127) : 0;
+  const uint64_t grid = uint64_t(a.row_ctas) + (pad + threads / 32 - 1) / (threads / 32);
   if (grid > 0x7fffffffull) return MXQ_ERR_SHAPE;
-  return launched(launch_pdl_ex(mxfp8_rmsnorm_kernel<T, RES, C, LOOP>, uint32_t(grid), a.row_threads * rows, 0, s, a));
+  return launched(launch_pdl_ex(mxfp8_rmsnorm_kernel<T, RES, C, LOOP>, uint32_t(grid), threads, 0, s, a));
 }
 
 template <typename T, bool RES>
