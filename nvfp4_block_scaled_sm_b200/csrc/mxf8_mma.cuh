@@ -171,8 +171,8 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
-// As above, after this thread's reads of shared memory that the other CTA
-// writes next.
+// As above, where the other CTA relies on what this one has written: ordered
+// over the cluster, which takes a microsecond.
 __device__ __forceinline__ void mbar_release_remote(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
@@ -243,17 +243,17 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
 }
 
 // A K block of the pair for a converged warp, issued by one lane: the scale
-// copies (A's at sfa, B's one or two tiles at sfb, sfb + 4), four MMAs of K =
-// 32 and the commit on `bar`. One elect.sync for all.
+// copies (A's tile to sfa, B's one or two, side by side, to sfb, sfb + 4), four
+// MMAs of K = 32 and the commit on `bar`. One elect.sync for all.
 __device__ __forceinline__ void mma_block_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
-                                               uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t sc_lo,
-                                               uint32_t sc_hi, uint32_t two, uint32_t accumulate, uint32_t bar) {
+                                               uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t sca_lo,
+                                               uint32_t scb_lo, uint32_t sc_hi, uint32_t two, uint32_t accumulate, uint32_t bar) {
   asm volatile(
       "{ .reg .pred e, t, p; .reg .b64 da, db, sc; .reg .b32 al, bl, sl, id, ta, tb;\n\t"
       "elect.sync _|e, 0xffffffff; setp.ne.and.b32 t, %9, 0, e; setp.ne.b32 p, %10, 0;\n\t"
-      "add.u32 sl, %7, 32; mov.b64 sc, {sl, %8};\n\t"
+      "mov.b64 sc, {%13, %8};\n\t"
       "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%6], sc;\n\t"
-      "add.u32 sl, %7, 64; add.u32 tb, %6, 4; mov.b64 sc, {sl, %8};\n\t"
+      "add.u32 sl, %13, 32; add.u32 tb, %6, 4; mov.b64 sc, {sl, %8};\n\t"
       "@t tcgen05.cp.cta_group::2.32x128b.warpx4 [tb], sc;\n\t"
       "mov.b64 sc, {%7, %8};\n\t"
       "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%5], sc;\n\t"
@@ -270,8 +270,8 @@ __device__ __forceinline__ void mma_block_pair(uint32_t d_tmem, uint32_t a_lo, u
       "or.b32 id, %4, 0x60000030; or.b32 ta, %5, 0xc0000000; or.b32 tb, %6, 0xc0000000;\n\t"
       "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], da, db, id, [ta], [tb], p;\n\t"
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%11], %12; }"
-      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(sc_lo), "r"(sc_hi),
-        "r"(two), "r"(accumulate), "r"(bar), "h"(uint16_t(3))
+      ::"r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(sca_lo), "r"(sc_hi),
+        "r"(two), "r"(accumulate), "r"(bar), "h"(uint16_t(3)), "r"(scb_lo)
       : "memory");
 }
 

@@ -37,6 +37,7 @@ constexpr int kGroupThreads = 32 * (4 + kEpiWarps);   // warps: 0, 10, 11 load, 
 constexpr uint32_t kSlicePitch = 144;
 constexpr uint32_t kSliceBytes = 16 * kSlicePitch;
 constexpr uint32_t kBarrierBytes = 256;
+constexpr uint32_t kScTileW = kSfTile >> 4;      // descriptors count 16 bytes
 constexpr int64_t kMostSum = int64_t(1) << 26;  // terms of a sum: a tile takes less than the waits' limit
 
 // Tiles of the weights' gradients.
@@ -72,6 +73,7 @@ struct GroupArgs {
   uint32_t nb128;           // rows: 128-row blocks of an expert's B scales
   uint32_t tiles_m;         // wgrad: output tiles along Na
   uint32_t tiles_n;         // output tiles along the columns
+  const uint8_t* sfw;       // rows, SWIGLU: the weights' scales
 };
 
 // Walks the experts in order, 32 at a time in the lanes of a converged warp.
@@ -234,12 +236,18 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // scales. A column of 32 lanes is 32 neighbouring outputs of a row, stored as
 // 64 (bf16, lanes exchanging halves of column pairs) or 128 bytes.
 //
-// SWIGLU: the even CTA holds 128 rows of the gate, the odd one the same rows of
-// the up half, so a pair of factors meets across the CTAs: of every 16 columns
-// the even CTA finishes the first eight and the odd one the last, and each
-// warp sends the other eight to its like in the peer's shared memory (st.async,
-// two slots of 1 KiB a warp, counted on a barrier of the receiver). The halves
-// are never written to memory. 4 % more time than the product alone.
+// SWIGLU: each CTA holds 64 rows of the gate and the same 64 of the up half, so
+// that the factors of an output are in one CTA, 64 accumulator lanes apart, and
+// two warps exchange them through shared memory; the halves of the product are
+// never written to memory. (With the gate in one CTA and the up half in the
+// other, sends to the peer's shared memory took 25000 cycles a tile and bound
+// the kernel below K = 4096.) The scale tile of those 128 rows is no tile of
+// memory: its quarters 0 and 1 come from a half of the gate's tile, 2 and 3
+// from a half of the up half's, and a TMA copy cannot put eight of 16 bytes
+// beside eight others; warp 11 joins them. 32768 rows of 64 experts, N = 4096,
+// K = 2048, under load: 346 us (505 with the sends; without SWIGLU 340); from K =
+// 4096 on the product's own time. At K = 512 silu itself is what bounds it, 8 us
+// a tile: 250 to 300 us (without SWIGLU 110).
 //
 // What bounds it: with few rows a weight, HBM (512 rows 297 us for weights of
 // 1.9 GB; 6.4 TB/s). With many, the power limit: 32768 rows of one expert take
@@ -251,14 +259,17 @@ constexpr uint32_t kRowTile = 256;                          // most rows of a ti
 constexpr int kRowStages = 6;
 constexpr uint32_t kWeightTile = 128 * kBK;                 // a CTA's rows of the weight
 constexpr uint32_t kRowStage = 2 * kWeightTile;             // and the room for its half of the rows
-constexpr uint32_t kRowScales = 3 * kSfTile;                // weight, two tiles of rows
+constexpr uint32_t kRowScales = 3 * kSfTile;                // weight (SWIGLU: unused), two tiles of rows
 constexpr uint32_t kRowSfCols = 12;
 constexpr uint32_t kSendBytes = 32 * 8 * 4;                 // eight columns of a warp
-constexpr uint32_t kRowBars = 512;
-constexpr uint32_t kRowSmem = kRowStages * (kRowStage + kRowScales) + kRowBars + 2 * kEpiWarps * kSendBytes + 1024;
+constexpr uint32_t kJoin = 8;                               // K blocks of a group of joined scale tiles
+constexpr uint32_t kJoinRing = 2;                           // groups
+constexpr uint32_t kRowBars = 256;
+constexpr uint32_t kRowSmem = kRowStages * (kRowStage + kRowScales) + kRowBars + 2 * kEpiWarps * kSendBytes +
+                              kJoinRing * kJoin * kSfTile + 1024;
 static_assert(256 + kRowStages * kRowSfCols <= 512, "tensor memory");
 static_assert(kRowSmem <= 232448, "shared memory");
-static_assert(8 * (2 * kRowStages + 2 + 4 * kEpiWarps) + 8 <= kRowBars, "barriers");
+static_assert(8 * (2 * kRowStages + 2 + 3 * kJoinRing) + 4 <= kRowBars, "barriers");
 
 // The rows in boxes of 128, 64, 32 and 16.
 struct RowMaps {
@@ -270,12 +281,21 @@ __device__ __forceinline__ uint32_t instr_desc_n(uint32_t n) {
   return ((n >> 3) << 17) | (1u << 23) | (uint32_t(256 >> 4) << 24);
 }
 
-// Four words into a CTA's shared memory of the cluster, counted on its barrier.
-__device__ __forceinline__ void send16(uint32_t dst, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+// Two warps (64 threads) at barrier `id`; true where `ok` was true in all of them.
+__device__ __forceinline__ bool meet(uint32_t id, bool ok) {
+  uint32_t r;
   asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];"
-      ::"r"(dst), "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
+      "{ .reg .pred p, q; setp.ne.u32 p, %2, 0; barrier.cta.red.and.pred q, %1, 64, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(id), "r"(uint32_t(ok))
       : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ uint2 ldg64(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
 }
 
 // COLS columns v of this lane's weight row, the tile's rows t .. (COLS even): p is
@@ -310,15 +330,17 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
   const uint32_t base = (raw + 1023u) & ~1023u;           // operand tiles: 128-byte swizzle atoms of 1 KiB
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t scales = base + kRowStages * kRowStage;
-  const uint32_t slots = scales + kRowStages * kRowScales;          // what the peer sends
+  const uint32_t joined = scales + kRowStages * kRowScales;         // SWIGLU: [group][K block], scale tiles
+  const uint32_t slots = joined + kJoinRing * kJoin * kSfTile;      // SWIGLU: [warp][2], columns for the other warp
   const uint32_t bars = slots + 2 * kEpiWarps * kSendBytes;
   auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bars + 8u * (kRowStages + s); };
   const uint32_t acc_full = bars + 8u * (2 * kRowStages);
   const uint32_t acc_empty = acc_full + 8u;
-  const uint32_t sent0 = acc_empty + 8u;                            // [warp][slot]: the peer's columns are here
-  const uint32_t free0 = sent0 + 8u * 2 * kEpiWarps;                // [warp][slot]: the peer has read mine
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (free0 - base) + 8 * 2 * kEpiWarps);
+  auto join_full = [&](uint32_t g) { return acc_empty + 8u * (1 + g); };
+  auto join_empty = [&](uint32_t g) { return acc_empty + 8u * (1 + kJoinRing + g); };
+  auto join_odd = [&](uint32_t g) { return acc_empty + 8u * (1 + 2 * kJoinRing + g); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + (join_odd(kJoinRing) - base));
 
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();                // 0: issues the MMAs
@@ -335,12 +357,13 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
+    for (uint32_t g = 0; g < kJoinRing; g++) {
+      mbar_init(join_full(g), 2);  // this CTA's warp 11 and the odd CTA's warp 1
+      mbar_init(join_empty(g), 1);
+      mbar_init(join_odd(g), 1);
+    }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 2 * kEpiWarps);
-    for (int i = 0; i < 2 * kEpiWarps; i++) {
-      mbar_init(sent0 + 8u * i, 1);
-      mbar_init(free0 + 8u * i, 1);
-    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   tc_fence_before();
@@ -356,19 +379,18 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
   // columns of a tile's accumulator: its rows, a multiple of 32
   auto columns = [&]() { return min(kRowTile, (p.left + 31u) & ~31u); };
 
-  // rows of the weight and their scale block of this CTA in a tile
+  // first row of the weight of this CTA in a tile (SWIGLU: of the gate's), and its scale block
   auto w_row_of = [&](const Place& q) {
-    return q.expert * a.b_rows + (SWIGLU ? q.n_blk * 128 + rank * a.n : q.n_blk * 256 + rank * 128);
+    return q.expert * a.b_rows + (SWIGLU ? q.n_blk * 128 + rank * 64 : q.n_blk * 256 + rank * 128);
   };
-  auto w_blk_of = [&](const Place& q) {
-    return q.expert * a.nb128 + (SWIGLU ? q.n_blk + rank * (a.n / 128) : q.n_blk * 2 + rank);
-  };
+  auto w_blk_of = [&](const Place& q) { return q.expert * a.nb128 + (SWIGLU ? q.n_blk : q.n_blk * 2 + rank); };
 
-  if (warp == 0 || warp >= 2 + kEpiWarps) {
+  if (warp == 0 || warp == 2 + kEpiWarps || (!SWIGLU && warp == 3 + kEpiWarps)) {
     // --------------------------------------------------------- producers
     // warp 0 loads the weight and its scales, warp 10 the rows, warp 11 their
-    // scales: the issue of a TMA load holds a warp for 100 cycles and more
-    const bool weights = warp == 0, scale_warp = warp == 3 + kEpiWarps;
+    // scales: the issue of a TMA load holds a warp for 100 cycles and more.
+    // SWIGLU: warp 0 the two halves of the weight and the rows' scales.
+    const bool weights = warp == 0, rows_warp = warp == 2 + kEpiWarps;
     const uint32_t bar0 = cluster_addr(full_bar(0), 0);
     uint32_t s = 0, phase = 1;
     bool ok = true;
@@ -377,7 +399,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       const uint32_t x_row = p.row + rank * mine;
       const uint32_t w_row = w_row_of(p), w_sf = 4 * w_blk_of(p) * a.kp4;
       const uint32_t x_sf = 4 * p.block * a.kp4;
-      const uint32_t tx = 2 * (kWeightTile + mine * kBK + kSfTile * (n > 128 ? 3 : 2));
+      const uint32_t tx = 2 * (kWeightTile + mine * kBK + kSfTile * ((n > 128 ? 2 : 1) + (SWIGLU ? 0 : 1)));
       for (uint32_t kb = 0; kb < a.nk; kb++) {
         if (!__all_sync(kFull, mbar_wait(empty_bar(s), phase, kWaitNs))) {
           if (lane == 0) record_error(a.err, kErrEmptyWait);
@@ -389,8 +411,14 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
         if (weights) {
           if (rank == 0) mbar_elect_expect_tx(full_bar(s), tx);
           tma_elect_2d_pair(st, &tma_w, bar, int32_t(x), int32_t(w_row));
-          tma_elect_2d_pair(sf, &tma_sfw, bar, 0, int32_t(w_sf + 4 * kb));
-        } else if (!scale_warp) {
+          if constexpr (SWIGLU) {
+            tma_elect_2d_pair(st + kWeightTile / 2, &tma_w, bar, int32_t(x), int32_t(w_row + a.n));
+            tma_elect_2d_pair(sf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
+            if (n > 128) tma_elect_2d_pair(sf + 2 * kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
+          } else {
+            tma_elect_2d_pair(sf, &tma_sfw, bar, 0, int32_t(w_sf + 4 * kb));
+          }
+        } else if (rows_warp) {
           uint32_t r = 0;
 #pragma unroll
           for (int b = 0; b < 4; b++)
@@ -408,6 +436,69 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
         }
       }
     }
+  } else if (SWIGLU && warp == 3 + kEpiWarps) {
+    // ------------------------------------- joined scale tiles of the weight
+    // Quarters 0 and 1 of a joined tile are the gate's 64 rows, 2 and 3 the up
+    // half's: a lane's line of it is eight bytes of the gate's tile and eight of
+    // half's: a lane's line of it is eight bytes of the gate's tile and eight of
+    // the up half's. They go in groups of kJoin K blocks: a release that the
+    // other CTA may rely on takes 1000 to 3000 cycles (one per K block: 610 us
+    // for K = 2048), and is left to the odd CTA's warp 1, which has no MMAs to
+    // issue (released by this warp: 310 us for 512 rows, 288 so).
+    uint32_t g = 0, phase = 1;
+    uint2 gate[kJoin], up[kJoin];
+    const uint64_t up_sf = uint64_t(a.n / 128) * a.kp4 * kSfTile;
+    auto load = [&](uint32_t kb) {
+      const uint8_t* src = a.sfw + (uint64_t(w_blk_of(p)) * a.kp4 + kb) * kSfTile + lane * 16 + rank * 8;
+#pragma unroll
+      for (uint32_t i = 0; i < kJoin; i++)
+        if (kb + i < a.nk) {
+          gate[i] = ldg64(src + uint64_t(i) * kSfTile);
+          up[i] = ldg64(src + up_sf + uint64_t(i) * kSfTile);
+        }
+    };
+    bool have = a.nk > 0 && find_rows(a, cursor, tile, lane, p);
+    if (have) load(0);
+    for (uint32_t kb = 0; have;) {
+      if (!__all_sync(kFull, mbar_wait(join_empty(g), phase, kWaitNs))) {
+        if (lane == 0) record_error(a.err, kErrEmptyWait);
+        break;
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < kJoin; i++)
+        sts128_u32(joined + (g * kJoin + i) * kSfTile + lane * 16, make_uint4(gate[i].x, gate[i].y, up[i].x, up[i].y));
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if ((kb += kJoin) >= a.nk) {
+        kb = 0;
+        have = find_rows(a, cursor, tile += step, lane, p);
+      }
+      if (lane == 0) mbar_arrive(rank == 0 ? join_full(g) : join_odd(g));
+      if (have) load(kb);
+      if (++g == kJoinRing) {
+        g = 0;
+        phase ^= 1u;
+      }
+    }
+  } else if (SWIGLU && warp == 1 && rank == 1) {
+    // hands the odd CTA's joined scale tiles over to the MMA issuer
+    if (a.nk > 0) {
+      uint32_t g = 0, phase = 0;
+      bool ok = true;
+      for (; ok && find_rows(a, cursor, tile, lane, p); tile += step)
+        for (uint32_t kb = 0; kb < a.nk; kb += kJoin) {
+          if (!__all_sync(kFull, mbar_wait(join_odd(g), phase, kWaitNs))) {
+            if (lane == 0) record_error(a.err, kErrFullWait);
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_release_remote(cluster_addr(join_full(g), 0));
+          if (++g == kJoinRing) {
+            g = 0;
+            phase ^= 1u;
+          }
+        }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
     // a converged warp with descriptors as 32-bit words plus offsets, as in
@@ -418,7 +509,8 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       const uint32_t sc_lo = uint32_t(sc0), sc_hi = uint32_t(sc0 >> 32);
       constexpr uint32_t kStageW = kRowStage >> 4, kTileW = kWeightTile >> 4;
       constexpr uint32_t kScaleW = kRowScales >> 4;
-      uint32_t s = 0, phase = 0, done = 0;
+      const uint32_t join_lo = uint32_t(scale_desc(joined));
+      uint32_t s = 0, phase = 0, done = 0, g = 0, join_phase = 0;
       for (; find_rows(a, cursor, tile, lane, p); tile += step, done++) {
         const uint32_t n = columns(), idesc = instr_desc_n(n);
         // the epilogue must have read the previous tile's accumulator
@@ -429,7 +521,9 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
         tc_fence_after();
         bool ok = true;
         for (uint32_t kb = 0; kb < a.nk; kb++) {
-          if (!__all_sync(kFull, mbar_wait(full_bar(s), phase, kWaitNs))) {
+          const bool first = SWIGLU && kb % kJoin == 0, last = SWIGLU && (kb % kJoin == kJoin - 1 || kb + 1 == a.nk);
+          if (!__all_sync(kFull, (!first || mbar_wait<true>(join_full(g), join_phase, kWaitNs)) &&
+                                     mbar_wait(full_bar(s), phase, kWaitNs))) {
             if (lane == 0) record_error(a.err, kErrFullWait);
             ok = false;
             break;
@@ -437,8 +531,16 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
           tc_fence_after();
           const uint32_t so = s * kStageW, sc = sc_lo + s * kScaleW;
           const uint32_t sfw_t = tmem + 256 + kRowSfCols * s, sfx_t = sfw_t + 4u;
-          mma_block_pair(tmem, op_lo + so, op_lo + so + kTileW, op_hi, idesc, sfw_t, sfx_t, sc, sc_hi, n > 128, kb,
+          mma_block_pair(tmem, op_lo + so, op_lo + so + kTileW, op_hi, idesc, sfw_t, sfx_t,
+                         SWIGLU ? join_lo + (g * kJoin + kb % kJoin) * kScTileW : sc, sc + kScTileW, sc_hi, n > 128, kb,
                          empty_bar(s));
+          if (last) {
+            mma_commit_pair(join_empty(g));
+            if (++g == kJoinRing) {
+              g = 0;
+              join_phase ^= 1u;
+            }
+          }
           if (++s == kRowStages) {
             s = 0;
             phase ^= 1u;
@@ -452,20 +554,25 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
     // ------------------------------------------------------------ epilogue
     // warp w reads accumulator lanes (weight rows) 32 (w % 4) .. + 31; the
     // second four warps take the second half of the columns
-    const uint32_t quarter = warp & 3, half = (warp - 2) >> 2, w = warp - 2;
+    const uint32_t quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lead_acc_empty = cluster_addr(acc_empty, 0);
-    const uint32_t peer_slots = cluster_addr(slots + w * 2 * kSendBytes, rank ^ 1u);
-    const uint32_t peer_sent = cluster_addr(sent0 + 16u * w, rank ^ 1u);
-    const uint32_t peer_free = cluster_addr(free0 + 16u * w, rank ^ 1u);
-    uint32_t done = 0, sends = 0, takes = 0;
-    bool ok = true;
-    for (; ok && find_rows(a, cursor, tile, lane, p); tile += step, done++) {
+    // SWIGLU: quarters 0 and 1 hold the gate, 2 and 3 the up half of the same
+    // outputs; the two warps that share outputs meet at a barrier of their own
+    const bool upper = quarter >= 2;
+    const uint32_t pair_id = 1 + 2 * half + (quarter & 1);
+    const uint32_t my_slots = slots + (4 * half + quarter) * 2 * kSendBytes;
+    const uint32_t its_slots = slots + (4 * half + (quarter ^ 2)) * 2 * kSendBytes;
+    uint32_t done = 0;
+    for (; find_rows(a, cursor, tile, lane, p); tile += step, done++) {
       const uint32_t cols = columns() / 2;                // of this warp, a multiple of 16
       const uint32_t taddr = tmem + ((quarter * 32) << 16) + half * cols;
       uint32_t v[128];
+      bool ok = true;
       if (a.nk > 0) {
         // the phase completes once for everyone: a lane that saw it lets the warp go
-        if (!__any_sync(kFull, mbar_wait(acc_full, done & 1u, kWaitNs))) {
+        ok = __any_sync(kFull, mbar_wait(acc_full, done & 1u, kWaitNs));
+        if constexpr (SWIGLU) ok = meet(pair_id, ok);     // (both warps go on, or neither)
+        if (!ok) {
           if (lane == 0) record_error(a.err, kErrAccumWait);
           break;
         }
@@ -482,69 +589,44 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
 #pragma unroll
         for (int c = 0; c < 128; c++) v[c] = 0;
       }
-      const uint32_t f = (SWIGLU ? p.n_blk * 128 : p.n_blk * 256 + rank * 128) + quarter * 32 + lane;
-      const uint32_t t0 = half * cols;
+      const uint32_t f = (SWIGLU ? p.n_blk * 128 + rank * 64 + (quarter & 1) * 32 : p.n_blk * 256 + rank * 128 + quarter * 32) + lane;
+      const uint32_t t0 = half * cols + (SWIGLU && upper ? 8 : 0);
       int32_t left = f < a.n ? int32_t(min(p.left, kRowTile)) - int32_t(t0) : 0;
-      OutT* d = static_cast<OutT*>(a.d) + uint64_t(p.row + t0 + (SWIGLU ? 8 * rank : 0)) * a.n + f;
+      OutT* d = static_cast<OutT*>(a.d) + uint64_t(p.row + t0) * a.n + f;
       if constexpr (sizeof(OutT) == 2) d += int64_t(lane & 1) * (int64_t(a.n) - 1);
-      if constexpr (!SWIGLU) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (uint32_t(c) >= cols) break;
+      for (int c = 0; c < 128; c += 16) {
+        if (uint32_t(c) >= cols) break;
+        if constexpr (!SWIGLU) {
           store_columns<16>(d, a.n, &v[c], left);
-          d += 16 * uint64_t(a.n);
-          left -= 16;
-        }
-      } else {
-        // chunk i is columns 16 i .. + 15: this CTA finishes v[own + 0 .. 7] of
-        // it and sends the others; the next chunk is sent before this one's
-        // factors are waited for
-        left -= int32_t(8 * rank);
-        auto send = [&](const uint32_t* x) {
-          const uint32_t slot = sends & 1u;
-          if (sends >= 2 && !__all_sync(kFull, mbar_wait<true>(free0 + 16u * w + 8u * slot, ((sends >> 1) - 1) & 1u, kWaitNs)))
-            return false;
-          if (lane == 0) mbar_expect_tx(sent0 + 16u * w + 8u * slot, kSendBytes);   // what the peer sends to this slot
-          const uint32_t dst = peer_slots + slot * kSendBytes + lane * 16, bar = peer_sent + 8u * slot;
-          send16(dst, bar, x[0], x[1], x[2], x[3]);
-          send16(dst + 512, bar, x[4], x[5], x[6], x[7]);
-          sends++;
-          return true;
-        };
-        ok = rank ? send(&v[0]) : send(&v[8]);
+        } else {
+          // of 16 columns the gate's warp finishes the first eight and the up
+          // half's the last: each gives the other's eight away. Two slots: what
+          // is written two chunks on was read before the barrier between.
+          const uint32_t off = (c & 16 ? kSendBytes : 0) + lane * 16;
 #pragma unroll
-        for (int c = 0; c < 128; c += 16) {
-          if (uint32_t(c) >= cols || !ok) break;
-          if (c + 16 < 128 && uint32_t(c + 16) < cols) {
-            ok = rank ? send(&v[(c + 16) % 128]) : send(&v[(c + 24) % 128]);
-            if (!ok) break;
-          }
-          const uint32_t slot = takes & 1u;
-          ok = __all_sync(kFull, mbar_wait<true>(sent0 + 16u * w + 8u * slot, (takes >> 1) & 1u, kWaitNs));
-          if (!ok) break;
-          const uint32_t src = slots + (2 * w + slot) * kSendBytes + lane * 16;
-          const uint4 q0 = lds128_u32(src), q1 = lds128_u32(src + 512);
-          __syncwarp();
-          if (lane == 0) mbar_release_remote(peer_free + 8u * slot);
-          takes++;
-          const uint32_t o[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-          uint32_t y[8];
+          for (int i = 0; i < 8; i += 4)
+            sts128_u32(my_slots + off + 128 * i,
+                       upper ? make_uint4(v[c + i], v[c + i + 1], v[c + i + 2], v[c + i + 3])
+                             : make_uint4(v[c + 8 + i], v[c + 9 + i], v[c + 10 + i], v[c + 11 + i]));
+          meet(pair_id, true);
+          const uint4 q0 = lds128_u32(its_slots + off), q1 = lds128_u32(its_slots + off + 512);
+          uint32_t y[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            const float mine = __uint_as_float(rank ? v[c + 8 + i] : v[c + i]), other = __uint_as_float(o[i]);
-            y[i] = __float_as_uint(rank ? swiglu(other, mine) : swiglu(mine, other));
+            const float mine = __uint_as_float(upper ? v[c + 8 + i] : v[c + i]), other = __uint_as_float(y[i]);
+            y[i] = __float_as_uint(upper ? swiglu(other, mine) : swiglu(mine, other));
           }
           store_columns<8>(d, a.n, y, left);
-          d += 16 * uint64_t(a.n);
-          left -= 16;
         }
-        if (!ok && lane == 0) record_error(a.err, kErrAccumWait);
+        d += 16 * uint64_t(a.n);
+        left -= 16;
       }
     }
   }
 
   // neither CTA leaves while the other may still reach its shared memory or
-  // tensor memory (barrier arrivals, MMA operand reads, scale copies, sends)
+  // tensor memory (barrier arrivals, MMA operand reads, scale copies)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -691,7 +773,7 @@ mxfp8_wgrad_kernel(const __grid_constant__ CUtensorMap tma_a, const __grid_const
           const uint32_t so = s * kStageW, sc = sc_lo + s * kScaleW;
           const uint32_t sfa_t = tmem + BN + C::kSfCols * s, sfb_t = sfa_t + 4u;
           if constexpr (PAIR) {
-            mma_block_pair(tmem, op_lo + so, op_lo + so + kTileAW, op_hi, instr_desc_n(BN), sfa_t, sfb_t, sc, sc_hi, 1u, i,
+            mma_block_pair(tmem, op_lo + so, op_lo + so + kTileAW, op_hi, instr_desc_n(BN), sfa_t, sfb_t, sc, sc + kScTileW, sc_hi, 1u, i,
                            empty_bar(s));
           } else {
             tmem_copy_scales(sfb_t, sc + kSfW, sc_hi);
@@ -926,6 +1008,7 @@ mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t 
   args.b_rows = uint32_t(N);
   args.nk = args.kp4 = uint32_t(kp4);
   args.nb128 = uint32_t(nb128);
+  args.sfw = sb_swz;
   // experts that can have rows, and the tiles that they can have
   const uint64_t active = uint64_t(std::min<int64_t>(E, M));
   if (K > 0) {
@@ -935,7 +1018,7 @@ mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t 
     if (sa_bytes < (M + 127) / 128 * kp4 * int64_t(kSfTile) || sa_bytes % int64_t(kSfTile) != 0) return MXQ_ERR_SHAPE;
     for (int b = 0; b < 4; b++)
       if (!make_operand_map(&maps.rows.box[b], qa, uint64_t(M), uint64_t(K), 128u >> b)) return MXQ_ERR_CUDA;
-    if (!make_operand_map(&maps.b, qb, uint64_t(N) * E, uint64_t(K), 128) ||
+    if (!make_operand_map(&maps.b, qb, uint64_t(N) * E, uint64_t(K), swiglu ? 64 : 128) ||
         !make_scale_map(&maps.sfa, sa_swz, uint64_t(sa_bytes)) ||
         !make_scale_map(&maps.sfb, sb_swz, uint64_t(nb128) * E * kp4 * kSfTile))
       return MXQ_ERR_CUDA;

@@ -62,6 +62,22 @@ print("first calls ok")
 """
 
 
+# SwiGLU's weight scales go through groups of eight K blocks, two at a time: one block, ends of and
+# inside a group, more groups than are held; one tile and several for a pair of CTAs
+@pytest.mark.parametrize("K", [32, 1024, 1056, 2048, 2176, 4000])
+@pytest.mark.parametrize("E,M,H", [(3, 700, 256), (2, 9000, 640), (9, 9, 128)])
+def test_swiglu_over_k(E, M, H, K):
+    cut = torch.linspace(0, M, E + 1).long()
+    off = on_device(*cut.tolist())
+    qx, sx, zx = mxq.mxfp8_quantize_grouped(normal(K, M, K), row_offsets=off, swizzled=True)
+    qw, sw, zw = mxq.mxfp8_quantize_grouped(normal(H, E, 2 * H, K, scale=0.05), swizzled=True)
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    y = mxq.mxfp8_gemm_grouped(qx, zx, qw, zw, off, FP32, swiglu=True, error_flag=flag)
+    want, bound = R.swiglu(*R.grouped(R.values(qx, sx), R.values(qw, sw), cut.tolist()), K)
+    R.check(y, want, bound, f"swiglu {E} {M} {H} {K}")
+    assert int(flag) == 0
+
+
 @pytest.mark.parametrize("M", [7, 1500])
 def test_first_calls_of_a_process_inside_a_capture(M):
     root = os.path.dirname(os.path.dirname(os.path.abspath(mxq.__file__)))
