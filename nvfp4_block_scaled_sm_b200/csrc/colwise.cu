@@ -34,9 +34,12 @@
 // table that each CTA builds from the offsets), the codes go to that expert's
 // columns or matrix, and the scale words straight into 128x4 tiles. Tiles
 // without rows are written as zeros without being staged. 32768 x 7168 bf16 of
-// 64 experts 146 us (a plain transpose of as many rows 127, the zero columns
-// among 40832 the rest), 8 x 2048 x 7168 59 us: loads and stores that do not
-// overlap, as in the plain form.
+// 64 experts 135 us (a plain transpose of as many rows 128; the output has 40832
+// columns), 8 x 2048 x 7168 59 us. What bounds them is the chain of a tile, copies
+// to barrier to codes to barrier to stores, at two CTAs a multiprocessor: three
+// CTAs, or three buffers, with the codes staged over the tile that was read and
+// two barriers more, take 5 % longer, fewer instructions for the addresses and
+// bands of row tiles the same.
 #include "common.cuh"
 
 namespace mxq {
@@ -113,42 +116,71 @@ struct ColArgs {
 enum Form { kPlain, kRagged, kStacked };
 
 struct TilePlace {
+  uint32_t rt, ct;   // row and column tile
+  uint32_t e;        // kRagged, kStacked: the expert
   int64_t r0;        // first row of x
   int rows;          // rows of x in the tile
   int64_t q0;        // q_t + q0: the tile's first code of column 0
   uint64_t s0;       // kRagged, kStacked: scale_t + s0: the scale tile of column block 0
 };
 
+// Of row tile p.rt; the expert is found by a walk from p.e.
 template <Form FORM>
-__device__ __forceinline__ TilePlace place_of(const ColArgs& a, uint32_t rt, const int64_t* off,
-                                              const int64_t* pb) {
-  TilePlace p{};
+__device__ __forceinline__ void set_place(const ColArgs& a, TilePlace& p, const int64_t* off, const int64_t* pb) {
+  const int64_t at = int64_t(p.rt) * kTileRows;
   if constexpr (FORM == kPlain) {
-    p.r0 = int64_t(rt) * kTileRows;
-    p.rows = a.M - p.r0 < kTileRows ? int(a.M - p.r0) : kTileRows;
-    p.q0 = p.r0;
+    p.r0 = p.q0 = at;
+    p.rows = a.M - at < kTileRows ? int(a.M - at) : kTileRows;
   } else if constexpr (FORM == kRagged) {
-    const int64_t at = int64_t(rt) * kTileRows;
     p.q0 = at;
-    p.s0 = uint64_t(rt) * 512;
-    if (at < pb[a.E]) {
-      int lo = 0, hi = a.E;  // invariant: pb[lo] <= at < pb[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pb[mid] <= at) lo = mid; else hi = mid;
-      }
-      p.r0 = off[lo] + (at - pb[lo]);
-      const int64_t left = off[lo + 1] - p.r0;
+    p.s0 = uint64_t(p.rt) * 512;
+    p.rows = 0;
+    while (p.e < uint32_t(a.E) && pb[p.e + 1] <= at) p.e++;
+    if (p.e < uint32_t(a.E)) {
+      p.r0 = off[p.e] + (at - pb[p.e]);
+      const int64_t left = off[p.e + 1] - p.r0;
       p.rows = left < kTileRows ? int(left) : kTileRows;
     }
   } else {
-    const uint32_t e = rt / a.n_rt, rb = rt - e * a.n_rt;
-    const int64_t at = int64_t(rb) * kTileRows;
-    p.r0 = int64_t(e) * a.M + at;
-    p.rows = a.M - at < kTileRows ? int(a.M - at) : kTileRows;
-    p.q0 = int64_t(e) * a.M * a.N + at;
-    p.s0 = e * a.swz_bytes + uint64_t(rb) * 512;
+    while (p.rt - p.e * a.n_rt >= a.n_rt) p.e++;
+    const uint32_t rb = p.rt - p.e * a.n_rt;
+    const int64_t r = int64_t(rb) * kTileRows;
+    p.r0 = int64_t(p.e) * a.M + r;
+    p.rows = a.M - r < kTileRows ? int(a.M - r) : kTileRows;
+    p.q0 = int64_t(p.e) * a.M * a.N + r;
+    p.s0 = p.e * a.swz_bytes + uint64_t(rb) * 512;
   }
+}
+
+// A CTA's tiles are blockIdx.x, + gridDim.x, ... The experts' forms advance row
+// and column tile by sums and the expert by the walk: divisions and a search by
+// every thread lie between a tile and the copies of the next (ragged, 32768 x
+// 7168 of 64: 147.8 us with them, 135.0 without; plain: 127.9, 129.3).
+template <Form FORM>
+__device__ __forceinline__ TilePlace first_place(const ColArgs& a, const int64_t* off, const int64_t* pb) {
+  TilePlace p{};
+  p.rt = blockIdx.x / a.n_ct;
+  p.ct = blockIdx.x - p.rt * a.n_ct;
+  if constexpr (FORM == kStacked) p.e = p.rt / a.n_rt;
+  set_place<FORM>(a, p, off, pb);
+  return p;
+}
+
+template <Form FORM>
+__device__ __forceinline__ TilePlace next_place(const ColArgs& a, TilePlace p, uint32_t tile, uint32_t d_rt, uint32_t d_ct,
+                                                const int64_t* off, const int64_t* pb) {
+  if constexpr (FORM == kPlain) {
+    p.rt = tile / a.n_ct;
+    p.ct = tile - p.rt * a.n_ct;
+  } else {
+    p.rt += d_rt;
+    p.ct += d_ct;
+    if (p.ct >= a.n_ct) {
+      p.ct -= a.n_ct;
+      p.rt++;
+    }
+  }
+  set_place<FORM>(a, p, off, pb);
   return p;
 }
 
@@ -228,11 +260,10 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
   int64_t* const pb = off + (FORM == kRagged ? a.E + 1 : 0);
   if constexpr (FORM == kRagged) load_expert_rows<false>(a.offsets, a.E, a.M, off, pb);
 
-  // stages tile `tile` into input buffer `b`: 128 rows x 16 chunks of 16
+  // stages a tile into input buffer `b`: 128 rows x 16 chunks of 16
   // bytes, 8 chunks per thread, zeros past M and N
-  auto stage = [&](uint32_t tile, const TilePlace& p, int b) {
-    const uint32_t ct = tile % a.n_ct;
-    const int64_t r0 = p.r0, c0 = int64_t(ct) * kTileCols;
+  auto stage = [&](const TilePlace& p, int b) {
+    const int64_t r0 = p.r0, c0 = int64_t(p.ct) * kTileCols;
     const int rows = p.rows;
     if (FORM == kRagged && rows == 0) return;  // written as zeros below
     const int row_bytes = (a.N - c0 < kTileCols ? int(a.N - c0) : kTileCols) * kEsize;
@@ -247,26 +278,26 @@ mxfp8_colwise_kernel(const __grid_constant__ ColArgs a) {
   };
 
   int b = 0;
+  const uint32_t d_rt = gridDim.x / a.n_ct, d_ct = gridDim.x - d_rt * a.n_ct;
   TilePlace next{};
   if (blockIdx.x < a.ntiles) {
-    next = place_of<FORM>(a, blockIdx.x / a.n_ct, off, pb);
-    stage(blockIdx.x, next, 0);
+    next = first_place<FORM>(a, off, pb);
+    stage(next, 0);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (uint32_t tile = blockIdx.x; tile < a.ntiles; tile += gridDim.x, b ^= 1) {
     // the next tile's copies go out before this one is worked on
     const TilePlace p = next;
     if (tile + gridDim.x < a.ntiles) {
-      next = place_of<FORM>(a, (tile + gridDim.x) / a.n_ct, off, pb);
-      stage(tile + gridDim.x, next, b ^ 1);
+      next = next_place<FORM>(a, p, tile + gridDim.x, d_rt, d_ct, off, pb);
+      stage(next, b ^ 1);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     __syncthreads();  // this tile is in shared memory; the previous one's outputs are written
 
     const uint8_t* in = smem + b * kInBytes;
-    const uint32_t ct = tile % a.n_ct;
-    const int64_t r0 = p.r0, c0 = int64_t(ct) * kTileCols;
+    const int64_t r0 = p.r0, c0 = int64_t(p.ct) * kTileCols;
     // rows of the output: ragged tiles are whole, with zeros behind the expert's rows
     const int rows = FORM == kRagged ? kTileRows : p.rows;
     const int row_bytes = (a.N - c0 < kTileCols ? int(a.N - c0) : kTileCols) * kEsize;  // multiple of 32
