@@ -193,13 +193,21 @@ __device__ __forceinline__ bool find_wgrad(const GroupArgs& a, ExpertCursor& c, 
 
 // silu(g) u = g u / (1 + e^-g). For g < 0 as (g t) (u t) / (1 + t^2) with t =
 // e^(g/2): e^-g has no fp32 value from -88.8 on where silu still has one, and a
-// large u brings back what lies below. The divisor is in [1, 2], where the
-// approximate reciprocal is off by at most an ulp (the division took 4 % more of
-// the kernel's time).
+// large u brings back what lies below. t = 2^p (1 + r ln 2), with p = -|g| log2(e)
+// / 2 rounded and r what the rounding and the constant's last bits took from
+// it, so that the error of p (2^-24 of up to 126) stays out of t; below g = -174
+// t has no normal value and the result is 0. The divisor is in [1, 2], where the
+// approximate reciprocal is off by at most an ulp. As the epilogue is what bounds
+// small K, its instructions count: with expf and a division 65 % more time at K =
+// 512, with expf alone 11 %, and 8 % at K = 2048.
 __device__ __forceinline__ float swiglu(float g, float u) {
-  const float t = expf(-0.5f * fabsf(g));
+  constexpr float kHi = 0.72134752f, kLo = 9.6298152e-9f;   // log2(e) / 2
+  const float a = fabsf(g), p = -kHi * a;
+  const float rest = fmaf(-kLo, a, fmaf(-kHi, a, -p));
+  float t, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(p));
+  t = fmaf(t, 0.69314718f * rest, t);
   const float m = g < 0.f ? t : 1.f;
-  float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(t, t, 1.f)));
   return (g * m * r) * (u * m);
 }
@@ -245,9 +253,9 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // memory: its quarters 0 and 1 come from a half of the gate's tile, 2 and 3
 // from a half of the up half's, and a TMA copy cannot put eight of 16 bytes
 // beside eight others; warp 11 joins them. 32768 rows of 64 experts, N = 4096,
-// K = 2048, under load: 346 us (505 with the sends; without SWIGLU 340); from K =
-// 4096 on the product's own time. At K = 512 silu itself is what bounds it, 8 us
-// a tile: 250 to 300 us (without SWIGLU 110).
+// K = 2048, under load: 325 us (505 with the sends; without SWIGLU 290 to 325); from K =
+// 4096 on the product's own time. At K = 512 silu itself is what bounds it, 6 us
+// a tile: 222 us (without SWIGLU 103).
 //
 // What bounds it: with few rows a weight, HBM (512 rows 297 us for weights of
 // 1.9 GB; 6.4 TB/s). With many, the power limit: 32768 rows of one expert take
