@@ -123,7 +123,8 @@ struct TilePlace {
   uint64_t s0;       // kRagged, kStacked: scale_t + s0: the scale tile of column block 0
 };
 
-// Of row tile p.rt; the expert is found by a walk from p.e.
+// Of row tile p.rt; the expert is found by a walk from p.e on, so a CTA's row
+// tiles may not fall.
 template <Form FORM>
 __device__ __forceinline__ void set_place(const ColArgs& a, TilePlace& p, const int64_t* off, const int64_t* pb) {
   const int64_t at = int64_t(p.rt) * kTileRows;
