@@ -125,3 +125,11 @@ def test_sizes():
     assert mxq.lib.mxq_grouped_padded_rows(1, 0) == 0
     assert mxq.lib.mxq_grouped_padded_rows(-1, 5) == -1
     assert mxq.lib.mxq_rmsnorm_backward_workspace_bytes(0, 64) == 0
+
+
+def test_sizes_in_python_are_the_librarys():
+    for M in (0, 1, 127, 128, 129, 5000):
+        for S in (0, 1, 3, 4, 5, 224):
+            assert mxq._tile_bytes(M, S) == mxq.lib.mxq_swizzled_scale_bytes(M, S)
+        for E in (1, 3, 1024):
+            assert (M + 127 * E) // 128 * 128 == mxq.lib.mxq_grouped_padded_rows(E, M)
