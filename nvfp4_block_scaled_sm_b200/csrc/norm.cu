@@ -6,10 +6,11 @@
 //   y = fp32(fp32(h rstd) weight), codes and scales of y by mx_rowwise.cu's rule
 //
 // The squares are added up in fp64 (the square of a bf16 or fp32 value leaves
-// fp32's range long before the value does), so that rstd is the correctly
-// rounded fp32 number but for sums that fp64 leaves on a border, and every
-// step after it is one IEEE operation: codes and scales are functions of the
-// inputs' bits whatever the order of the sum.
+// fp32's range long before the value does), and the root's reciprocal is one of
+// fp64 (an ulp or two), so that rstd is the correctly rounded fp32 number but
+// where fp64 leaves it on a border, and every step after it is one IEEE
+// operation: codes and scales are functions of the inputs' bits whatever the
+// order of the sum.
 //
 // Gradient: dx = grad_hidden + rstd (g w - xh mean(g w xh)) with xh = h rstd,
 // dweight = sum over the rows of g xh.
@@ -43,8 +44,9 @@ struct NormArgs {
   uint32_t S4;            // ceil(N / 128)
   uint32_t row_threads;   // threads of a row, a multiple of 32
   uint32_t row_ctas;      // CTAs with rows
-  double eps;
+  double eps, inv_n;      // inv_n = 1 / N
   int weight_bf16;
+  bool weight_v8;         // the weights lie on a 32-byte boundary
   bool v8;                // x, residual, hidden and normed: rows on 32-byte boundaries
   bool scale_words;       // compact scales can be written as words
 };
@@ -111,26 +113,35 @@ __device__ __forceinline__ double squares(const In16<T>& v) {
   return s;
 }
 
-// The 16 weights from element c on, in fp32.
-__device__ __forceinline__ void load_weight(float (&w)[16], const NormArgs& a, uint32_t c) {
-  if (a.weight_bf16) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.weight) + c);
-    const uint4 q0 = __ldg(p), q1 = __ldg(p + 1);
-    const uint32_t u[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+// 16 weights, as they lie in memory. fp32 ones by 32 bytes a load where they
+// lie on such boundaries: a warp's load by 16 touches as many lines for half of
+// them (16384 x 7168 bf16 115 us, so 100). bf16 ones are not faster so.
+template <bool WB>
+struct Weights16 {
+  static constexpr int kWords = WB ? 8 : 16;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const NormArgs& a, uint32_t c) {
+    const uint32_t* p = static_cast<const uint32_t*>(a.weight) + uint64_t(c >> 4) * kWords;
+    if (!WB && a.weight_v8) {
 #pragma unroll
-    for (int k = 0; k < 8; k++) {
-      w[2 * k] = bf16_lo(u[k]);
-      w[2 * k + 1] = bf16_hi(u[k]);
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c);
+      for (int i = 0; i < kWords; i += 8)
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+              "=r"(w[i + 6]), "=r"(w[i + 7])
+            : "l"(p + i));
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-      const float4 q = __ldg(p + k);
-      w[4 * k] = q.x; w[4 * k + 1] = q.y; w[4 * k + 2] = q.z; w[4 * k + 3] = q.w;
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + i));
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+      }
     }
   }
-}
+  __device__ __forceinline__ float2 pair(int k) const {
+    return WB ? make_float2(bf16_lo(w[k]), bf16_hi(w[k]))
+              : make_float2(__uint_as_float(w[2 * k % kWords]), __uint_as_float(w[(2 * k + 1) % kWords]));
+  }
+};
 
 // (a0 b0, a1 b1) and (a0 b0 + c0, a1 b1 + c1), each rounded once, in one instruction.
 __device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
@@ -152,15 +163,15 @@ __device__ __forceinline__ float2 fma2v(float2 a, float2 b, float2 c) {
 
 // y of 16 elements of a row, their codes, the group's scale (two lanes a
 // group, both or neither of them active; the lanes of a warp call together) and, where asked for, y itself.
-template <typename T>
-__device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, const float (&w)[16], int64_t row,
+template <typename T, bool WB>
+__device__ __forceinline__ void finish16(const NormArgs& a, const In16<T>& h, const Weights16<WB>& w, int64_t row,
                                          uint32_t c, float rstd, bool active) {
   const uint32_t lane = threadIdx.x & 31;
   float2 y[8];
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; k++) {
-    y[k] = mul2v(mul2(h.lo(k), h.hi(k), rstd), make_float2(w[2 * k], w[2 * k + 1]));
+    y[k] = mul2v(mul2(h.lo(k), h.hi(k), rstd), w.pair(k));
     amax = fmaxf(amax, fmaxf(fabsf(y[k].x), fabsf(y[k].y)));   // NaN raises no maximum
   }
   amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
@@ -205,7 +216,7 @@ __device__ __forceinline__ void pad_tiles(const NormArgs& a, uint32_t cta) {
   for (uint32_t j = threadIdx.x & 31; j < a.S4; j += 32) st_u32(p + (uint64_t(j) << 9), 0);
 }
 
-template <typename T, bool RES, int C, bool LOOP>
+template <typename T, bool RES, bool WB, int C, bool LOOP>
 __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   pdl_enter();
   if (blockIdx.x >= a.row_ctas) return pad_tiles(a, blockIdx.x - a.row_ctas);
@@ -221,7 +232,12 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
   const T* res = static_cast<const T*>(a.residual) + (RES ? row * a.ld_res : 0);
   T* hidden = static_cast<T*>(a.hidden) + (RES ? row * int64_t(a.N) : 0);
 
+  // the first piece's weights are asked for before the row's sum is known where
+  // the registers have room for them (16384 x 7168 98 us, so 90) and a row has
+  // work to hide the rest (32768 x 2048, one piece, 57 and 59)
+  constexpr bool kEarly = sizeof(T) == 2 && WB && C == 2;
   In16<T> v[C];
+  Weights16<WB> w;
   double ss = 0.0;
   if constexpr (LOOP) {
     for (uint32_t c = t * 16; have && c < a.N; c += a.row_threads * 16) {
@@ -247,6 +263,7 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
         if constexpr (RES) r[i].zero();
       }
     }
+    if (kEarly && t * 16 < a.N) w.load(a, t * 16);
 #pragma unroll
     for (int i = 0; i < C; i++) {
       const uint32_t c = (i * a.row_threads + t) * 16;
@@ -261,11 +278,12 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
   if (lane == 0) sums[warp] = ss;
   __syncthreads();
-  // one thread a row: the other warps' fp64 pipes stay free
+  // one thread a row: the other warps' fp64 pipes stay free; no division, no
+  // square root and its reciprocal (32768 x 2048 57 us with them, so 51)
   if (t == 0) {
     double s = 0.0;
     for (uint32_t i = 0; i < row_warps; i++) s += sums[warp + i];
-    const float r = float(1.0 / sqrt(s / double(a.N) + a.eps));
+    const float r = float(rsqrt(fma(s, a.inv_n, a.eps)));
     rstds[sub] = r;
     if (have) a.rstd[row] = r;
   }
@@ -276,10 +294,9 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
     for (uint32_t c0 = (t & ~31u) * 16; c0 < a.N; c0 += a.row_threads * 16) {   // warps stay together
       const uint32_t c = c0 + lane * 16;
       const bool active = have && c < a.N;
-      float w[16];
       if (active) {
         load16(v[0], h + c, a.v8);
-        load_weight(w, a, c);
+        w.load(a, c);
       } else {
         v[0].zero();
       }
@@ -290,34 +307,41 @@ __global__ void __launch_bounds__(1024) mxfp8_rmsnorm_kernel(const __grid_consta
     for (int i = 0; i < C; i++) {
       const uint32_t c = (i * a.row_threads + t) * 16;
       const bool active = have && c < a.N;
-      float w[16];
-      if (active) load_weight(w, a, c);
+      if ((!kEarly || i > 0) && active) w.load(a, c);
       finish16(a, v[i], w, row, c, rstd, active);
     }
   }
 }
 
-template <typename T, bool RES, int C, bool LOOP>
+template <typename T, bool RES, bool WB, int C, bool LOOP>
 mxq_status launch_norm(NormArgs& a, uint32_t rows, cudaStream_t s) {
   const uint32_t threads = a.row_threads * rows;
   a.row_ctas = uint32_t((uint64_t(a.M) + rows - 1) / rows);
   const uint32_t pad = a.swz ? uint32_t(-a.M & 127) : 0;
   const uint64_t grid = uint64_t(a.row_ctas) + (pad + threads / 32 - 1) / (threads / 32);
   if (grid > 0x7fffffffull) return MXQ_ERR_SHAPE;
-  return launched(launch_pdl_ex(mxfp8_rmsnorm_kernel<T, RES, C, LOOP>, uint32_t(grid), threads, 0, s, a));
+  return launched(launch_pdl_ex(mxfp8_rmsnorm_kernel<T, RES, WB, C, LOOP>, uint32_t(grid), threads, 0, s, a));
 }
 
-template <typename T, bool RES>
+template <typename T, bool RES, bool WB>
 mxq_status norm_dispatch(NormArgs& a, cudaStream_t s) {
   const uint32_t pieces = a.N / 16;
   if (pieces > 2048) {
     a.row_threads = 1024;
-    return launch_norm<T, RES, 1, true>(a, 1, s);
+    return launch_norm<T, RES, WB, 1, true>(a, 1, s);
   }
-  const int C = pieces <= 128 ? 1 : 2;
+  // one piece a lane for short rows; also for fp32 with a residual, whose two
+  // pieces a lane leave the registers (16384 x 4096 fp32 146 us, so 132; at 14336
+  // columns 142 against 146)
+  const int C = pieces <= (sizeof(T) == 4 && RES ? 512 : 128) ? 1 : 2;
   a.row_threads = ((pieces + C - 1) / C + 31) / 32 * 32;
   const uint32_t rows = std::max(1u, 128 / a.row_threads);
-  return C == 1 ? launch_norm<T, RES, 1, false>(a, rows, s) : launch_norm<T, RES, 2, false>(a, rows, s);
+  return C == 1 ? launch_norm<T, RES, WB, 1, false>(a, rows, s) : launch_norm<T, RES, WB, 2, false>(a, rows, s);
+}
+
+template <typename T, bool RES>
+mxq_status norm_weight(NormArgs& a, cudaStream_t s) {
+  return a.weight_bf16 ? norm_dispatch<T, RES, true>(a, s) : norm_dispatch<T, RES, false>(a, s);
 }
 
 // ------------------------------------------------------------ gradient
@@ -763,13 +787,15 @@ mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld
   a.N = uint32_t(N);
   a.S4 = uint32_t((N + 127) / 128);
   a.eps = eps;
+  a.inv_n = 1.0 / double(N);
   a.weight_bf16 = weight_dt == MXQ_BF16;
+  a.weight_v8 = aligned32(weight);
   a.v8 = aligned32(x) && (uint64_t(ld_x) * es) % 32 == 0 && aligned32(hidden) && aligned32(normed) &&
          aligned32(residual) && (!residual || (uint64_t(ld_res) * es) % 32 == 0);
   a.scale_words = (reinterpret_cast<uintptr_t>(scale) & 3u) == 0 && (N / 32) % 4 == 0;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dt == MXQ_BF16) return residual ? norm_dispatch<uint16_t, true>(a, s) : norm_dispatch<uint16_t, false>(a, s);
-  return residual ? norm_dispatch<float, true>(a, s) : norm_dispatch<float, false>(a, s);
+  if (dt == MXQ_BF16) return residual ? norm_weight<uint16_t, true>(a, s) : norm_weight<uint16_t, false>(a, s);
+  return residual ? norm_weight<float, true>(a, s) : norm_weight<float, false>(a, s);
 }
 
 size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
