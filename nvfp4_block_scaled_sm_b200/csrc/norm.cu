@@ -27,6 +27,9 @@ namespace {
 // such pieces a lane; the warps of a row exchange their sums through shared
 // memory once. Small rows share a CTA. Rows of more than 32 * 1024 elements are
 // read twice instead (LOOP), the second time from L2.
+// 16384 x 7168 bf16 with a residual 125 us (127 at the copy rate); without one 87
+// (54), where a row's chain of load, sum, barrier and codes bounds it, at the
+// rows that the registers hold.
 
 struct NormArgs {
   const void* x;
