@@ -575,15 +575,14 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       const uint32_t cols = columns() / 2;                // of this warp, a multiple of 16
       const uint32_t taddr = tmem + ((quarter * 32) << 16) + half * cols;
       uint32_t v[128];
-      bool ok = true;
+      // the phase completes once for everyone: a lane that saw it lets the warp go
+      bool ok = a.nk == 0 || __any_sync(kFull, mbar_wait(acc_full, done & 1u, kWaitNs));
+      if constexpr (SWIGLU) ok = meet(pair_id, ok);       // (both warps go on, or neither; the slots are read)
+      if (!ok) {
+        if (lane == 0) record_error(a.err, kErrAccumWait);
+        break;
+      }
       if (a.nk > 0) {
-        // the phase completes once for everyone: a lane that saw it lets the warp go
-        ok = __any_sync(kFull, mbar_wait(acc_full, done & 1u, kWaitNs));
-        if constexpr (SWIGLU) ok = meet(pair_id, ok);     // (both warps go on, or neither)
-        if (!ok) {
-          if (lane == 0) record_error(a.err, kErrAccumWait);
-          break;
-        }
         tc_fence_after();
         // (columns that the tile does not have are read and not used)
 #pragma unroll

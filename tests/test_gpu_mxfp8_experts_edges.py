@@ -78,6 +78,22 @@ def test_swiglu_over_k(E, M, H, K):
     assert int(flag) == 0
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_a_sum_of_nothing(swiglu):
+    """K = 0: the experts' rows are zeros, rows of no expert are left."""
+    M, N, E = 3000, 512, 4
+    none = lambda *shape: torch.empty(*shape, dtype=torch.uint8, device="cuda")
+    flag = torch.zeros(1, dtype=torch.int32, device="cuda")
+    d = torch.full((M, N // 2 if swiglu else N), 7.0, dtype=BF16, device="cuda")
+    off = on_device(0, 5, 5, 1700, 2990)
+    st = mxq.lib.mxfp8_gemm_grouped(None, None, 0, None, None, E, off.data_ptr(), M, N, 0, int(swiglu), d.data_ptr(), 0,
+                                    flag.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert not d[:2990].any() and (d[2990:] == 7).all() and int(flag) == 0
+    y = mxq.mxfp8_gemm_grouped(none(M, 0), none(0), none(E, N, 0), none(0), off, swiglu=swiglu)
+    assert not y[:2990].any()
+
+
 @pytest.mark.parametrize("M", [7, 1500])
 def test_first_calls_of_a_process_inside_a_capture(M):
     root = os.path.dirname(os.path.dirname(os.path.abspath(mxq.__file__)))
