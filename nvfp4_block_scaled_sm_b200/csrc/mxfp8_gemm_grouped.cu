@@ -263,21 +263,36 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 // weights from HBM, 750 to 835 us, and 985 us once the clock has settled at
 // 1.2 GHz under load.
 
-constexpr uint32_t kRowTile = 256;                          // most rows of a tile
-constexpr int kRowStages = 6;
 constexpr uint32_t kWeightTile = 128 * kBK;                 // a CTA's rows of the weight
-constexpr uint32_t kRowStage = 2 * kWeightTile;             // and the room for its half of the rows
-constexpr uint32_t kRowScales = 3 * kSfTile;                // weight (SWIGLU: unused), two tiles of rows
-constexpr uint32_t kRowSfCols = 12;
 constexpr uint32_t kSendBytes = 32 * 8 * 4;                 // eight columns of a warp
 constexpr uint32_t kJoin = 8;                               // K blocks of a group of joined scale tiles
 constexpr uint32_t kJoinRing = 2;                           // groups
 constexpr uint32_t kRowBars = 256;
-constexpr uint32_t kRowSmem = kRowStages * (kRowStage + kRowScales) + kRowBars + 2 * kEpiWarps * kSendBytes +
-                              kJoinRing * kJoin * kSfTile + 1024;
-static_assert(256 + kRowStages * kRowSfCols <= 512, "tensor memory");
-static_assert(kRowSmem <= 232448, "shared memory");
-static_assert(8 * (2 * kRowStages + 2 + 3 * kJoinRing) + 4 <= kRowBars, "barriers");
+
+// FEW: calls of at most 64 rows, whose tiles leave the shared memory to more
+// stages: a pair's loads are bound by the bytes in flight where few pairs have
+// tiles (8 rows, K = 7168: one expert of 4096 17.0 us with six stages, FEW us
+// with ten).
+template <bool SWIGLU, bool FEW>
+struct RowCfg {
+  static constexpr uint32_t kTile = FEW ? 64 : 256;                      // most rows of a tile
+  static constexpr int kStages = FEW ? (SWIGLU ? 9 : 10) : 6;
+  static constexpr uint32_t kStage = kWeightTile + kTile / 2 * kBK;      // and its half of the rows
+  static constexpr uint32_t kXTiles = FEW ? 1 : 2;                       // scale tiles of the rows
+  static constexpr uint32_t kXSf = SWIGLU ? 0 : kSfTile;                 // behind the weight's, which SWIGLU joins
+  static constexpr uint32_t kScales = kXSf + kXTiles * kSfTile;
+  static constexpr uint32_t kSfCols = 4 * (1 + kXTiles);
+  // shared memory behind the stages' tiles; SWIGLU: joined scale tiles [group][K
+  // block], columns for the other warp [warp][2]
+  static constexpr uint32_t kScalesAt = kStages * kStage;
+  static constexpr uint32_t kJoinedAt = kScalesAt + kStages * kScales;
+  static constexpr uint32_t kSlotsAt = kJoinedAt + (SWIGLU ? kJoinRing * kJoin * kSfTile : 0);
+  static constexpr uint32_t kBarsAt = kSlotsAt + (SWIGLU ? 2 * kEpiWarps * kSendBytes : 0);
+  static constexpr uint32_t kSmem = kBarsAt + kRowBars + 1024;           // (the start is rounded up to 1 KiB)
+  static_assert(256 + kStages * kSfCols <= 512, "tensor memory");
+  static_assert(kSmem <= 232448, "shared memory");
+  static_assert(8 * (2 * kStages + 2 + 2 * kJoinRing + kJoinRing) + 4 <= kRowBars, "barriers");
+};
 
 // The rows in boxes of 128, 64, 32 and 16.
 struct RowMaps {
@@ -328,22 +343,22 @@ __device__ __forceinline__ void store_columns(OutT* p, uint32_t ld, const uint32
   }
 }
 
-template <bool SWIGLU, typename OutT>
+template <bool SWIGLU, bool FEW, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGroupThreads, 1)
 mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ RowMaps rows,
                   const __grid_constant__ CUtensorMap tma_sfw,
                   const __grid_constant__ CUtensorMap tma_sfx, const __grid_constant__ GroupArgs a) {
+  using R = RowCfg<SWIGLU, FEW>;
+  constexpr int kStages = R::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;           // operand tiles: 128-byte swizzle atoms of 1 KiB
   uint8_t* smem = smem_raw + (base - raw);
-  const uint32_t scales = base + kRowStages * kRowStage;
-  const uint32_t joined = scales + kRowStages * kRowScales;         // SWIGLU: [group][K block], scale tiles
-  const uint32_t slots = joined + kJoinRing * kJoin * kSfTile;      // SWIGLU: [warp][2], columns for the other warp
-  const uint32_t bars = slots + 2 * kEpiWarps * kSendBytes;
+  const uint32_t scales = base + R::kScalesAt, joined = base + R::kJoinedAt, slots = base + R::kSlotsAt;
+  const uint32_t bars = base + R::kBarsAt;
   auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
-  auto empty_bar = [&](uint32_t s) { return bars + 8u * (kRowStages + s); };
-  const uint32_t acc_full = bars + 8u * (2 * kRowStages);
+  auto empty_bar = [&](uint32_t s) { return bars + 8u * (kStages + s); };
+  const uint32_t acc_full = bars + 8u * (2 * kStages);
   const uint32_t acc_empty = acc_full + 8u;
   auto join_full = [&](uint32_t g) { return acc_empty + 8u * (1 + g); };
   auto join_empty = [&](uint32_t g) { return acc_empty + 8u * (1 + kJoinRing + g); };
@@ -361,7 +376,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 32) {
-    for (int s = 0; s < kRowStages; s++) {
+    for (int s = 0; s < kStages; s++) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
@@ -382,10 +397,10 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
   pdl_enter();  // (all of the above overlaps the end of the grid before)
 
   ExpertCursor cursor;
-  cursor.start(a.offsets, a.E, a.rows, kRowTile, lane);
+  cursor.start(a.offsets, a.E, a.rows, R::kTile, lane);
   Place p{};
   // columns of a tile's accumulator: its rows, a multiple of 32
-  auto columns = [&]() { return min(kRowTile, (p.left + 31u) & ~31u); };
+  auto columns = [&]() { return min(R::kTile, (p.left + 31u) & ~31u); };
 
   // first row of the weight of this CTA in a tile (SWIGLU: of the gate's), and its scale block
   auto w_row_of = [&](const Place& q) {
@@ -415,14 +430,14 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
           break;
         }
         const uint32_t bar = bar0 + 8u * s, x = kb * kBK;
-        const uint32_t st = base + s * kRowStage, sf = scales + s * kRowScales;
+        const uint32_t st = base + s * R::kStage, sf = scales + s * R::kScales;
         if (weights) {
           if (rank == 0) mbar_elect_expect_tx(full_bar(s), tx);
           tma_elect_2d_pair(st, &tma_w, bar, int32_t(x), int32_t(w_row));
           if constexpr (SWIGLU) {
             tma_elect_2d_pair(st + kWeightTile / 2, &tma_w, bar, int32_t(x), int32_t(w_row + a.n));
-            tma_elect_2d_pair(sf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
-            if (n > 128) tma_elect_2d_pair(sf + 2 * kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
+            tma_elect_2d_pair(sf + R::kXSf, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
+            if (!FEW && n > 128) tma_elect_2d_pair(sf + R::kXSf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
           } else {
             tma_elect_2d_pair(sf, &tma_sfw, bar, 0, int32_t(w_sf + 4 * kb));
           }
@@ -435,10 +450,10 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
               r += 128u >> b;
             }
         } else {
-          tma_elect_2d_pair(sf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
-          if (n > 128) tma_elect_2d_pair(sf + 2 * kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
+          tma_elect_2d_pair(sf + R::kXSf, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
+          if (!FEW && n > 128) tma_elect_2d_pair(sf + R::kXSf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
         }
-        if (++s == kRowStages) {
+        if (++s == kStages) {
           s = 0;
           phase ^= 1u;
         }
@@ -515,8 +530,8 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       const uint64_t op0 = operand_desc(base), sc0 = scale_desc(scales);
       const uint32_t op_lo = uint32_t(op0), op_hi = uint32_t(op0 >> 32);
       const uint32_t sc_lo = uint32_t(sc0), sc_hi = uint32_t(sc0 >> 32);
-      constexpr uint32_t kStageW = kRowStage >> 4, kTileW = kWeightTile >> 4;
-      constexpr uint32_t kScaleW = kRowScales >> 4;
+      constexpr uint32_t kStageW = R::kStage >> 4, kTileW = kWeightTile >> 4;
+      constexpr uint32_t kScaleW = R::kScales >> 4;
       const uint32_t join_lo = uint32_t(scale_desc(joined));
       uint32_t s = 0, phase = 0, done = 0, g = 0, join_phase = 0;
       for (; find_rows(a, cursor, tile, lane, p); tile += step, done++) {
@@ -538,9 +553,9 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
           }
           tc_fence_after();
           const uint32_t so = s * kStageW, sc = sc_lo + s * kScaleW;
-          const uint32_t sfw_t = tmem + 256 + kRowSfCols * s, sfx_t = sfw_t + 4u;
+          const uint32_t sfw_t = tmem + 256 + R::kSfCols * s, sfx_t = sfw_t + 4u;
           mma_block_pair(tmem, op_lo + so, op_lo + so + kTileW, op_hi, idesc, sfw_t, sfx_t,
-                         SWIGLU ? join_lo + (g * kJoin + kb % kJoin) * kScTileW : sc, sc + kScTileW, sc_hi, n > 128, kb,
+                         SWIGLU ? join_lo + (g * kJoin + kb % kJoin) * kScTileW : sc, sc + (R::kXSf >> 4), sc_hi, !FEW && n > 128, kb,
                          empty_bar(s));
           if (last) {
             mma_commit_pair(join_empty(g));
@@ -549,7 +564,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
               join_phase ^= 1u;
             }
           }
-          if (++s == kRowStages) {
+          if (++s == kStages) {
             s = 0;
             phase ^= 1u;
           }
@@ -574,7 +589,8 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
     for (; find_rows(a, cursor, tile, lane, p); tile += step, done++) {
       const uint32_t cols = columns() / 2;                // of this warp, a multiple of 16
       const uint32_t taddr = tmem + ((quarter * 32) << 16) + half * cols;
-      uint32_t v[128];
+      constexpr int kCols = R::kTile / 2;                 // most columns of a warp
+      uint32_t v[kCols];
       // the phase completes once for everyone: a lane that saw it lets the warp go
       bool ok = a.nk == 0 || __any_sync(kFull, mbar_wait(acc_full, done & 1u, kWaitNs));
       if constexpr (SWIGLU) ok = meet(pair_id, ok);       // (both warps go on, or neither; the slots are read)
@@ -586,23 +602,23 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
         tc_fence_after();
         // (columns that the tile does not have are read and not used)
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32_start(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+        for (int c = 0; c < kCols; c += 32) tmem_ld32_start(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&v[c]));
+        for (int c = 0; c < kCols; c += 32) tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&v[c]));
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(lead_acc_empty);
       } else {
 #pragma unroll
-        for (int c = 0; c < 128; c++) v[c] = 0;
+        for (int c = 0; c < kCols; c++) v[c] = 0;
       }
       const uint32_t f = (SWIGLU ? p.n_blk * 128 + rank * 64 + (quarter & 1) * 32 : p.n_blk * 256 + rank * 128 + quarter * 32) + lane;
       const uint32_t t0 = half * cols + (SWIGLU && upper ? 8 : 0);
-      int32_t left = f < a.n ? int32_t(min(p.left, kRowTile)) - int32_t(t0) : 0;
+      int32_t left = f < a.n ? int32_t(min(p.left, R::kTile)) - int32_t(t0) : 0;
       OutT* d = static_cast<OutT*>(a.d) + uint64_t(p.row + t0) * a.n + f;
       if constexpr (sizeof(OutT) == 2) d += int64_t(lane & 1) * (int64_t(a.n) - 1);
 #pragma unroll
-      for (int c = 0; c < 128; c += 16) {
+      for (int c = 0; c < kCols; c += 16) {
         if (uint32_t(c) >= cols) break;
         if constexpr (!SWIGLU) {
           store_columns<16>(d, a.n, &v[c], left);
@@ -964,9 +980,19 @@ mxq_status launch_group(uint32_t smem, uint64_t most, cudaStream_t s, const Args
   return launched(cudaLaunchKernelEx(&cfg, Kernel, args...));
 }
 
-template <bool SWIGLU, typename OutT>
+template <bool SWIGLU, bool FEW, typename OutT>
 mxq_status launch_rows(const GroupMaps& m, const GroupArgs& args, uint64_t most, cudaStream_t s) {
-  return launch_group<mxfp8_rows_kernel<SWIGLU, OutT>, true>(kRowSmem, most, s, m.b, m.rows, m.sfb, m.sfa, args);
+  return launch_group<mxfp8_rows_kernel<SWIGLU, FEW, OutT>, true>(RowCfg<SWIGLU, FEW>::kSmem, most, s, m.b, m.rows,
+                                                                   m.sfb, m.sfa, args);
+}
+
+template <typename OutT>
+mxq_status launch_rows(const GroupMaps& m, const GroupArgs& args, bool swiglu, uint64_t active, cudaStream_t s) {
+  const bool few = args.rows <= RowCfg<false, true>::kTile;
+  // tiles that the experts with rows can have
+  const uint64_t most = (few ? active : args.rows / RowCfg<false, false>::kTile + active) * args.tiles_n;
+  if (few) return swiglu ? launch_rows<true, true, OutT>(m, args, most, s) : launch_rows<false, true, OutT>(m, args, most, s);
+  return swiglu ? launch_rows<true, false, OutT>(m, args, most, s) : launch_rows<false, false, OutT>(m, args, most, s);
 }
 
 template <bool PAIR, typename OutT>
@@ -1032,10 +1058,8 @@ mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t 
   }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   args.tiles_n = uint32_t((N + 255) / 256);               // swiglu: 128 rows of each half
-  const uint64_t most = (uint64_t(M) / kRowTile + active) * args.tiles_n;
-  if (out_dt == MXQ_BF16)
-    return swiglu ? launch_rows<true, uint16_t>(maps, args, most, s) : launch_rows<false, uint16_t>(maps, args, most, s);
-  return swiglu ? launch_rows<true, float>(maps, args, most, s) : launch_rows<false, float>(maps, args, most, s);
+  return out_dt == MXQ_BF16 ? launch_rows<uint16_t>(maps, args, swiglu != 0, active, s)
+                            : launch_rows<float>(maps, args, swiglu != 0, active, s);
 }
 
 mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, const uint8_t* qb_t,
