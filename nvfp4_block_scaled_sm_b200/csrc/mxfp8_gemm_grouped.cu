@@ -271,8 +271,8 @@ constexpr uint32_t kRowBars = 256;
 
 // FEW: calls of at most 64 rows, whose tiles leave the shared memory to more
 // stages: a pair's loads are bound by the bytes in flight where few pairs have
-// tiles (8 rows, K = 7168: one expert of 4096 17.0 us with six stages, FEW us
-// with ten).
+// tiles, and by the issue of the loads (8 rows of eight experts, 4096 x 7168,
+// 42.9 us with six stages, 40.2 with ten; one expert 17.0 and 12.6).
 template <bool SWIGLU, bool FEW>
 struct RowCfg {
   static constexpr uint32_t kTile = FEW ? 64 : 256;                      // most rows of a tile
@@ -410,12 +410,19 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
 
   if (warp == 0 || warp == 2 + kEpiWarps || (!SWIGLU && warp == 3 + kEpiWarps)) {
     // --------------------------------------------------------- producers
-    // warp 0 loads the weight and its scales, warp 10 the rows, warp 11 their
-    // scales: the issue of a TMA load holds a warp for 100 cycles and more.
-    // SWIGLU: warp 0 the two halves of the weight and the rows' scales.
+    // The issue of a TMA load holds a warp for 100 cycles and more. Warp 0 loads
+    // the weight and its scales, warp 10 the rows, warp 11 their scales; SWIGLU:
+    // warp 0 the two halves of the weight and the rows' scales. FEW without
+    // SWIGLU: the three take the K blocks in turn, each all loads of its own, as
+    // no MMAs hide the longest share (one expert of 4096 x 7168 15.5 us, in turn
+    // 12.6). Else a stage would only be loaded later (32768 rows of 64 970 us, in
+    // turn 1050; SWIGLU, two warps, 8 rows 42.6 and 44.2).
+    constexpr bool kTurns = FEW && !SWIGLU;
+    constexpr uint32_t kStep = kTurns ? 3 : 1;
     const bool weights = warp == 0, rows_warp = warp == 2 + kEpiWarps;
+    const uint32_t first = !kTurns || warp == 0 ? 0 : warp - (1 + kEpiWarps);
     const uint32_t bar0 = cluster_addr(full_bar(0), 0);
-    uint32_t s = 0, phase = 1;
+    uint32_t s = first, phase = 1, kb = first;
     bool ok = true;
     for (; ok && find_rows(a, cursor, tile, lane, p); tile += step) {
       const uint32_t n = columns(), mine = n / 2;         // this CTA's share of the rows, a multiple of 16
@@ -423,7 +430,7 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
       const uint32_t w_row = w_row_of(p), w_sf = 4 * w_blk_of(p) * a.kp4;
       const uint32_t x_sf = 4 * p.block * a.kp4;
       const uint32_t tx = 2 * (kWeightTile + mine * kBK + kSfTile * ((n > 128 ? 2 : 1) + (SWIGLU ? 0 : 1)));
-      for (uint32_t kb = 0; kb < a.nk; kb++) {
+      for (; kb < a.nk; kb += kStep) {
         if (!__all_sync(kFull, mbar_wait(empty_bar(s), phase, kWaitNs))) {
           if (lane == 0) record_error(a.err, kErrEmptyWait);
           ok = false;
@@ -431,33 +438,47 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
         }
         const uint32_t bar = bar0 + 8u * s, x = kb * kBK;
         const uint32_t st = base + s * R::kStage, sf = scales + s * R::kScales;
-        if (weights) {
+        auto load_weight = [&]() {
           if (rank == 0) mbar_elect_expect_tx(full_bar(s), tx);
           tma_elect_2d_pair(st, &tma_w, bar, int32_t(x), int32_t(w_row));
-          if constexpr (SWIGLU) {
+          if constexpr (SWIGLU)
             tma_elect_2d_pair(st + kWeightTile / 2, &tma_w, bar, int32_t(x), int32_t(w_row + a.n));
-            tma_elect_2d_pair(sf + R::kXSf, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
-            if (!FEW && n > 128) tma_elect_2d_pair(sf + R::kXSf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
-          } else {
+          else
             tma_elect_2d_pair(sf, &tma_sfw, bar, 0, int32_t(w_sf + 4 * kb));
-          }
-        } else if (rows_warp) {
+        };
+        auto load_rows = [&]() {
           uint32_t r = 0;
 #pragma unroll
-          for (int b = 0; b < 4; b++)
+          for (int b = FEW ? 2 : 0; b < 4; b++)
             if (mine & (128u >> b)) {
               tma_elect_2d_pair(st + kWeightTile + r * kBK, &rows.box[b], bar, int32_t(x), int32_t(x_row + r));
               r += 128u >> b;
             }
-        } else {
+        };
+        auto load_row_scales = [&]() {
           tma_elect_2d_pair(sf + R::kXSf, &tma_sfx, bar, 0, int32_t(x_sf + 4 * kb));
-          if (!FEW && n > 128) tma_elect_2d_pair(sf + R::kXSf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
+          if (!FEW && n > 128)
+            tma_elect_2d_pair(sf + R::kXSf + kSfTile, &tma_sfx, bar, 0, int32_t(x_sf + 4 * a.kp4 + 4 * kb));
+        };
+        if constexpr (kTurns) {
+          load_weight();
+          load_rows();
+          load_row_scales();
+        } else if (weights) {
+          load_weight();
+          if constexpr (SWIGLU) load_row_scales();
+        } else if (rows_warp) {
+          load_rows();
+        } else {
+          load_row_scales();
         }
-        if (++s == kStages) {
-          s = 0;
+        s += kStep;
+        if (s >= kStages) {
+          s -= kStages;
           phase ^= 1u;
         }
       }
+      kb -= a.nk;                                         // of the next tile
     }
   } else if (SWIGLU && warp == 3 + kEpiWarps) {
     // ------------------------------------- joined scale tiles of the weight
