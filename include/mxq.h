@@ -351,8 +351,8 @@ mxq_status mxfp8_gemm(const uint8_t* qa, const uint8_t* sa_swz, const uint8_t* q
  * K % 32 == 0; N % 16 == 0, with swiglu N % 256 == 0 (each half is whole scale
  * tiles); pointers 16-byte aligned. K == 0 writes zeros into the experts' rows.
  * M, N and E * N are below 2^31 - 256, K at most 2^26, and the scales of either
- * side below 2^38 bytes. One launch of persistent pairs of CTAs (384 threads and about
- * 226 KB of shared memory each) over tiles of up to 256 rows x 256 columns. */
+ * side below 2^38 bytes. One launch of persistent pairs of CTAs (384 threads and up to
+ * 224 KB of shared memory each) over tiles of up to 256 rows x 256 columns. */
 mxq_status mxfp8_gemm_grouped(const uint8_t* qa, const uint8_t* sa_swz, int64_t sa_bytes,
                               const uint8_t* qb, const uint8_t* sb_swz, int32_t E,
                               const int64_t* row_offsets, int64_t M, int64_t N, int64_t K, int swiglu,
