@@ -1104,10 +1104,11 @@ def rmsnorm_backward(grad: torch.Tensor, hidden: torch.Tensor, weight: torch.Ten
         gh, ld_gh = grad_hidden.data_ptr(), _rows_view(grad_hidden)[2]
     dx = _empty_as(hidden, dtype)
     dw = _empty_like(hidden, (N,), weight.dtype)
-    n = lib.mxq_rmsnorm_backward_workspace_bytes(M, N)
-    work = _empty_like(hidden, (n,), torch.uint8)
+    n = lib.mxq_rmsnorm_backward_workspace_bytes(M, N)           # (none for few rows)
+    work = _empty_like(hidden, (n,), torch.uint8) if n else None
     _launch("mxq_rmsnorm_backward", index, grad.data_ptr(), dt, M, N, ld_g, hidden.data_ptr(), ld_h,
-            weight.data_ptr(), wdt, rstd.data_ptr(), gh, ld_gh, dx.data_ptr(), dw.data_ptr(), work.data_ptr(), n)
+            weight.data_ptr(), wdt, rstd.data_ptr(), gh, ld_gh, dx.data_ptr(), dw.data_ptr(),
+            None if work is None else work.data_ptr(), n)
     return dx, dw
 
 

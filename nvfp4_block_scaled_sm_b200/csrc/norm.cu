@@ -356,7 +356,8 @@ mxq_status norm_weight(NormArgs& a, cudaStream_t s) {
 // memory with cp.async, each thread its own units: no thread waits for
 // another's copies, and the only barrier of a row is that of the sum
 // mean(g w xh). The CTAs' sums of dweight go to the workspace [grid, N] and a
-// second kernel adds them up in a fixed order. Rows of more than 16384
+// second kernel adds them up in a fixed order; for few rows the CTAs are a
+// cluster and add them up in its shared memory. Rows of more than 16384
 // elements take a kernel that reads them twice, and dweight one of its own.
 
 struct GradArgs {
@@ -364,6 +365,7 @@ struct GradArgs {
   const float* rstd;
   void* dx;
   float* part;            // [grid, N], or NULL
+  void* dweight;          // of a cluster, or NULL
   int64_t ld_g, ld_h, ld_gh;
   int64_t M;
   uint32_t N;
@@ -402,6 +404,29 @@ struct Unit {
                           __float_as_uint(f[1].y)));
   }
 };
+
+__device__ __forceinline__ void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The float at this CTA's shared address `at`, in CTA `rank` of the cluster.
+__device__ __forceinline__ float load_cluster(uint32_t at, uint32_t rank) {
+  float v;
+  asm volatile("{ .reg .b32 a; mapa.shared::cluster.u32 a, %1, %2; ld.shared::cluster.f32 %0, [a]; }"
+               : "=f"(v)
+               : "r"(at), "r"(rank)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void store_weight(void* dweight, int bf16, uint32_t c, float s) {
+  if (bf16)
+    static_cast<uint16_t*>(dweight)[c] = uint16_t(cvt_bf16x2(s, 0.f));
+  else
+    static_cast<float*>(dweight)[c] = s;
+}
+
+constexpr uint32_t kCluster = 16;        // CTAs (more than the portable eight)
 
 __device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
@@ -583,6 +608,26 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
       }
     }
   }
+  if (a.dweight) {
+    // the ring, which holds at least 8 N bytes, takes the sums
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < C; i++)
+      if (column(i) < a.N)
+#pragma unroll
+        for (int k = 0; k < kPairs; k++) *reinterpret_cast<float2*>(ring + 4 * column(i) + 8 * k) = dw[i][k];
+    sync_cluster();
+    for (uint32_t c = blockIdx.x * T0 + t; c < a.N; c += kCluster * T0) {
+      float v[kCluster], sum = 0.f;
+#pragma unroll
+      for (uint32_t r = 0; r < kCluster; r++) v[r] = load_cluster(ring0 + 4 * c, r);
+#pragma unroll
+      for (uint32_t r = 0; r < kCluster; r++) sum += v[r];
+      store_weight(a.dweight, a.weight_bf16, c, sum);
+    }
+    sync_cluster();      // no CTA leaves while another reads its sums
+  }
 }
 
 // dx of long rows, one row a CTA at a time, read twice.
@@ -674,10 +719,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_join_kernel(const float* __r
   s = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; i++) s += red[i][lane];
-  if (bf16)
-    static_cast<uint16_t*>(dweight)[c] = uint16_t(cvt_bf16x2(s, 0.f));
-  else
-    static_cast<float*>(dweight)[c] = s;
+  store_weight(dweight, bf16, c, s);
 }
 
 constexpr uint32_t kLongRow = 16384;     // elements
@@ -692,6 +734,26 @@ uint32_t grad_ctas(int64_t M, int64_t row_bytes) {
   return uint32_t(std::min<int64_t>(M, int64_t(kSms) * per));
 }
 
+// Few rows: one cluster, no workspace and no second kernel. From the host 12.9 us
+// for 17.0; on the device 61 x 1056 fp32 4.4 for 4.5, 32 x 7168 bf16 6.2 for 5.7,
+// and 64 x 7168, which the rule leaves to the two kernels, 8.1 for 5.8. (Eight
+// CTAs: 6.6, 7.6, 11.4.)
+bool grad_cluster(int64_t M, int64_t N) { return M <= 64 && N <= kLongRow && M * N <= 262144; }
+
+// Allows Kernel clusters of more than eight CTAs on the current device, as
+// ensure_smem_limit.
+template <auto Kernel>
+cudaError_t ensure_large_cluster() {
+  static std::atomic<unsigned char> done[256];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 256 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && dev >= 0 && dev < 256) done[dev].store(1, std::memory_order_release);
+  return e;
+}
+
 template <typename T, bool GH, int C, int ROWS, int DEPTH>
 mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaStream_t s) {
   const uint32_t smem = ROWS * DEPTH * threads * C * 16 * (GH && sizeof(T) == 2 ? 3 : 2);
@@ -699,6 +761,27 @@ mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaS
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return MXQ_ERR_CUDA;
+  }
+  if (a.dweight) {
+    const cudaError_t allowed = ensure_large_cluster<rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>>();
+    if (allowed != cudaSuccess) {
+      record_cuda_error(allowed);
+      return MXQ_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return launched(cudaLaunchKernelEx(&cfg, rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>, a));
   }
   return launched(launch_pdl_ex(rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>, grid, threads, smem, s, a));
 }
@@ -802,7 +885,7 @@ mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld
 }
 
 size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
-  if (M <= 0 || N <= 0) return 0;
+  if (M <= 0 || N <= 0 || mxq::grad_cluster(M, N)) return 0;
   return size_t(mxq::grad_ctas(M, 2 * N)) * size_t(N) * sizeof(float);   // (fp32 rows take no more)
 }
 
@@ -834,7 +917,8 @@ mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, 
       (grad_hidden && (uint64_t(ld_gh) * es) % 16 != 0) || (reinterpret_cast<uintptr_t>(rstd) & 3u) ||
       (reinterpret_cast<uintptr_t>(dweight) & (weight_dt == MXQ_BF16 ? 1u : 3u)) || (dweight && !aligned16(workspace)))
     return MXQ_ERR_ALIGN;
-  if (dweight && (!workspace || workspace_bytes < mxq_rmsnorm_backward_workspace_bytes(M, N)))
+  const bool cluster = dweight && grad_cluster(M, N);
+  if (dweight && !cluster && (!workspace || workspace_bytes < mxq_rmsnorm_backward_workspace_bytes(M, N)))
     return MXQ_ERR_WORKSPACE;
   GradArgs a{};
   a.g = grad;
@@ -843,7 +927,8 @@ mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, 
   a.weight = weight;
   a.rstd = rstd;
   a.dx = dx;
-  a.part = dweight ? static_cast<float*>(workspace) : nullptr;
+  a.part = dweight && !cluster ? static_cast<float*>(workspace) : nullptr;
+  a.dweight = cluster ? dweight : nullptr;
   a.ld_g = ld_g;
   a.ld_h = ld_h;
   a.ld_gh = ld_gh;
@@ -856,7 +941,7 @@ mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, 
     st = grad_hidden ? grad_dispatch<uint16_t, true>(a, parts, s) : grad_dispatch<uint16_t, false>(a, parts, s);
   else
     st = grad_hidden ? grad_dispatch<float, true>(a, parts, s) : grad_dispatch<float, false>(a, parts, s);
-  if (st != MXQ_OK || !dweight) return st;
+  if (st != MXQ_OK || !a.part) return st;
   return launched(launch_pdl_ex(rmsnorm_join_kernel, (a.N + 31) / 32, kThreads, 0, s,
                                 static_cast<const float*>(workspace), parts, a.N, dweight, a.weight_bf16));
 }

@@ -99,9 +99,9 @@ def test_norm():
 
 def test_norm_backward():
     f = mxq.lib.mxq_rmsnorm_backward
-    n = mxq.lib.mxq_rmsnorm_backward_workspace_bytes(4, 64)
-    assert n == 4 * 64 * 4
-    base = dict(g=A, dt=0, M=4, N=64, ldg=64, h=A, ldh=64, w=A, wdt=1, rstd=A, gh=A, ldgh=64, dx=A, dw=A, ws=A, wsb=n, stream=None)
+    n = mxq.lib.mxq_rmsnorm_backward_workspace_bytes(400, 64)
+    assert n == 400 * 64 * 4
+    base = dict(g=A, dt=0, M=400, N=64, ldg=64, h=A, ldh=64, w=A, wdt=1, rstd=A, gh=A, ldgh=64, dx=A, dw=A, ws=A, wsb=n, stream=None)
     assert f(*edit(base)) == CUDA
     assert f(*edit(base, dt=2)) == DTYPE
     assert f(*edit(base, wdt=2)) == DTYPE
@@ -117,6 +117,9 @@ def test_norm_backward():
     assert f(*edit(base, wsb=n - 1)) == WORKSPACE
     assert f(*edit(base, dw=None, ws=None, wsb=0, gh=None, ldgh=0)) == CUDA
     assert f(*edit(base, M=0, dw=None)) == OK
+    assert mxq.lib.mxq_rmsnorm_backward_workspace_bytes(64, 64) == 0 < mxq.lib.mxq_rmsnorm_backward_workspace_bytes(65, 64)
+    assert mxq.lib.mxq_rmsnorm_backward_workspace_bytes(17, 16384) == 17 * 16384 * 4
+    assert f(*edit(base, M=64, ws=None, wsb=0)) == CUDA
 
 
 def test_sizes():

@@ -115,6 +115,33 @@ def test_gradient(M, N, dtype):
         assert same_bits(dx, again[0]) and same_bits(dw, again[1])
 
 
+# few rows are summed over by a cluster: both sides of its limits (64 rows, 2^18 elements, rows of 16384)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("M,N", [(2, 8), (16, 16384), (17, 16384), (15, 16392), (33, 1000), (64, 4096), (65, 4096), (64, 4104)])
+def test_gradient_of_few_rows(M, N, dtype):
+    g, h, gh, w = rows(M, M, N, dtype, 0.1).cuda(), rows(N, M, N, dtype).cuda(), rows(M + N, M, N, dtype, 0.1).cuda(), weights(7, N, dtype).cuda()
+    rstd = torch.rsqrt(h.double().square().mean(1) + 1e-6).float()
+    dx, dw = mxq.rmsnorm_backward(g, h, w, rstd, grad_hidden=gh)
+    want, bound, want_w, bound_w = R.norm_gradient(*(t.cpu().double() for t in (g, h, w, rstd, gh)))
+    R.check(dx.cpu(), want, bound, f"dx {M}x{N}")
+    R.check(dw.cpu(), want_w, bound_w, f"dweight {M}x{N}")
+    # captured, and dx in place of grad
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    n = mxq.lib.mxq_rmsnorm_backward_workspace_bytes(M, N)
+    work, out, out_w = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda"), g.clone(), torch.empty_like(dw)
+    with torch.cuda.graph(graph, stream=side):
+        a = mxq.rmsnorm_backward(g, h, w, rstd, grad_hidden=gh)
+        st = mxq.lib.mxq_rmsnorm_backward(out.data_ptr(), 0 if dtype == BF16 else 1, M, N, N, h.data_ptr(), N, w.data_ptr(),
+                                          0 if dtype == BF16 else 1, rstd.data_ptr(), gh.data_ptr(), N, out.data_ptr(), out_w.data_ptr(),
+                                          work.data_ptr() if n else None, n, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y in ((a[0], dx), (a[1], dw), (out, dx), (out_w, dw)):
+        assert same_bits(x, y)
+
+
 def test_gradient_against_differences():
     """Central differences of sum(g y) in float64: off by the third derivative's h^2 term, below 1e-7 here."""
     M, N, step = 3, 64, 1e-4
