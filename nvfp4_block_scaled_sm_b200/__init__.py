@@ -866,10 +866,15 @@ def _tile_bytes(M: int, S: int) -> int:
     return (M + 127) // 128 * ((S + 3) // 4) * 512
 
 
-def _bytes(t: torch.Tensor, what: str) -> torch.Tensor:
-    if t.dtype is not torch.uint8 or not t.is_contiguous():
-        raise TypeError(f"{what} must be contiguous uint8 tensors")
-    return t
+def _byte_tensors(*ts: torch.Tensor) -> int:
+    """The index of the CUDA device that all of the contiguous uint8 tensors live on."""
+    index = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != index or index < 0:
+            return _same_device(*ts)                             # (raises)
+        if t.dtype is not torch.uint8 or not t.is_contiguous():
+            raise TypeError("codes and scales must be contiguous uint8 tensors")
+    return index
 
 
 def _error_flag(error_flag, index: int):
@@ -903,9 +908,7 @@ def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Te
 
     Returns [M, N] (or [M, N/2]) as ``dtype``. Rows that belong to no expert are
     not written: what they hold is undefined. Records no gradient."""
-    index = _same_device(qa, sa_swizzled, qb, sb_swizzled)
-    for t in (qa, sa_swizzled, qb, sb_swizzled):
-        _bytes(t, "codes and scales")
+    index = _byte_tensors(qa, sa_swizzled, qb, sb_swizzled)
     if qa.dim() != 2 or qb.dim() != 3 or qa.shape[1] != qb.shape[2]:
         raise ValueError("expected qa [M, K] and qb [E, N, K]")
     (M, K), (E, N) = qa.shape, qb.shape[:2]
@@ -917,7 +920,7 @@ def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Te
     if sb_swizzled.numel() < E * _tile_bytes(N, K // 32):
         raise ValueError("swizzled scales are smaller than the operands need")
     offsets = _device_offsets(qa, row_offsets, E, M)
-    if not isinstance(row_offsets, torch.Tensor) or not row_offsets.is_cuda:
+    if offsets is not row_offsets and not (isinstance(row_offsets, torch.Tensor) and row_offsets.is_cuda):
         host = [int(v) for v in row_offsets]
         if host and host[0] != 0:
             raise ValueError("row_offsets must start at 0")
@@ -992,9 +995,7 @@ def mxfp8_gemm_grouped_wgrad(qa_t: torch.Tensor, sa_swizzled: torch.Tensor, qb_t
     weights [E, Na, Nb].
 
     Returns [E, Na, Nb] as ``dtype``; experts without rows get zeros."""
-    index = _same_device(qa_t, sa_swizzled, qb_t, sb_swizzled)
-    for t in (qa_t, sa_swizzled, qb_t, sb_swizzled):
-        _bytes(t, "codes and scales")
+    index = _byte_tensors(qa_t, sa_swizzled, qb_t, sb_swizzled)
     if qa_t.dim() != 2 or qb_t.dim() != 2 or qa_t.shape[1] != qb_t.shape[1]:
         raise ValueError("expected qa_t [Na, P] and qb_t [Nb, P]")
     (Na, P), Nb = qa_t.shape, qb_t.shape[0]
