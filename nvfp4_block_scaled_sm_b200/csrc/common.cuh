@@ -503,6 +503,28 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return r;
 }
 
+// ------------------------------------------------------- packed fp32
+
+// (a0 b0, a1 b1) and (a0 b0 + c0, a1 b1 + c1), each rounded once, in one instruction.
+__device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
+  float2 r;
+  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2v(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
 // ------------------------------------------------------- experts' rows
 
 // Row offsets of a stacked tensor's experts in shared memory: off[e] = the

@@ -146,24 +146,6 @@ struct Weights16 {
   }
 };
 
-// (a0 b0, a1 b1) and (a0 b0 + c0, a1 b1 + c1), each rounded once, in one instruction.
-__device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
-  float2 r;
-  asm("{ .reg .b64 a, b, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b; mov.b64 {%0, %1}, d; }"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2v(float2 a, float2 b, float2 c) {
-  float2 r;
-  asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return r;
-}
-
 // y of 16 elements of a row, their codes, the group's scale (two lanes a
 // group, both or neither of them active; the lanes of a warp call together) and, where asked for, y itself.
 template <typename T, bool WB>
@@ -427,8 +409,6 @@ __device__ __forceinline__ void store_weight(void* dweight, int bf16, uint32_t c
 }
 
 constexpr uint32_t kCluster = 16;        // CTAs (more than the portable eight)
-
-__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
 
 // The weights of P pairs of columns from c on (a multiple of 2 P).
 template <int P>
