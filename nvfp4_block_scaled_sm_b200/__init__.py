@@ -866,6 +866,19 @@ def _tile_bytes(M: int, S: int) -> int:
     return (M + 127) // 128 * ((S + 3) // 4) * 512
 
 
+def _expert_offsets(x: torch.Tensor, row_offsets, E: int, R: int):
+    """:func:`_device_offsets` of experts whose rows start at 0 (the kernels take
+    the first offset as that), and the offsets as a list where the host has them."""
+    if isinstance(row_offsets, torch.Tensor):
+        if row_offsets.is_cuda:
+            return _device_offsets(x, row_offsets, E, R), None
+        row_offsets = row_offsets.tolist()
+    host = [int(v) for v in row_offsets]
+    if host and host[0] != 0:
+        raise ValueError("row_offsets must start at 0")
+    return _device_offsets(x, host, E, R), host
+
+
 def _byte_tensors(*ts: torch.Tensor) -> int:
     """The index of the CUDA device that all of the contiguous uint8 tensors live on."""
     index = ts[0].get_device()
@@ -919,14 +932,10 @@ def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Te
         raise ValueError("halves of an expert need whole scale tiles: N a multiple of 256")
     if sb_swizzled.numel() < E * _tile_bytes(N, K // 32):
         raise ValueError("swizzled scales are smaller than the operands need")
-    offsets = _device_offsets(qa, row_offsets, E, M)
-    if offsets is not row_offsets and not (isinstance(row_offsets, torch.Tensor) and row_offsets.is_cuda):
-        host = [int(v) for v in row_offsets]
-        if host and host[0] != 0:
-            raise ValueError("row_offsets must start at 0")
+    offsets, host = _expert_offsets(qa, row_offsets, E, M)
+    need = _tile_bytes(M, K // 32)              # whatever the experts' padding adds
+    if host is not None:
         need = sum(_tile_bytes(b - a, K // 32) for a, b in zip(host[:-1], host[1:]))
-    else:
-        need = _tile_bytes(M, K // 32)          # whatever the experts' padding adds
     if sa_swizzled.numel() < need:
         raise ValueError("swizzled scales are smaller than the operands need")
     flag = _error_flag(error_flag, index)
@@ -974,7 +983,7 @@ def mxfp8_quantize_columnwise_grouped(xs: torch.Tensor, *, row_offsets=None):
         raise ValueError(f"row_offsets must have 2 to {_MOST_EXPERTS + 1} entries")
     if N % 16:
         raise ValueError("N must be a multiple of 16")
-    offsets = _device_offsets(xs, row_offsets, E, M)
+    offsets, _ = _expert_offsets(xs, row_offsets, E, M)
     P = (M + 127 * E) // 128 * 128                     # mxq_grouped_padded_rows
     q = _empty_like(xs, (N, P), torch.uint8)
     s = _empty_like(xs, (_tile_bytes(N, P // 32),), torch.uint8)
@@ -1007,7 +1016,7 @@ def mxfp8_gemm_grouped_wgrad(qa_t: torch.Tensor, sa_swizzled: torch.Tensor, qb_t
     if sa_swizzled.numel() < _tile_bytes(Na, P // 32) or \
             sb_swizzled.numel() < _tile_bytes(Nb, P // 32):
         raise ValueError("swizzled scales are smaller than the operands need")
-    offsets = _device_offsets(qa_t, row_offsets, E, P)
+    offsets, _ = _expert_offsets(qa_t, row_offsets, E, P)
     flag = _error_flag(error_flag, index)
     d = _empty_like(qa_t, (E, Na, Nb), dtype)
     _launch("mxfp8_gemm_grouped_wgrad", index, qa_t.data_ptr(), sa_swizzled.data_ptr(), qb_t.data_ptr(),

@@ -1,0 +1,57 @@
+"""Offsets that the host holds, as the Python functions of the experts' MXFP8
+operators check them. Runs only without a GPU: the tensors live on the CPU and
+the launches are recorded instead of made."""
+import pytest
+import torch
+
+import nvfp4_block_scaled_sm_b200 as mxq
+
+if torch.cuda.is_available():
+    pytest.skip("host-validation tests with CPU tensors run without a GPU only", allow_module_level=True)
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    made = []
+    monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
+    monkeypatch.setattr(mxq, "_byte_tensors", lambda *ts: 0)
+    monkeypatch.setattr(mxq, "_launch", lambda fn, index, *args: made.append(fn))
+    return made
+
+
+def u8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
+def product(offsets):
+    return mxq.mxfp8_gemm_grouped(u8(200, 64), u8(4096), u8(2, 32, 64), u8(1024), offsets)
+
+
+def transposes(offsets):
+    return mxq.mxfp8_quantize_columnwise_grouped(torch.zeros(200, 32), row_offsets=offsets)
+
+
+def gradients(offsets):
+    P = (200 + 127 * 2) // 128 * 128
+    return mxq.mxfp8_gemm_grouped_wgrad(u8(16, P), u8(2048), u8(16, P), u8(2048), offsets)
+
+
+@pytest.mark.parametrize("call", [product, transposes, gradients])
+@pytest.mark.parametrize("kind", [list, tuple, torch.tensor])
+def test_offsets_start_at_zero(call, kind, launches):
+    """The kernels take the first offset as 0: [50, 100, 200] would count rows 0 to 49 as expert 0's."""
+    for good in ([0, 0, 0], [0, 100, 200], [0, 50, 120]):
+        call(kind(good))
+    assert len(launches) == 3
+    for bad in ([50, 100, 200], [1, 1, 1], [200, 200, 200], [-1, 0, 200]):
+        with pytest.raises(ValueError, match="row_offsets must"):
+            call(kind(bad))
+    assert len(launches) == 3
+
+
+@pytest.mark.parametrize("call", [product, transposes, gradients])
+def test_offsets_rise_within_the_rows(call, launches):
+    for bad in ([0, 100, 500], [0, 100, 99], [0, -1, 200]):
+        with pytest.raises(ValueError, match="row_offsets must"):
+            call(bad)
+    assert not launches
