@@ -1016,7 +1016,9 @@ def mxfp8_gemm_grouped_wgrad(qa_t: torch.Tensor, sa_swizzled: torch.Tensor, qb_t
     if sa_swizzled.numel() < _tile_bytes(Na, P // 32) or \
             sb_swizzled.numel() < _tile_bytes(Nb, P // 32):
         raise ValueError("swizzled scales are smaller than the operands need")
-    offsets, _ = _expert_offsets(qa_t, row_offsets, E, P)
+    offsets, host = _expert_offsets(qa_t, row_offsets, E, P)
+    if host is not None and sum((b - a + 127) // 128 * 128 for a, b in zip(host[:-1], host[1:])) > P:
+        raise ValueError("the experts' rows, padded to multiples of 128, exceed the operands' columns")
     flag = _error_flag(error_flag, index)
     d = _empty_like(qa_t, (E, Na, Nb), dtype)
     _launch("mxfp8_gemm_grouped_wgrad", index, qa_t.data_ptr(), sa_swizzled.data_ptr(), qb_t.data_ptr(),

@@ -55,3 +55,14 @@ def test_offsets_rise_within_the_rows(call, launches):
         with pytest.raises(ValueError, match="row_offsets must"):
             call(bad)
     assert not launches
+
+
+def test_weight_gradients_of_offsets_that_the_columns_do_not_hold(launches):
+    """An expert whose columns lie behind P would silently get zeros, or a part of its sum."""
+    two = lambda P, off: mxq.mxfp8_gemm_grouped_wgrad(u8(16, P), u8(2048), u8(16, P), u8(2048), off)
+    two(256, [0, 1, 2]), two(384, [0, 129, 200]), two(128, [0, 0, 128]), two(0, [0, 0, 0])
+    assert len(launches) == 4
+    for P, off in ((128, [0, 1, 2]), (256, [0, 129, 200]), (256, torch.tensor([0, 1, 130]))):
+        with pytest.raises(ValueError, match="columns"):
+            two(P, off)
+    assert len(launches) == 4
