@@ -446,8 +446,8 @@ mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld
  *  workspace  with dweight: mxq_rmsnorm_backward_workspace_bytes(M, N) bytes
  *          (0 and NULL for few rows, M <= 64 and M N <= 2^18), 16-byte aligned,
  *          no initialization needed; not shared by calls that may overlap.
- * N % 8 == 0. Two launches; one without dweight, and one of a cluster of 16 CTAs
- * for few rows. */
+ * N % 8 == 0. Two launches; one without dweight, and one of a cluster of CTAs
+ * for few rows (16, or as many as the device can hold as one). */
 size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, int64_t ld_g,
                                 const void* hidden, int64_t ld_h, const void* weight, int weight_dt,

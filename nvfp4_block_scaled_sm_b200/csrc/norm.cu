@@ -408,7 +408,7 @@ __device__ __forceinline__ void store_weight(void* dweight, int bf16, uint32_t c
     static_cast<float*>(dweight)[c] = s;
 }
 
-constexpr uint32_t kCluster = 16;        // CTAs (more than the portable eight)
+constexpr uint32_t kCluster = 16;        // most CTAs of a cluster (more than the portable eight)
 
 // The weights of P pairs of columns from c on (a multiple of 2 P).
 template <int P>
@@ -598,10 +598,10 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_kernel(const __grid_const
 #pragma unroll
         for (int k = 0; k < kPairs; k++) *reinterpret_cast<float2*>(ring + 4 * column(i) + 8 * k) = dw[i][k];
     sync_cluster();
-    for (uint32_t c = blockIdx.x * T0 + t; c < a.N; c += kCluster * T0) {
+    for (uint32_t c = blockIdx.x * T0 + t; c < a.N; c += gridDim.x * T0) {
       float v[kCluster], sum = 0.f;
 #pragma unroll
-      for (uint32_t r = 0; r < kCluster; r++) v[r] = load_cluster(ring0 + 4 * c, r);
+      for (uint32_t r = 0; r < kCluster; r++) v[r] = r < gridDim.x ? load_cluster(ring0 + 4 * c, r) : 0.f;
 #pragma unroll
       for (uint32_t r = 0; r < kCluster; r++) sum += v[r];
       store_weight(a.dweight, a.weight_bf16, c, sum);
@@ -717,21 +717,39 @@ uint32_t grad_ctas(int64_t M, int64_t row_bytes) {
 // Few rows: one cluster, no workspace and no second kernel. From the host 12.9 us
 // for 17.0; on the device 61 x 1056 fp32 4.4 for 4.5, 32 x 7168 bf16 6.2 for 5.7,
 // and 64 x 7168, which the rule leaves to the two kernels, 8.1 for 5.8. (Eight
-// CTAs: 6.6, 7.6, 11.4.)
+// CTAs: 6.6, 7.6, 11.4; as many as there are pairs of rows, one 1 x 16384 16.0 for
+// 7.5, two 4 x 7168 7.5 for 5.8.)
 bool grad_cluster(int64_t M, int64_t N) { return M <= 64 && N <= kLongRow && M * N <= 262144; }
 
-// Allows Kernel clusters of more than eight CTAs on the current device, as
-// ensure_smem_limit.
+// The largest cluster of CTAs of Kernel, 16, 8, 4, 2 or 1, that the current device
+// can hold: clusters of more than eight have to be allowed, and need as many
+// multiprocessors within one's reach. Asked for once per device, for CTAs of the
+// most shared memory.
 template <auto Kernel>
-cudaError_t ensure_large_cluster() {
-  static std::atomic<unsigned char> done[256];
+uint32_t largest_cluster() {
+  static std::atomic<uint32_t> known[256];
   int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 256 && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess && dev >= 0 && dev < 256) done[dev].store(1, std::memory_order_release);
-  return e;
+  const bool slot = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 256;
+  uint32_t n = slot ? known[dev].load(std::memory_order_acquire) : 0;
+  if (n > 0) return n;
+  const bool large = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  for (n = large ? kCluster : 8; n > 1; n /= 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = kRingBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int resident = 0;
+    if (cudaOccupancyMaxActiveClusters(&resident, Kernel, &cfg) == cudaSuccess && resident > 0) break;
+  }
+  (void)cudaGetLastError();
+  if (slot && n > 1) known[dev].store(n, std::memory_order_release);
+  return n;
 }
 
 template <typename T, bool GH, int C, int ROWS, int DEPTH>
@@ -743,13 +761,9 @@ mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaS
     return MXQ_ERR_CUDA;
   }
   if (a.dweight) {
-    const cudaError_t allowed = ensure_large_cluster<rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>>();
-    if (allowed != cudaSuccess) {
-      record_cuda_error(allowed);
-      return MXQ_ERR_CUDA;
-    }
+    const uint32_t ctas = largest_cluster<rmsnorm_grad_kernel<T, GH, C, ROWS, DEPTH>>();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster);
+    cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -757,7 +771,7 @@ mxq_status launch_grad(const GradArgs& a, uint32_t grid, uint32_t threads, cudaS
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.x = ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
