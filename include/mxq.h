@@ -426,7 +426,7 @@ mxq_status mxfp8_gemm_grouped_wgrad(const uint8_t* qa_t, const uint8_t* sa_swz, 
  *               tiles: as for mxfp8_quantize.
  *  normed       NULL, or [M, N] of dt: y rounded to nearest even.
  *  rstd         [M] fp32, for mxq_rmsnorm_backward.
- * N % 32 == 0, eps >= 0. One launch. */
+ * N % 32 == 0, eps >= 0. One launch; nothing is written for M == 0 or N == 0. */
 mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld_x, const void* residual,
                          int64_t ld_res, const void* weight, int weight_dt, double eps, void* hidden,
                          uint8_t* qweight, uint8_t* scale, uint8_t* scale_swz, void* normed, float* rstd,
@@ -444,10 +444,13 @@ mxq_status mxfp8_rmsnorm(const void* x, int dt, int64_t M, int64_t N, int64_t ld
  *          that is compact). With a residual it is the gradient of both summands.
  *  dweight [N] of weight_dt, or NULL (not computed).
  *  workspace  with dweight: mxq_rmsnorm_backward_workspace_bytes(M, N) bytes
- *          (0 and NULL for few rows, M <= 64 and M N <= 2^18), 16-byte aligned,
- *          no initialization needed; not shared by calls that may overlap.
- * N % 8 == 0. Two launches; one without dweight, and one of a cluster of CTAs
- * for few rows (16, or as many as the device can hold as one). */
+ *          (0 and NULL for few rows: M <= 64, N <= 16384 and M N <= 2^18),
+ *          16-byte aligned, no initialization needed; not shared by calls that
+ *          may overlap.
+ * N % 8 == 0. M == 0 writes zeros into dweight. One launch without dweight; with
+ * it two, three for N > 16384, and one of a cluster of CTAs for few rows (16, or
+ * as many as the device can hold as one).
+ */
 size_t mxq_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 mxq_status mxq_rmsnorm_backward(const void* grad, int dt, int64_t M, int64_t N, int64_t ld_g,
                                 const void* hidden, int64_t ld_h, const void* weight, int weight_dt,
