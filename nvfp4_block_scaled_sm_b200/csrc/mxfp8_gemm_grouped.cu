@@ -270,15 +270,18 @@ __device__ __forceinline__ void swiglu2(float2 g, float2 u, uint32_t& y0, uint32
 // memory: its quarters 0 and 1 come from a half of the gate's tile, 2 and 3
 // from a half of the up half's, and a TMA copy cannot put eight of 16 bytes
 // beside eight others; warp 11 joins them. 32768 rows of 64 experts, N = 4096,
-// K = 2048, under load: 325 us (505 with the sends; without SWIGLU 290 to 325); from K =
-// 4096 on the product's own time. At K = 512 silu itself is what bounds it, 6 us
-// a tile: 222 us (without SWIGLU 103).
+// K = 2048: 265 us in short runs, 313 under load (505 with the sends; without
+// SWIGLU 250 and 297); from K = 4096 on within 3 % of the product's own time. At K
+// = 512 silu itself is what bounds it, 4.7 us a tile: 161 us (without SWIGLU 94 in
+// short runs, 113 under load).
 //
 // What bounds it: with few rows a weight, HBM (512 rows 297 us for weights of
-// 1.9 GB; 6.4 TB/s). With many, the power limit: 32768 rows of one expert take
-// 671 us, as the single product does (2.87 PFLOP/s); of 64 experts, with the
-// weights from HBM, 750 to 835 us, and 985 us once the clock has settled at
-// 1.2 GHz under load.
+// 1.9 GB; 6.4 TB/s). With many, the clock that the power limit leaves and the
+// ragged tails: 32768 rows of one expert take 671 us, as the single product does
+// (2.87 PFLOP/s). Spread over 64 experts they are about 159 row tiles instead of
+// 128, and a tail takes as long as a whole tile (its stages are part empty, so
+// that the bytes in flight do not cover the latency of the weight's): 750 to 835
+// us, and 960 to 1000 once the clock has settled at 1.1 to 1.2 GHz under load.
 
 constexpr uint32_t kWeightTile = 128 * kBK;                 // a CTA's rows of the weight
 constexpr uint32_t kSendBytes = 32 * 8 * 4;                 // eight columns of a warp
@@ -500,7 +503,6 @@ mxfp8_rows_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_consta
   } else if (SWIGLU && warp == 3 + kEpiWarps) {
     // ------------------------------------- joined scale tiles of the weight
     // Quarters 0 and 1 of a joined tile are the gate's 64 rows, 2 and 3 the up
-    // half's: a lane's line of it is eight bytes of the gate's tile and eight of
     // half's: a lane's line of it is eight bytes of the gate's tile and eight of
     // the up half's. They go in groups of kJoin K blocks: a release that the
     // other CTA may rely on takes 1000 to 3000 cycles (one per K block: 610 us
