@@ -909,7 +909,8 @@ def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Te
 
     ``qa`` [M, K] and ``sa_swizzled``: the codes of the sorted rows and each
     expert's scales in tiles of its own, as ``mxfp8_quantize_grouped(x,
-    row_offsets=..., swizzled=True)`` returns them for these offsets. ``qb`` [E,
+    row_offsets=..., swizzled=True)`` returns them for these offsets (rows
+    behind the last offset need no scales). ``qb`` [E,
     N, K] and ``sb_swizzled``: a stack of weights,
     ``mxfp8_quantize_grouped(w, swizzled=True)``; with the stack of
     :func:`mxfp8_quantize_columnwise_grouped` the product is the gradient of the
@@ -933,16 +934,19 @@ def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Te
     if sb_swizzled.numel() < E * _tile_bytes(N, K // 32):
         raise ValueError("swizzled scales are smaller than the operands need")
     offsets, host = _expert_offsets(qa, row_offsets, E, M)
-    need = _tile_bytes(M, K // 32)              # whatever the experts' padding adds
+    block = _tile_bytes(1, K // 32)             # the scales of 128 rows
+    need = block if M else 0                    # (what offsets on the device ask for is not known here)
     if host is not None:
-        need = sum(_tile_bytes(b - a, K // 32) for a, b in zip(host[:-1], host[1:]))
+        need = sum((b - a + 127) // 128 * block for a, b in zip(host[:-1], host[1:]))
     if sa_swizzled.numel() < need:
         raise ValueError("swizzled scales are smaller than the operands need")
+    # scales are there for experts' rows: the rows that they cannot hold are no expert's
+    rows = min(M, sa_swizzled.numel() // block * 128) if block else M
     flag = _error_flag(error_flag, index)
     d = _empty_like(qa, (M, N // 2 if swiglu else N), dtype)
     _launch("mxfp8_gemm_grouped", index, qa.data_ptr(), sa_swizzled.data_ptr(),
             sa_swizzled.numel() // 512 * 512, qb.data_ptr(), sb_swizzled.data_ptr(), E,
-            offsets.data_ptr(), M, N, K, 1 if swiglu else 0, d.data_ptr(), _code(dtype), flag)
+            offsets.data_ptr(), rows, N, K, 1 if swiglu else 0, d.data_ptr(), _code(dtype), flag)
     return d
 
 

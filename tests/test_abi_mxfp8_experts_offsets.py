@@ -15,7 +15,7 @@ def launches(monkeypatch):
     made = []
     monkeypatch.setattr(mxq, "_same_device", lambda *ts: 0)
     monkeypatch.setattr(mxq, "_byte_tensors", lambda *ts: 0)
-    monkeypatch.setattr(mxq, "_launch", lambda fn, index, *args: made.append(fn))
+    monkeypatch.setattr(mxq, "_launch", lambda fn, index, *args: made.append((fn, args)))
     return made
 
 
@@ -66,3 +66,21 @@ def test_weight_gradients_of_offsets_that_the_columns_do_not_hold(launches):
         with pytest.raises(ValueError, match="columns"):
             two(P, off)
     assert len(launches) == 4
+
+
+def test_scales_of_the_experts_rows_are_enough(launches):
+    """Rows behind the last offset belong to no expert: scales that hold the experts' tiles are not refused, and the
+    library is given the rows that they can hold (it wants scales for every row)."""
+    K, N, M = 320, 32, 1000
+    w, sw = u8(2, N, K), u8(2 * mxq._tile_bytes(N, K // 32))
+    tile = mxq._tile_bytes(128, K // 32)
+    for tiles, offsets, rows in ((8, [0, 500, 1000], 1000), (8, [0, 0, 800], 1000), (7, [0, 0, 800], 896), (7, [0, 128, 896], 896),
+                                 (2, [0, 1, 2], 256), (1, [0, 0, 100], 128), (0, [0, 0, 0], 0), (9, [0, 500, 1000], 1000)):
+        y = mxq.mxfp8_gemm_grouped(u8(M, K), u8(tiles * tile), w, sw, offsets)
+        fn, args = launches.pop()
+        assert fn == "mxfp8_gemm_grouped" and args[2] == tiles * tile and args[7] == rows and y.shape == (M, N)
+        assert args[2] >= mxq._tile_bytes(rows, K // 32)
+    for tiles, offsets in ((7, [0, 500, 1000]), (6, [0, 0, 800]), (1, [0, 1, 2]), (0, [0, 0, 1])):
+        with pytest.raises(ValueError, match="scales"):
+            mxq.mxfp8_gemm_grouped(u8(M, K), u8(tiles * tile), w, sw, offsets)
+    assert not launches
