@@ -909,8 +909,9 @@ def mxfp8_gemm_grouped(qa: torch.Tensor, sa_swizzled: torch.Tensor, qb: torch.Te
 
     ``qa`` [M, K] and ``sa_swizzled``: the codes of the sorted rows and each
     expert's scales in tiles of its own, as ``mxfp8_quantize_grouped(x,
-    row_offsets=..., swizzled=True)`` returns them for these offsets (rows
-    behind the last offset need no scales). ``qb`` [E,
+    row_offsets=..., swizzled=True)`` returns them for these offsets. Rows
+    behind the last offset need no scales; with offsets on the device, rows
+    that the scales cannot hold count as such. ``qb`` [E,
     N, K] and ``sb_swizzled``: a stack of weights,
     ``mxfp8_quantize_grouped(w, swizzled=True)``; with the stack of
     :func:`mxfp8_quantize_columnwise_grouped` the product is the gradient of the
